@@ -402,6 +402,93 @@ SSD_API ssd_status_t ssd_chunk_scan_fwd_with_flow(const void* x, const float* dt
                                                   void* workspace, size_t workspace_bytes,
                                                   void* stream, int flow);
 
+/*
+ * Operators around the layer
+ * --------------------------
+ * What a model runs beside the SSD layer: the short causal convolution that
+ * feeds it, the selective scan with a decay of its own for every (channel,
+ * state) ("论文解读：Mamba: ...", 选择性状态空间模型: dt, B and C vary per token
+ * and A is a full (channels, states) matrix; ssd_chunk_scan_fwd covers the
+ * scalar-A case, which becomes matrix products), and the norm and rotation of
+ * B and C.  The conventions at the top of this file hold, with these
+ * additions:
+ *  - An input that has an ssd_stride_t may be a view of a wider tensor (a slice
+ *    of a projection's output): its last dimension (channels, or groups and
+ *    states) is contiguous, its batch and token strides are given in elements,
+ *    and its pointer only has to be aligned to its element.  Everything else is
+ *    dense and 16-byte aligned.
+ *  - Parameters (convolution weights and bias, A, D, dt_bias, norm weights,
+ *    frequencies) and their gradients are fp32.  Gradients of activations are in
+ *    dtype: computed in fp32, rounded once.  No result depends on the order of
+ *    atomics: sums over tokens or channels go through the workspace, so two runs
+ *    give the same bits.
+ *  - seq_lens (batch) int32 in device memory, or NULL for sequences that all have
+ *    seqlen tokens: a padded batch.  Row t of sequence i belongs to it while
+ *    t < seq_lens[i] (values are clamped to [0, seqlen]).  Rows behind it are
+ *    never read; in outputs of the inputs' shape they are written as zero, and
+ *    final states are the states after the sequence's own last token (the
+ *    entering state for a sequence of length 0).
+ *  - Unless said otherwise, inputs and outputs must not overlap.
+ */
+typedef struct {
+    int64_t batch;   /* elements from one sequence to the next */
+    int64_t token;   /* elements from one token to the next (ignored by the step calls) */
+} ssd_stride_t;
+
+typedef struct {
+    int64_t batch;     /* b >= 0 */
+    int64_t seqlen;    /* L >= 0 */
+    int64_t channels;  /* D >= 1 */
+    int64_t width;     /* W, 2..4: taps */
+} ssd_conv_dims_t;
+
+/*
+ * Short causal depthwise convolution:
+ *     p_t[d] = bias[d] + sum_k weight[d][k] * x_{t-W+1+k}[d],   k = 0..W-1
+ *     y_t = silu(p_t) if silu is non-zero, else p_t
+ * x (b,L,D) dtype (strided); weight (D,W) fp32, the last tap on the token
+ * itself; bias (D) fp32 or NULL (zero).  init_state (b,W-1,D) dtype, or NULL
+ * (zero): the W-1 inputs before token 0, oldest first.  final_state (b,W-1,D)
+ * dtype, or NULL when not wanted: the last W-1 inputs, in the same order, as
+ * ssd_causal_conv_step takes them.  y (b,L,D) dtype.
+ */
+SSD_API ssd_status_t ssd_causal_conv_fwd(const void* x, const ssd_stride_t* x_stride,
+                                         const float* weight, const float* bias,
+                                         const void* init_state, const int32_t* seq_lens,
+                                         int silu, void* y, void* final_state,
+                                         const ssd_conv_dims_t* dims, ssd_dtype_t dtype,
+                                         void* stream);
+
+/*
+ * Gradients of ssd_causal_conv_fwd.  dy (b,L,D) dense, in dtype or (dy_f32
+ * non-zero) fp32, as ssd_chunk_scan_bwd writes its gradients; dfinal_state
+ * (b,W-1,D) dtype = dL/dfinal_state or NULL (zero).  Outputs, all fully
+ * written: dx (b,L,D) dtype, dweight (D,W) fp32, dbias (D) fp32, dinit_state
+ * (b,W-1,D) dtype (NULL = not wanted).  workspace: partial sums of dweight and
+ * dbias; NULL only when the reported size is 0.
+ */
+SSD_API ssd_status_t ssd_causal_conv_bwd_workspace_size(const ssd_conv_dims_t* dims,
+                                                        ssd_dtype_t dtype, size_t* bytes);
+SSD_API ssd_status_t ssd_causal_conv_bwd(const void* x, const ssd_stride_t* x_stride,
+                                         const float* weight, const float* bias,
+                                         const void* init_state, const int32_t* seq_lens,
+                                         int silu, const void* dy, int dy_f32,
+                                         const void* dfinal_state, void* dx, float* dweight,
+                                         float* dbias, void* dinit_state,
+                                         const ssd_conv_dims_t* dims, ssd_dtype_t dtype,
+                                         void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * One token of ssd_causal_conv_fwd for a batch of sequences.  state (b,W-1,D)
+ * dtype, updated in place: the oldest input leaves, x enters.  x (b,D) dtype
+ * (strided), y (b,D) dtype.  dims->seqlen is ignored.
+ */
+SSD_API ssd_status_t ssd_causal_conv_step(void* state, const void* x,
+                                          const ssd_stride_t* x_stride, const float* weight,
+                                          const float* bias, int silu, void* y,
+                                          const ssd_conv_dims_t* dims, ssd_dtype_t dtype,
+                                          void* stream);
+
 #ifdef __cplusplus
 }
 #endif

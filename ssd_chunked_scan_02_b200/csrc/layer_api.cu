@@ -1,0 +1,176 @@
+// layer_api.cu -- C-ABI entry points of the operators around the SSD layer
+// (include/ssd.h, "Operators around the layer"): host-side validation, then
+// launches.  Nothing here allocates device memory or synchronises the device.
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "api_checks.h"
+#include "layer_ops.h"
+
+namespace {
+
+using ssd::cuda_fail;
+using ssd::fail;
+
+constexpr int64_t kMaxSize = 0x7fffffffLL;
+
+ssd_status_t check_dtype(ssd_dtype_t dtype, ssd::Elt* t) {
+    if (dtype != SSD_F32 && dtype != SSD_BF16)
+        return fail(SSD_ERR_INVALID_ARG, "unknown dtype %d", (int)dtype);
+    *t = dtype == SSD_F32 ? ssd::Elt::F32 : ssd::Elt::BF16;
+    return SSD_OK;
+}
+
+// batch, seqlen >= 0 and every size below 2^31, so that their products fit 64 bits.
+ssd_status_t check_tokens(int64_t batch, int64_t seqlen) {
+    if (batch < 0 || seqlen < 0)
+        return fail(SSD_ERR_INVALID_ARG, "batch (%lld) and seqlen (%lld) must be >= 0",
+                    (long long)batch, (long long)seqlen);
+    if (batch > kMaxSize || seqlen > kMaxSize)
+        return fail(SSD_ERR_UNSUPPORTED, "batch and seqlen must be below 2^31");
+    return SSD_OK;
+}
+
+ssd_status_t conv_dims(const ssd_conv_dims_t* dims, ssd_dtype_t dtype, ssd::ConvDims* d,
+                       ssd::Elt* t) {
+    if (!dims) return fail(SSD_ERR_INVALID_ARG, "dims is NULL");
+    ssd_status_t st = check_tokens(dims->batch, dims->seqlen);
+    if (st != SSD_OK) return st;
+    if (dims->channels < 1) return fail(SSD_ERR_INVALID_ARG, "channels must be >= 1");
+    if (dims->width < 2 || dims->width > 4)
+        return fail(SSD_ERR_UNSUPPORTED, "width must be in 2..4, got %lld",
+                    (long long)dims->width);
+    if (dims->channels > kMaxSize / 8)
+        return fail(SSD_ERR_UNSUPPORTED, "channels must be below 2^28");
+    // the finest split: one thread a channel and 8 tokens, 256 threads a block
+    if ((double)dims->batch * ((double)dims->seqlen / 8 + 1) * ((double)dims->channels / 32 + 1) >
+        (double)kMaxSize)
+        return fail(SSD_ERR_UNSUPPORTED, "batch * seqlen * channels exceeds the launch grid");
+    *d = ssd::ConvDims{dims->batch, dims->seqlen, dims->channels, (int)dims->width};
+    return check_dtype(dtype, t);
+}
+
+#define REQUIRE_STRIDE(p)                                                                \
+    do {                                                                                 \
+        if (!(p)) return fail(SSD_ERR_INVALID_ARG, "%s is NULL", #p);                    \
+    } while (0)
+
+// A view: any pointer aligned to its element.
+ssd_status_t check_view(const void* p, const char* name, ssd::Elt t) {
+    if (!p) return fail(SSD_ERR_INVALID_ARG, "%s is NULL", name);
+    if (!ssd::aligned_to(p, t == ssd::Elt::F32 ? 4 : 2))
+        return fail(SSD_ERR_INVALID_ARG, "%s is not aligned to its element", name);
+    return SSD_OK;
+}
+
+#define REQUIRE_VIEW(p)                                                                  \
+    do {                                                                                 \
+        ssd_status_t st_view_ = check_view((p), #p, t);                                  \
+        if (st_view_ != SSD_OK) return st_view_;                                         \
+    } while (0)
+
+#define REQUIRE_LENS(p)                                                                  \
+    do {                                                                                 \
+        if ((p) && !ssd::aligned_to((p), 4))                                             \
+            return fail(SSD_ERR_INVALID_ARG, "%s is not aligned to its element", #p);    \
+    } while (0)
+
+ssd::Stride stride_of(const ssd_stride_t& s) { return ssd::Stride{s.batch, s.token}; }
+
+}  // namespace
+
+extern "C" {
+
+// ---------------------------------------------------------------- causal convolution
+ssd_status_t ssd_causal_conv_fwd(const void* x, const ssd_stride_t* x_stride,
+                                 const float* weight, const float* bias, const void* init_state,
+                                 const int32_t* seq_lens, int silu, void* y, void* final_state,
+                                 const ssd_conv_dims_t* dims, ssd_dtype_t dtype, void* stream) {
+    ssd::clear_error_detail();
+    ssd::ConvDims d{}; ssd::Elt t = ssd::Elt::BF16;
+    ssd_status_t st = conv_dims(dims, dtype, &d, &t);
+    if (st != SSD_OK) return st;
+    OPTIONAL_PTR(bias); OPTIONAL_PTR(init_state); OPTIONAL_PTR(final_state);
+    REQUIRE_LENS(seq_lens);
+    REQUIRE_STRIDE(x_stride);
+    if (d.b == 0 || (d.L == 0 && !final_state)) return SSD_OK;
+    REQUIRE_PTR(weight);
+    if (d.L > 0) {
+        REQUIRE_VIEW(x);
+        REQUIRE_PTR(y);
+    }
+    REQUIRE_DEVICE(weight);
+    cudaError_t e = ssd::launch_conv_fwd(x, stride_of(*x_stride), weight, bias, init_state,
+                                         seq_lens, silu != 0, y, final_state, d, t,
+                                         static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? SSD_OK : cuda_fail(e, "convolution kernel");
+}
+
+ssd_status_t ssd_causal_conv_bwd_workspace_size(const ssd_conv_dims_t* dims, ssd_dtype_t dtype,
+                                                size_t* bytes) {
+    ssd::clear_error_detail();
+    if (!bytes) return fail(SSD_ERR_INVALID_ARG, "bytes is NULL");
+    ssd::ConvDims d{}; ssd::Elt t = ssd::Elt::BF16;
+    ssd_status_t st = conv_dims(dims, dtype, &d, &t);
+    if (st != SSD_OK) return st;
+    *bytes = ssd::conv_bwd_workspace_bytes(d);
+    return SSD_OK;
+}
+
+ssd_status_t ssd_causal_conv_bwd(const void* x, const ssd_stride_t* x_stride,
+                                 const float* weight, const float* bias, const void* init_state,
+                                 const int32_t* seq_lens, int silu, const void* dy, int dy_f32,
+                                 const void* dfinal_state, void* dx, float* dweight,
+                                 float* dbias, void* dinit_state, const ssd_conv_dims_t* dims,
+                                 ssd_dtype_t dtype, void* workspace, size_t workspace_bytes,
+                                 void* stream) {
+    ssd::clear_error_detail();
+    ssd::ConvDims d{}; ssd::Elt t = ssd::Elt::BF16;
+    ssd_status_t st = conv_dims(dims, dtype, &d, &t);
+    if (st != SSD_OK) return st;
+    OPTIONAL_PTR(bias); OPTIONAL_PTR(init_state); OPTIONAL_PTR(dfinal_state);
+    OPTIONAL_PTR(dinit_state);
+    REQUIRE_LENS(seq_lens);
+    REQUIRE_STRIDE(x_stride);
+    REQUIRE_PTR(weight); REQUIRE_PTR(dweight); REQUIRE_PTR(dbias);
+    if (d.b > 0 && d.L > 0) {
+        REQUIRE_VIEW(x);
+        REQUIRE_PTR(dy);
+        REQUIRE_PTR(dx);
+    }
+    const size_t need = ssd::conv_bwd_workspace_bytes(d);
+    if (workspace_bytes < need)
+        return fail(SSD_ERR_INVALID_ARG, "workspace too small: %zu bytes given, %zu needed",
+                    workspace_bytes, need);
+    if (need > 0) REQUIRE_PTR(workspace);
+    REQUIRE_DEVICE(weight);
+    cudaError_t e = ssd::launch_conv_bwd(x, stride_of(*x_stride), weight, bias, init_state,
+                                         seq_lens, silu != 0, dy, dy_f32 != 0, dfinal_state, dx,
+                                         dweight, dbias, dinit_state,
+                                         static_cast<float*>(workspace), d, t,
+                                         static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? SSD_OK : cuda_fail(e, "convolution gradient kernels");
+}
+
+ssd_status_t ssd_causal_conv_step(void* state, const void* x, const ssd_stride_t* x_stride,
+                                  const float* weight, const float* bias, int silu, void* y,
+                                  const ssd_conv_dims_t* dims, ssd_dtype_t dtype, void* stream) {
+    ssd::clear_error_detail();
+    ssd::ConvDims d{}; ssd::Elt t = ssd::Elt::BF16;
+    ssd_conv_dims_t one{};
+    if (dims) one = *dims;
+    one.seqlen = 1;
+    ssd_status_t st = conv_dims(dims ? &one : nullptr, dtype, &d, &t);
+    if (st != SSD_OK) return st;
+    OPTIONAL_PTR(bias);
+    REQUIRE_STRIDE(x_stride);
+    if (d.b == 0) return SSD_OK;
+    REQUIRE_PTR(state); REQUIRE_PTR(weight); REQUIRE_PTR(y);
+    REQUIRE_VIEW(x);
+    REQUIRE_DEVICE(state);
+    cudaError_t e = ssd::launch_conv_step(state, x, x_stride->batch, weight, bias, silu != 0, y,
+                                          d, t, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? SSD_OK : cuda_fail(e, "convolution step kernel");
+}
+
+}  // extern "C"

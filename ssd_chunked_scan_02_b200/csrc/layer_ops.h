@@ -1,0 +1,32 @@
+// layer_ops.h -- launchers of the operators around the SSD layer, shared
+// between their C-ABI entry points (layer_api.cu) and their kernels.
+#pragma once
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "ssd_internal.h"
+
+namespace ssd {
+
+struct Stride {
+    int64_t batch, token;    // elements
+};
+
+// ------------------------------------------------------------------ causal convolution
+struct ConvDims {
+    int64_t b, L, D;
+    int W;                   // 2..4
+};
+cudaError_t launch_conv_fwd(const void* x, Stride xs, const float* w, const float* bias,
+                            const void* init, const int32_t* lens, bool silu, void* y,
+                            void* final_state, const ConvDims& d, Elt t, cudaStream_t s);
+size_t conv_bwd_workspace_bytes(const ConvDims& d);
+cudaError_t launch_conv_bwd(const void* x, Stride xs, const float* w, const float* bias,
+                            const void* init, const int32_t* lens, bool silu, const void* dy,
+                            bool dy_f32, const void* dfinal, void* dx, float* dw, float* dbias,
+                            void* dinit, float* ws, const ConvDims& d, Elt t, cudaStream_t s);
+cudaError_t launch_conv_step(void* state, const void* x, int64_t x_batch, const float* w,
+                             const float* bias, bool silu, void* y, const ConvDims& d, Elt t,
+                             cudaStream_t s);
+
+}  // namespace ssd

@@ -7,6 +7,7 @@
 #include <stdio.h>
 
 #include "../../include/ssd.h"
+#include "api_checks.h"
 #include "seqpar.h"
 #include "ssd_internal.h"
 #include "tc_host.h"
@@ -14,23 +15,12 @@
 
 namespace {
 
+using ssd::aligned16;
+using ssd::cuda_fail;
+using ssd::fail;
+using ssd::round_up;
+
 thread_local char g_detail[512] = "";
-
-ssd_status_t fail(ssd_status_t s, const char* fmt, ...) {
-    va_list ap;
-    va_start(ap, fmt);
-    vsnprintf(g_detail, sizeof(g_detail), fmt, ap);
-    va_end(ap);
-    return s;
-}
-
-ssd_status_t cuda_fail(cudaError_t e, const char* where) {
-    return fail(SSD_ERR_CUDA, "%s: %s (%s)", where, cudaGetErrorName(e), cudaGetErrorString(e));
-}
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-size_t round_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 
 size_t elt_size(ssd::Elt t) { return t == ssd::Elt::F32 ? 4 : 2; }
 
@@ -151,11 +141,31 @@ WsLayout ws_layout(const ssd::Dims& d, ssd::Elt t, Flow flow) {
     return w;
 }
 
-// A tensor handed to the kernels must be device memory of the current device:
-// tensor maps, the status word and scratch are looked up per current device,
-// and a kernel on one GPU given another GPU's (or unregistered host) memory
-// faults or reads the wrong memory.  Checked once per call, after every other
-// validation, on the call's main input.
+}  // namespace
+
+namespace ssd {
+
+void clear_error_detail() { g_detail[0] = 0; }
+
+void set_error_detail(const char* fmt, ...) {
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(g_detail, sizeof(g_detail), fmt, ap);
+    va_end(ap);
+}
+
+ssd_status_t fail(ssd_status_t s, const char* fmt, ...) {
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(g_detail, sizeof(g_detail), fmt, ap);
+    va_end(ap);
+    return s;
+}
+
+ssd_status_t cuda_fail(cudaError_t e, const char* where) {
+    return fail(SSD_ERR_CUDA, "%s: %s (%s)", where, cudaGetErrorName(e), cudaGetErrorString(e));
+}
+
 ssd_status_t check_current_device(const void* p, const char* name) {
     cudaPointerAttributes a{};
     cudaError_t e = cudaPointerGetAttributes(&a, p);
@@ -174,33 +184,6 @@ ssd_status_t check_current_device(const void* p, const char* name) {
     return SSD_OK;
 }
 
-#define REQUIRE_DEVICE(p)                                                                \
-    do {                                                                                 \
-        ssd_status_t st_dev_ = check_current_device((p), #p);                            \
-        if (st_dev_ != SSD_OK) return st_dev_;                                           \
-    } while (0)
-
-#define REQUIRE_PTR(p)                                                                   \
-    do {                                                                                 \
-        if (!(p)) return fail(SSD_ERR_INVALID_ARG, "%s is NULL", #p);                    \
-        if (!aligned16(p)) return fail(SSD_ERR_INVALID_ARG, "%s is not 16-byte aligned", #p); \
-    } while (0)
-#define OPTIONAL_PTR(p)                                                                  \
-    do {                                                                                 \
-        if ((p) && !aligned16(p))                                                        \
-            return fail(SSD_ERR_INVALID_ARG, "%s is not 16-byte aligned", #p);           \
-    } while (0)
-
-}  // namespace
-
-namespace ssd {
-// Records a message for ssd_last_error_detail() on this host thread.
-void set_error_detail(const char* fmt, ...) {
-    va_list ap;
-    va_start(ap, fmt);
-    vsnprintf(g_detail, sizeof(g_detail), fmt, ap);
-    va_end(ap);
-}
 }  // namespace ssd
 
 extern "C" {

@@ -30,7 +30,9 @@ EXPORTED = ("ssd_status_string", "ssd_last_error_detail", "ssd_chunk_scan_fwd_wo
             "ssd_debug_expire_wait", "ssd_chunk_scan_bwd_workspace_size", "ssd_chunk_scan_bwd",
             "ssd_chunk_scan_fwd_data_flow", "ssd_seq_logdecay", "ssd_state_exchange_combine",
             "ssd_state_correction_workspace_size", "ssd_state_correction_fwd",
-            "ssd_chunk_scan_fwd_flow_workspace_size", "ssd_chunk_scan_fwd_with_flow")
+            "ssd_chunk_scan_fwd_flow_workspace_size", "ssd_chunk_scan_fwd_with_flow",
+            "ssd_causal_conv_fwd", "ssd_causal_conv_bwd_workspace_size", "ssd_causal_conv_bwd",
+            "ssd_causal_conv_step")
 
 # ssd_chunk_scan_fwd_data_flow results
 SSD_FLOW_SIMT, SSD_FLOW_TC_THREE_KERNEL, SSD_FLOW_WALK_OUTPUT, SSD_FLOW_WALK_OUTPUT_FUSED = 0, 1, 2, 3
@@ -46,6 +48,15 @@ class ssd_dims_t(ctypes.Structure):
     _fields_ = [("batch", ctypes.c_int64), ("seqlen", ctypes.c_int64),
                 ("nheads", ctypes.c_int64), ("headdim", ctypes.c_int64),
                 ("dstate", ctypes.c_int64), ("ngroups", ctypes.c_int64)]
+
+
+class ssd_stride_t(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("token", ctypes.c_int64)]
+
+
+class ssd_conv_dims_t(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("seqlen", ctypes.c_int64),
+                ("channels", ctypes.c_int64), ("width", ctypes.c_int64)]
 
 
 _lib = None
@@ -119,8 +130,22 @@ def load(path: str = LIB_PATH):
     lib.ssd_state_correction_fwd.restype = ctypes.c_int
     lib.ssd_state_correction_fwd.argtypes = [_vp] * 6 + [dims_p, ctypes.c_int, _vp,
                                                          ctypes.c_size_t, _vp]
+    stride_p, conv_p = ctypes.POINTER(ssd_stride_t), ctypes.POINTER(ssd_conv_dims_t)
+    size_p, ci, cs = ctypes.POINTER(ctypes.c_size_t), ctypes.c_int, ctypes.c_size_t
+    _declare(lib, "ssd_causal_conv_fwd", _vp, stride_p, *[_vp] * 4, ci, _vp, _vp, conv_p, ci, _vp)
+    _declare(lib, "ssd_causal_conv_bwd_workspace_size", conv_p, ci, size_p)
+    _declare(lib, "ssd_causal_conv_bwd", _vp, stride_p, *[_vp] * 4, ci, _vp, ci, *[_vp] * 5, conv_p,
+             ci, _vp, cs, _vp)
+    _declare(lib, "ssd_causal_conv_step", _vp, _vp, stride_p, _vp, _vp, ci, _vp, conv_p, ci, _vp)
     _lib = lib
     return lib
+
+
+def _declare(lib, name, *argtypes):
+    """One entry point that returns a status."""
+    f = getattr(lib, name)
+    f.restype = ctypes.c_int
+    f.argtypes = list(argtypes)
 
 
 def status_name(status: int) -> str:
@@ -519,4 +544,160 @@ def ssd_state_correction_fwd(h_in, dt, A, C, y, final_states=None, workspace=Non
                                              _dtype_code(y.dtype), _ptr(workspace),
                                              workspace.numel(), _stream(stream, dev))
     _check(st, "ssd_state_correction_fwd")
+    return y
+
+
+# ---------------------------------------------------------------- operators around the layer
+class _scope:
+    """Makes the call's device, and the stream it is asked to run on, current,
+    so that what the call allocates belongs to the stream that uses it.  Nothing
+    is entered where they are current already."""
+
+    def __init__(self, device, stream):
+        self.entered = []
+        if stream is not None:
+            if not isinstance(stream, torch.cuda.Stream):
+                stream = (torch.cuda.ExternalStream(int(stream), device=device) if int(stream)
+                          else torch.cuda.default_stream(device))
+            self.entered.append(torch.cuda.stream(stream))
+        elif device.index != torch.cuda.current_device():
+            self.entered.append(torch.cuda.device(device))
+
+    def __enter__(self):
+        for c in self.entered:
+            c.__enter__()
+        return torch.cuda.current_stream().cuda_stream
+
+    def __exit__(self, *exc):
+        for c in reversed(self.entered):
+            c.__exit__(*exc)
+
+
+def _dense(name, t, shape, dtype, device):
+    """A dense argument (or None): checked, then its address."""
+    if t is None:
+        return None
+    _expect(name, t, shape, dtype, device)
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: must be contiguous")
+    return t.data_ptr()
+
+
+def _view(name, t, shape, dtype, device, tokens=True):
+    """An argument that may be a view of a wider tensor: checked, then its
+    address and its batch and token strides.  The dimensions behind the token
+    (or, without tokens, the batch) have to be contiguous."""
+    if t is None:
+        return None, ssd_stride_t(0, 0)
+    _expect(name, t, shape, dtype, device)
+    lead, strides, run = 2 if tokens else 1, t.stride(), 1
+    for i in range(len(shape) - 1, lead - 1, -1):
+        if shape[i] != 1 and strides[i] != run:
+            raise ValueError(f"{name}: its last {len(shape) - lead} dimension(s) must be contiguous")
+        run *= shape[i]
+    return t.data_ptr(), ssd_stride_t(strides[0], strides[1] if tokens else 0)
+
+
+def _workspace(workspace, need, device):
+    """The caller's workspace, or one of ``need`` bytes."""
+    if workspace is None:
+        workspace = torch.empty(max(need, 16), device=device, dtype=torch.uint8)
+    elif not workspace.is_contiguous() or workspace.device != device:
+        raise ValueError(f"workspace: must be contiguous and on {device}")
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def _conv_dims(x, weight):
+    if x.dim() != 3 or weight.dim() != 2:
+        raise ValueError("x must be (b, L, D) and weight (D, W)")
+    b, L, D = x.shape
+    return b, L, D, weight.shape[1], ssd_conv_dims_t(b, L, D, weight.shape[1])
+
+
+def ssd_causal_conv_fwd(x, weight, bias=None, init_state=None, seq_lens=None, silu: bool = True,
+                        return_final_state: bool = False, y=None, final_state=None, stream=None):
+    """Causal depthwise convolution of x (b,L,D; may be a view with strided
+    tokens) by weight (D,W) and bias (D), then (``silu``) the SiLU activation.
+    init_state (b,W-1,D): the inputs before token 0, oldest first (None: zero).
+    seq_lens (b,) int32: the sequences' own lengths in a padded batch; rows of y
+    behind them are zero.  Returns y [, final_state (b,W-1,D): the last inputs]."""
+    b, L, D, W, dims = _conv_dims(x, weight)
+    dev, T, f32 = x.device, x.dtype, torch.float32
+    code = _dtype_code(T)
+    px, sx = _view("x", x, (b, L, D), T, dev)
+    pw = _dense("weight", weight, (D, W), f32, dev)
+    pb = _dense("bias", bias, (D,), f32, dev)
+    pi = _dense("init_state", init_state, (b, W - 1, D), T, dev)
+    pl = _dense("seq_lens", seq_lens, (b,), torch.int32, dev)
+    py = _dense("y", y, (b, L, D), T, dev)
+    pf = _dense("final_state", final_state, (b, W - 1, D), T, dev)
+    with _scope(_device_of(x), stream) as st:
+        if y is None:
+            y = torch.empty((b, L, D), device=dev, dtype=T)
+            py = y.data_ptr()
+        if return_final_state and final_state is None:
+            final_state = torch.empty((b, W - 1, D), device=dev, dtype=T)
+            pf = final_state.data_ptr()
+        _check(load().ssd_causal_conv_fwd(px, sx, pw, pb, pi, pl, int(silu), py, pf, dims, code, st),
+               "ssd_causal_conv_fwd")
+    return (y, final_state) if final_state is not None else y
+
+
+def ssd_causal_conv_bwd_workspace_size(dims: ssd_conv_dims_t, dtype: torch.dtype) -> int:
+    n = ctypes.c_size_t(0)
+    _check(load().ssd_causal_conv_bwd_workspace_size(dims, _dtype_code(dtype), n),
+           "ssd_causal_conv_bwd_workspace_size")
+    return int(n.value)
+
+
+def ssd_causal_conv_bwd(x, weight, bias, dy, init_state=None, dfinal_state=None, seq_lens=None,
+                        silu: bool = True, want_dinit: bool = True, workspace=None, stream=None):
+    """Gradients of ssd_causal_conv_fwd for dL/dy = dy ((b,L,D), x's dtype or
+    fp32) and dL/dfinal_state (None: zero).  Returns a dict: dx and (if
+    want_dinit) dinit in x's dtype, dweight and dbias fp32."""
+    b, L, D, W, dims = _conv_dims(x, weight)
+    dev, T, f32 = x.device, x.dtype, torch.float32
+    code = _dtype_code(T)
+    px, sx = _view("x", x, (b, L, D), T, dev)
+    pw = _dense("weight", weight, (D, W), f32, dev)
+    pb = _dense("bias", bias, (D,), f32, dev)
+    pi = _dense("init_state", init_state, (b, W - 1, D), T, dev)
+    pl = _dense("seq_lens", seq_lens, (b,), torch.int32, dev)
+    pdy = _dense("dy", dy, (b, L, D), f32 if dy.dtype == f32 else T, dev)
+    pdf = _dense("dfinal_state", dfinal_state, (b, W - 1, D), T, dev)
+    with _scope(_device_of(x), stream) as st:
+        out = {"dx": torch.empty((b, L, D), device=dev, dtype=T),
+               "dweight": torch.empty((D, W), device=dev, dtype=f32),
+               "dbias": torch.empty((D,), device=dev, dtype=f32),
+               "dinit": torch.empty((b, W - 1, D), device=dev, dtype=T) if want_dinit else None}
+        workspace, pws, nws = _workspace(workspace, ssd_causal_conv_bwd_workspace_size(dims, T), dev)
+        _check(load().ssd_causal_conv_bwd(
+            px, sx, pw, pb, pi, pl, int(silu), pdy, int(dy.dtype == f32), pdf,
+            out["dx"].data_ptr(), out["dweight"].data_ptr(), out["dbias"].data_ptr(),
+            out["dinit"].data_ptr() if want_dinit else None, dims, code, pws, nws, st),
+            "ssd_causal_conv_bwd")
+    return out
+
+
+def ssd_causal_conv_step(state, x, weight, bias=None, silu: bool = True, y=None, stream=None):
+    """One token: ``state`` (b,W-1,D), the last inputs, is updated in place;
+    x (b,D).  Returns y (b,D)."""
+    if x.dim() != 2 or weight.dim() != 2:
+        raise ValueError("x must be (b, D) and weight (D, W)")
+    b, D = x.shape
+    W = weight.shape[1]
+    dev, T, f32 = x.device, x.dtype, torch.float32
+    code = _dtype_code(T)
+    px, sx = _view("x", x, (b, D), T, dev, tokens=False)
+    ps = _dense("state", state, (b, W - 1, D), T, dev)
+    pw = _dense("weight", weight, (D, W), f32, dev)
+    pb = _dense("bias", bias, (D,), f32, dev)
+    py = _dense("y", y, (b, D), T, dev)
+    with _scope(_device_of(x), stream) as st:
+        if y is None:
+            y = torch.empty((b, D), device=dev, dtype=T)
+            py = y.data_ptr()
+        _check(load().ssd_causal_conv_step(ps, px, sx, pw, pb, int(silu), py,
+                                           ssd_conv_dims_t(b, 1, D, W), code, st),
+               "ssd_causal_conv_step")
     return y
