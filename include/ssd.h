@@ -489,6 +489,60 @@ SSD_API ssd_status_t ssd_causal_conv_step(void* state, const void* x,
                                           const ssd_conv_dims_t* dims, ssd_dtype_t dtype,
                                           void* stream);
 
+typedef struct {
+    int64_t batch;    /* b >= 0 */
+    int64_t seqlen;   /* L >= 0 */
+    int64_t ngroups;  /* G >= 1 */
+    int64_t dstate;   /* N, 1..256 */
+    int64_t rotary;   /* R, even, 0..N: elements of each row that are turned */
+} ssd_rotate_dims_t;
+
+/*
+ * Root-mean-square norm and position rotation of B and C, in one pass.  For
+ * each row v of N elements (one group of one token, of B or of C):
+ *     u = v / sqrt(mean(v^2) + eps) * weight
+ *     (u_i, u_j) <- (u_i cos f - u_j sin f, u_i sin f + u_j cos f),
+ *     f = positions[b,t] * freq[p],  p = 0..R/2-1,
+ * where pair p is (2p, 2p+1) if interleaved is non-zero, else (p, p + R/2);
+ * elements from R on are left unturned.  By the layer's duality C_t is the
+ * query and B_t the key of a group ("Transformers are SSMs" (CiteArk), what
+ * this means): turning both by the position gives the decaying state complex
+ * eigenvalues exp(dt A +- i freq), and the outputs are ssd_chunk_scan_fwd's
+ * and ssd_step's (at seqlen 1) B and C as they stand.
+ * B, C (b,L,G,N) dtype (strided, by B_stride and C_stride); B_out, C_out (b,L,G,N) dtype,
+ * dense.  B_weight, C_weight fp32, (N) for all groups or (if weight_per_group
+ * is non-zero) (G,N).  positions (b,L) int64 (any value: the angle is reduced
+ * in exact integer arithmetic); freq (R/2) fp32, radians a position.
+ */
+SSD_API ssd_status_t ssd_bc_norm_rotate_fwd(const void* B, const ssd_stride_t* B_stride,
+                                            const void* C, const ssd_stride_t* C_stride,
+                                            const float* B_weight, const float* C_weight,
+                                            int weight_per_group, const int64_t* positions,
+                                            const float* freq, float eps, int interleaved,
+                                            void* B_out, void* C_out,
+                                            const ssd_rotate_dims_t* dims, ssd_dtype_t dtype,
+                                            void* stream);
+
+/*
+ * Gradients of ssd_bc_norm_rotate_fwd.  dB_out, dC_out (b,L,G,N) dense, in
+ * dtype or (grad_f32 non-zero) fp32, as ssd_chunk_scan_bwd writes them.
+ * Outputs: dB, dC (b,L,G,N) dtype, dense; dB_weight, dC_weight fp32, of the
+ * weights' shape.  Positions and frequencies get no gradient.  workspace:
+ * partial sums of the weights' gradients.
+ */
+SSD_API ssd_status_t ssd_bc_norm_rotate_bwd_workspace_size(const ssd_rotate_dims_t* dims,
+                                                           ssd_dtype_t dtype, size_t* bytes);
+SSD_API ssd_status_t ssd_bc_norm_rotate_bwd(const void* B, const ssd_stride_t* B_stride,
+                                            const void* C, const ssd_stride_t* C_stride,
+                                            const float* B_weight, const float* C_weight,
+                                            int weight_per_group, const int64_t* positions,
+                                            const float* freq, float eps, int interleaved,
+                                            const void* dB_out, const void* dC_out, int grad_f32,
+                                            void* dB, void* dC, float* dB_weight,
+                                            float* dC_weight, const ssd_rotate_dims_t* dims,
+                                            ssd_dtype_t dtype, void* workspace,
+                                            size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -50,6 +50,22 @@ ssd_status_t conv_dims(const ssd_conv_dims_t* dims, ssd_dtype_t dtype, ssd::Conv
     return check_dtype(dtype, t);
 }
 
+ssd_status_t rotate_dims(const ssd_rotate_dims_t* dims, ssd_dtype_t dtype, ssd::RotateDims* d,
+                         ssd::Elt* t) {
+    if (!dims) return fail(SSD_ERR_INVALID_ARG, "dims is NULL");
+    ssd_status_t st = check_tokens(dims->batch, dims->seqlen);
+    if (st != SSD_OK) return st;
+    if (dims->ngroups < 1 || dims->dstate < 1)
+        return fail(SSD_ERR_INVALID_ARG, "ngroups and dstate must be >= 1");
+    if (dims->dstate > 256) return fail(SSD_ERR_UNSUPPORTED, "dstate must be <= 256");
+    if (dims->ngroups > 65535) return fail(SSD_ERR_UNSUPPORTED, "ngroups must be <= 65535");
+    if (dims->rotary < 0 || dims->rotary % 2 != 0 || dims->rotary > dims->dstate)
+        return fail(SSD_ERR_INVALID_ARG, "rotary (%lld) must be even and in 0..dstate",
+                    (long long)dims->rotary);
+    *d = ssd::RotateDims{dims->batch, dims->seqlen, dims->ngroups, dims->dstate, dims->rotary};
+    return check_dtype(dtype, t);
+}
+
 #define REQUIRE_STRIDE(p)                                                                \
     do {                                                                                 \
         if (!(p)) return fail(SSD_ERR_INVALID_ARG, "%s is NULL", #p);                    \
@@ -171,6 +187,80 @@ ssd_status_t ssd_causal_conv_step(void* state, const void* x, const ssd_stride_t
     cudaError_t e = ssd::launch_conv_step(state, x, x_stride->batch, weight, bias, silu != 0, y,
                                           d, t, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? SSD_OK : cuda_fail(e, "convolution step kernel");
+}
+
+// ---------------------------------------------------------------- norm and rotation of B and C
+ssd_status_t ssd_bc_norm_rotate_fwd(const void* B, const ssd_stride_t* B_stride, const void* C,
+                                    const ssd_stride_t* C_stride, const float* B_weight,
+                                    const float* C_weight, int weight_per_group,
+                                    const int64_t* positions, const float* freq, float eps,
+                                    int interleaved, void* B_out, void* C_out,
+                                    const ssd_rotate_dims_t* dims, ssd_dtype_t dtype,
+                                    void* stream) {
+    ssd::clear_error_detail();
+    ssd::RotateDims d{}; ssd::Elt t = ssd::Elt::BF16;
+    ssd_status_t st = rotate_dims(dims, dtype, &d, &t);
+    if (st != SSD_OK) return st;
+    if (!(eps >= 0.f)) return fail(SSD_ERR_INVALID_ARG, "eps must be >= 0");
+    REQUIRE_STRIDE(B_stride); REQUIRE_STRIDE(C_stride);
+    if (d.b == 0 || d.L == 0) return SSD_OK;
+    REQUIRE_VIEW(B); REQUIRE_VIEW(C);
+    REQUIRE_PTR(B_weight); REQUIRE_PTR(C_weight); REQUIRE_PTR(B_out); REQUIRE_PTR(C_out);
+    if (d.R > 0) { REQUIRE_PTR(positions); REQUIRE_PTR(freq); }
+    REQUIRE_DEVICE(B);
+    const ssd::RotateArgs r{B, C, stride_of(*B_stride), stride_of(*C_stride), B_weight, C_weight,
+                            weight_per_group != 0, positions, freq, eps, interleaved != 0};
+    cudaError_t e = ssd::launch_norm_rotate_fwd(r, B_out, C_out, d, t,
+                                                static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? SSD_OK : cuda_fail(e, "norm and rotation kernel");
+}
+
+ssd_status_t ssd_bc_norm_rotate_bwd_workspace_size(const ssd_rotate_dims_t* dims,
+                                                   ssd_dtype_t dtype, size_t* bytes) {
+    ssd::clear_error_detail();
+    if (!bytes) return fail(SSD_ERR_INVALID_ARG, "bytes is NULL");
+    ssd::RotateDims d{}; ssd::Elt t = ssd::Elt::BF16;
+    ssd_status_t st = rotate_dims(dims, dtype, &d, &t);
+    if (st != SSD_OK) return st;
+    *bytes = ssd::norm_rotate_bwd_workspace_bytes(d);
+    return SSD_OK;
+}
+
+ssd_status_t ssd_bc_norm_rotate_bwd(const void* B, const ssd_stride_t* B_stride, const void* C,
+                                    const ssd_stride_t* C_stride, const float* B_weight,
+                                    const float* C_weight, int weight_per_group,
+                                    const int64_t* positions, const float* freq, float eps,
+                                    int interleaved, const void* dB_out, const void* dC_out,
+                                    int grad_f32, void* dB, void* dC, float* dB_weight,
+                                    float* dC_weight, const ssd_rotate_dims_t* dims,
+                                    ssd_dtype_t dtype, void* workspace, size_t workspace_bytes,
+                                    void* stream) {
+    ssd::clear_error_detail();
+    ssd::RotateDims d{}; ssd::Elt t = ssd::Elt::BF16;
+    ssd_status_t st = rotate_dims(dims, dtype, &d, &t);
+    if (st != SSD_OK) return st;
+    if (!(eps >= 0.f)) return fail(SSD_ERR_INVALID_ARG, "eps must be >= 0");
+    REQUIRE_STRIDE(B_stride); REQUIRE_STRIDE(C_stride);
+    REQUIRE_PTR(B_weight); REQUIRE_PTR(C_weight);
+    REQUIRE_PTR(dB_weight); REQUIRE_PTR(dC_weight);
+    if (d.b > 0 && d.L > 0) {
+        REQUIRE_VIEW(B); REQUIRE_VIEW(C);
+        REQUIRE_PTR(dB_out); REQUIRE_PTR(dC_out); REQUIRE_PTR(dB); REQUIRE_PTR(dC);
+        if (d.R > 0) { REQUIRE_PTR(positions); REQUIRE_PTR(freq); }
+    }
+    const size_t need = ssd::norm_rotate_bwd_workspace_bytes(d);
+    if (workspace_bytes < need)
+        return fail(SSD_ERR_INVALID_ARG, "workspace too small: %zu bytes given, %zu needed",
+                    workspace_bytes, need);
+    if (need > 0) REQUIRE_PTR(workspace);
+    REQUIRE_DEVICE(B_weight);
+    const ssd::RotateArgs r{B, C, stride_of(*B_stride), stride_of(*C_stride), B_weight, C_weight,
+                            weight_per_group != 0, positions, freq, eps, interleaved != 0};
+    cudaError_t e = ssd::launch_norm_rotate_bwd(r, dB_out, dC_out, grad_f32 != 0, dB, dC,
+                                                dB_weight, dC_weight,
+                                                static_cast<float*>(workspace), d, t,
+                                                static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? SSD_OK : cuda_fail(e, "norm and rotation gradient kernels");
 }
 
 }  // extern "C"

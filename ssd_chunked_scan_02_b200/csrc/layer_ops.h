@@ -29,4 +29,25 @@ cudaError_t launch_conv_step(void* state, const void* x, int64_t x_batch, const 
                              const float* bias, bool silu, void* y, const ConvDims& d, Elt t,
                              cudaStream_t s);
 
+// ------------------------------------------------------------------ norm and rotation of B and C
+struct RotateDims {
+    int64_t b, L, G, N, R;
+};
+struct RotateArgs {
+    const void *B, *C;
+    Stride bs, cs;
+    const float *wB, *wC;
+    bool per_group;
+    const int64_t* pos;
+    const float* freq;
+    float eps;
+    bool interleaved;
+};
+cudaError_t launch_norm_rotate_fwd(const RotateArgs& r, void* oB, void* oC, const RotateDims& d,
+                                   Elt t, cudaStream_t s);
+size_t norm_rotate_bwd_workspace_bytes(const RotateDims& d);
+cudaError_t launch_norm_rotate_bwd(const RotateArgs& r, const void* gB, const void* gC,
+                                   bool grad_f32, void* dB, void* dC, float* dwB, float* dwC,
+                                   float* ws, const RotateDims& d, Elt t, cudaStream_t s);
+
 }  // namespace ssd

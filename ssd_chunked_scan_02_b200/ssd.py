@@ -32,7 +32,8 @@ EXPORTED = ("ssd_status_string", "ssd_last_error_detail", "ssd_chunk_scan_fwd_wo
             "ssd_state_correction_workspace_size", "ssd_state_correction_fwd",
             "ssd_chunk_scan_fwd_flow_workspace_size", "ssd_chunk_scan_fwd_with_flow",
             "ssd_causal_conv_fwd", "ssd_causal_conv_bwd_workspace_size", "ssd_causal_conv_bwd",
-            "ssd_causal_conv_step")
+            "ssd_causal_conv_step", "ssd_bc_norm_rotate_fwd",
+            "ssd_bc_norm_rotate_bwd_workspace_size", "ssd_bc_norm_rotate_bwd")
 
 # ssd_chunk_scan_fwd_data_flow results
 SSD_FLOW_SIMT, SSD_FLOW_TC_THREE_KERNEL, SSD_FLOW_WALK_OUTPUT, SSD_FLOW_WALK_OUTPUT_FUSED = 0, 1, 2, 3
@@ -57,6 +58,12 @@ class ssd_stride_t(ctypes.Structure):
 class ssd_conv_dims_t(ctypes.Structure):
     _fields_ = [("batch", ctypes.c_int64), ("seqlen", ctypes.c_int64),
                 ("channels", ctypes.c_int64), ("width", ctypes.c_int64)]
+
+
+class ssd_rotate_dims_t(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("seqlen", ctypes.c_int64),
+                ("ngroups", ctypes.c_int64), ("dstate", ctypes.c_int64),
+                ("rotary", ctypes.c_int64)]
 
 
 _lib = None
@@ -137,6 +144,11 @@ def load(path: str = LIB_PATH):
     _declare(lib, "ssd_causal_conv_bwd", _vp, stride_p, *[_vp] * 4, ci, _vp, ci, *[_vp] * 5, conv_p,
              ci, _vp, cs, _vp)
     _declare(lib, "ssd_causal_conv_step", _vp, _vp, stride_p, _vp, _vp, ci, _vp, conv_p, ci, _vp)
+    rot_p, rot = ctypes.POINTER(ssd_rotate_dims_t), [_vp, stride_p] * 2 + [_vp, _vp, ci, _vp, _vp,
+                                                                           ctypes.c_float, ci]
+    _declare(lib, "ssd_bc_norm_rotate_fwd", *rot, _vp, _vp, rot_p, ci, _vp)
+    _declare(lib, "ssd_bc_norm_rotate_bwd_workspace_size", rot_p, ci, size_p)
+    _declare(lib, "ssd_bc_norm_rotate_bwd", *rot, _vp, _vp, ci, *[_vp] * 4, rot_p, ci, _vp, cs, _vp)
     _lib = lib
     return lib
 
@@ -699,5 +711,80 @@ def ssd_causal_conv_step(state, x, weight, bias=None, silu: bool = True, y=None,
             py = y.data_ptr()
         _check(load().ssd_causal_conv_step(ps, px, sx, pw, pb, int(silu), py,
                                            ssd_conv_dims_t(b, 1, D, W), code, st),
-               "ssd_causal_conv_step")
+               "ssd_causal_conv_step", "ssd_bc_norm_rotate_fwd",
+            "ssd_bc_norm_rotate_bwd_workspace_size", "ssd_bc_norm_rotate_bwd")
     return y
+
+
+def _rotate_args(B, C, B_weight, C_weight, positions, freq, eps, interleaved):
+    """Checks the inputs that ssd_bc_norm_rotate_fwd and _bwd share; returns
+    their C arguments, the dims, the device and the weights' shape."""
+    if B.dim() != 4 or freq.dim() != 1:
+        raise ValueError("B and C must be (b, L, G, N) and freq (R / 2)")
+    b, L, G, N = B.shape
+    dev, T, f32 = B.device, B.dtype, torch.float32
+    code = _dtype_code(T)
+    pB, sB = _view("B", B, (b, L, G, N), T, dev)
+    pC, sC = _view("C", C, (b, L, G, N), T, dev)
+    per_group = B_weight.dim() == 2
+    shape = (G, N) if per_group else (N,)
+    args = (pB, sB, pC, sC, _dense("B_weight", B_weight, shape, f32, dev),
+            _dense("C_weight", C_weight, shape, f32, dev), int(per_group),
+            _dense("positions", positions, (b, L), torch.int64, dev),
+            _dense("freq", freq, (freq.shape[0],), f32, dev), float(eps), int(interleaved))
+    return args, ssd_rotate_dims_t(b, L, G, N, 2 * freq.shape[0]), dev, code, shape
+
+
+def ssd_bc_norm_rotate_fwd(B, C, B_weight, C_weight, positions, freq, eps: float = 1e-5,
+                           interleaved: bool = False, B_out=None, C_out=None, stream=None):
+    """Each row (one group of one token) of B and of C (b,L,G,N; may be views with
+    strided tokens) divided by its root mean square, multiplied by the weight ((N)
+    or (G,N)), and its first 2 * len(freq) elements turned in pairs by
+    positions (b,L, int64) * freq.  Returns dense B, C for ssd_chunk_scan_fwd or
+    (at L = 1) ssd_step."""
+    args, dims, dev, code, _ = _rotate_args(B, C, B_weight, C_weight, positions, freq, eps,
+                                            interleaved)
+    oB = _dense("B_out", B_out, tuple(B.shape), B.dtype, dev)
+    oC = _dense("C_out", C_out, tuple(B.shape), B.dtype, dev)
+    with _scope(_device_of(B), stream) as st:
+        if B_out is None:
+            B_out = torch.empty(B.shape, device=dev, dtype=B.dtype)
+            oB = B_out.data_ptr()
+        if C_out is None:
+            C_out = torch.empty(B.shape, device=dev, dtype=B.dtype)
+            oC = C_out.data_ptr()
+        _check(load().ssd_bc_norm_rotate_fwd(*args, oB, oC, dims, code, st),
+               "ssd_bc_norm_rotate_fwd")
+    return B_out, C_out
+
+
+def ssd_bc_norm_rotate_bwd_workspace_size(dims: ssd_rotate_dims_t, dtype: torch.dtype) -> int:
+    n = ctypes.c_size_t(0)
+    _check(load().ssd_bc_norm_rotate_bwd_workspace_size(dims, _dtype_code(dtype), n),
+           "ssd_bc_norm_rotate_bwd_workspace_size")
+    return int(n.value)
+
+
+def ssd_bc_norm_rotate_bwd(B, C, B_weight, C_weight, positions, freq, dB_out, dC_out,
+                           eps: float = 1e-5, interleaved: bool = False, workspace=None,
+                           stream=None):
+    """Gradients of ssd_bc_norm_rotate_fwd for dL/d its outputs (b,L,G,N), in B's
+    dtype or fp32.  Returns a dict: dB, dC in B's dtype, dwB, dwC fp32 (of the
+    weights' shape)."""
+    args, dims, dev, code, shape = _rotate_args(B, C, B_weight, C_weight, positions, freq, eps,
+                                                interleaved)
+    f32 = torch.float32
+    gt = f32 if dB_out.dtype == f32 else B.dtype
+    gB = _dense("dB_out", dB_out, tuple(B.shape), gt, dev)
+    gC = _dense("dC_out", dC_out, tuple(B.shape), gt, dev)
+    with _scope(_device_of(B), stream) as st:
+        out = {"dB": torch.empty(B.shape, device=dev, dtype=B.dtype),
+               "dC": torch.empty(B.shape, device=dev, dtype=B.dtype),
+               "dwB": torch.empty(shape, device=dev, dtype=f32),
+               "dwC": torch.empty(shape, device=dev, dtype=f32)}
+        workspace, pws, nws = _workspace(workspace,
+                                         ssd_bc_norm_rotate_bwd_workspace_size(dims, B.dtype), dev)
+        _check(load().ssd_bc_norm_rotate_bwd(*args, gB, gC, int(gt == f32),
+                                             *(v.data_ptr() for v in out.values()), dims, code,
+                                             pws, nws, st), "ssd_bc_norm_rotate_bwd")
+    return out

@@ -53,3 +53,18 @@ def conv(x, w, bias, init, lens, silu):
         ys.append(torch.cat(out + [x.new_zeros(L - n, D)], 0))
         fs.append(rows[n:n + W - 1])
     return torch.stack(ys), torch.stack(fs)
+
+
+# ------------------------------------------------------------------ norm and rotation of B and C
+def norm_rotate(v, w, pos, freq, eps, interleaved):
+    """v (b,L,G,N), w (N) or (G,N), pos (b,L), freq (R/2): fp64, differentiable."""
+    R = 2 * freq.numel()
+    u = v / torch.sqrt(v.square().mean(-1, keepdim=True) + eps) * w
+    f = (pos.double()[..., None] * freq.double())[:, :, None]
+    c, s = torch.cos(f), torch.sin(f)
+    out = list(u.unbind(-1))
+    for p in range(R // 2):
+        i, j = (2 * p, 2 * p + 1) if interleaved else (p, p + R // 2)
+        out[i], out[j] = u[..., i] * c[..., p] - u[..., j] * s[..., p], \
+            u[..., i] * s[..., p] + u[..., j] * c[..., p]
+    return torch.stack(out, -1)
