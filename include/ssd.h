@@ -490,6 +490,81 @@ SSD_API ssd_status_t ssd_causal_conv_step(void* state, const void* x,
                                           void* stream);
 
 typedef struct {
+    int64_t batch;     /* b >= 0 */
+    int64_t seqlen;    /* L >= 0 */
+    int64_t channels;  /* D >= 1 */
+    int64_t dstate;    /* N, 1..256 */
+    int64_t ngroups;   /* G >= 1, D % G == 0: channel d reads B/C group d / (D / G) */
+} ssd_selective_dims_t;
+
+typedef struct {
+    ssd_stride_t x, dt, B, C, z;   /* z is ignored where z is NULL */
+} ssd_selective_strides_t;
+
+/*
+ * Selective scan with a decay per (channel, state):
+ *     dt'_t[d]  = softplus(dt_t[d] + dt_bias[d]) if softplus is non-zero,
+ *                 else dt_t[d] + dt_bias[d]
+ *     h_t[d,n]  = exp(dt'_t[d] * A[d,n]) * h_{t-1}[d,n] + dt'_t[d] * x_t[d] * B_t[n]
+ *     y_t[d]    = (sum_n C_t[n] * h_t[d,n] + D[d] * x_t[d]) * silu(z_t[d])
+ * x, dt, z, y (b,L,D) dtype; B, C (b,L,G,N) dtype; A (D,N), D (D), dt_bias (D)
+ * fp32; init_states, final_states (b,D,N) fp32.  D and dt_bias may be NULL
+ * (zero), z NULL (no gate), init_states NULL (zero), final_states NULL (not
+ * wanted).  All arithmetic, and the state, is fp32.  A <= 0 is the model's
+ * regime; a growing state (A > 0) is computed as far as fp32 reaches.
+ * workspace: where batch x channels alone do not fill the GPU, the sequence is
+ * cut into spans that run side by side, and holds the state that each span
+ * contributes and its sum of dt' (NULL only when the reported size is 0).
+ */
+SSD_API ssd_status_t ssd_selective_scan_fwd_workspace_size(const ssd_selective_dims_t* dims,
+                                                           ssd_dtype_t dtype, size_t* bytes);
+SSD_API ssd_status_t ssd_selective_scan_fwd(const void* x, const void* dt, const float* A,
+                                            const void* B, const void* C, const float* D,
+                                            const void* z, const float* dt_bias, int softplus,
+                                            const float* init_states, const int32_t* seq_lens,
+                                            void* y, float* final_states,
+                                            const ssd_selective_strides_t* strides,
+                                            const ssd_selective_dims_t* dims, ssd_dtype_t dtype,
+                                            void* workspace, size_t workspace_bytes,
+                                            void* stream);
+
+/*
+ * Gradients of ssd_selective_scan_fwd (the chain rule on its recurrence; the
+ * states are computed again).  dy (b,L,D) dtype, dense; dfinal_states (b,D,N)
+ * fp32 or NULL (zero).  Outputs, all fully written: dx, ddt (b,L,D) dtype, dB,
+ * dC (b,L,G,N) dtype (sums over a group's channels), dz (b,L,D) dtype (only
+ * where z is given), dA (D,N), dD (D), ddt_bias (D) fp32 (dD, ddt_bias, and
+ * dinit_states (b,D,N) fp32 = dL/dinit_states, may be NULL: not wanted).
+ * workspace: the states at every eighth token, and partial sums.
+ */
+SSD_API ssd_status_t ssd_selective_scan_bwd_workspace_size(const ssd_selective_dims_t* dims,
+                                                           ssd_dtype_t dtype, size_t* bytes);
+SSD_API ssd_status_t ssd_selective_scan_bwd(const void* x, const void* dt, const float* A,
+                                            const void* B, const void* C, const float* D,
+                                            const void* z, const float* dt_bias, int softplus,
+                                            const float* init_states, const int32_t* seq_lens,
+                                            const void* dy, const float* dfinal_states, void* dx,
+                                            void* ddt, float* dA, void* dB, void* dC, float* dD,
+                                            void* dz, float* ddt_bias, float* dinit_states,
+                                            const ssd_selective_strides_t* strides,
+                                            const ssd_selective_dims_t* dims, ssd_dtype_t dtype,
+                                            void* workspace, size_t workspace_bytes,
+                                            void* stream);
+
+/*
+ * One token of ssd_selective_scan_fwd for a batch of sequences: state (b,D,N)
+ * fp32 is updated in place.  x, dt, z (b,D) and B, C (b,G,N) dtype (strided:
+ * the batch strides), y (b,D) dtype.  dims->seqlen is ignored.
+ */
+SSD_API ssd_status_t ssd_selective_step(float* state, const void* x, const void* dt,
+                                        const float* A, const void* B, const void* C,
+                                        const float* D, const void* z, const float* dt_bias,
+                                        int softplus, void* y,
+                                        const ssd_selective_strides_t* strides,
+                                        const ssd_selective_dims_t* dims, ssd_dtype_t dtype,
+                                        void* stream);
+
+typedef struct {
     int64_t batch;    /* b >= 0 */
     int64_t seqlen;   /* L >= 0 */
     int64_t ngroups;  /* G >= 1 */

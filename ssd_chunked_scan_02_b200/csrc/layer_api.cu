@@ -50,6 +50,27 @@ ssd_status_t conv_dims(const ssd_conv_dims_t* dims, ssd_dtype_t dtype, ssd::Conv
     return check_dtype(dtype, t);
 }
 
+ssd_status_t selective_dims(const ssd_selective_dims_t* dims, ssd_dtype_t dtype,
+                            ssd::SelectiveDims* d, ssd::Elt* t) {
+    if (!dims) return fail(SSD_ERR_INVALID_ARG, "dims is NULL");
+    ssd_status_t st = check_tokens(dims->batch, dims->seqlen);
+    if (st != SSD_OK) return st;
+    if (dims->channels < 1 || dims->dstate < 1 || dims->ngroups < 1)
+        return fail(SSD_ERR_INVALID_ARG, "channels, dstate and ngroups must be >= 1");
+    if (dims->channels % dims->ngroups != 0)
+        return fail(SSD_ERR_INVALID_ARG, "channels (%lld) must be a multiple of ngroups (%lld)",
+                    (long long)dims->channels, (long long)dims->ngroups);
+    if (dims->dstate > 256) return fail(SSD_ERR_UNSUPPORTED, "dstate must be <= 256");
+    // at least one block of 128 threads for every four channels of a sequence, in
+    // the widest layout; 32-token pieces of a sequence run side by side at most
+    if ((double)dims->batch * (double)dims->channels * ((double)dims->seqlen / 32 + 1) >
+        (double)kMaxSize * 4)
+        return fail(SSD_ERR_UNSUPPORTED, "batch * channels * seqlen exceeds the launch grid");
+    *d = ssd::SelectiveDims{dims->batch, dims->seqlen, dims->channels, dims->dstate,
+                            dims->ngroups};
+    return check_dtype(dtype, t);
+}
+
 ssd_status_t rotate_dims(const ssd_rotate_dims_t* dims, ssd_dtype_t dtype, ssd::RotateDims* d,
                          ssd::Elt* t) {
     if (!dims) return fail(SSD_ERR_INVALID_ARG, "dims is NULL");
@@ -187,6 +208,138 @@ ssd_status_t ssd_causal_conv_step(void* state, const void* x, const ssd_stride_t
     cudaError_t e = ssd::launch_conv_step(state, x, x_stride->batch, weight, bias, silu != 0, y,
                                           d, t, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? SSD_OK : cuda_fail(e, "convolution step kernel");
+}
+
+// ---------------------------------------------------------------- selective scan
+namespace {
+ssd::SelectiveArgs selective_args(const void* x, const void* dt, const float* A, const void* B,
+                                  const void* C, const float* D, const void* z,
+                                  const float* dt_bias, int softplus, const float* init,
+                                  const int32_t* lens, const ssd_selective_strides_t& st) {
+    return ssd::SelectiveArgs{x, dt, B, C, z, stride_of(st.x), stride_of(st.dt),
+                              stride_of(st.B), stride_of(st.C), stride_of(st.z), A, D, dt_bias,
+                              init, lens, softplus != 0};
+}
+}  // namespace
+
+ssd_status_t ssd_selective_scan_fwd_workspace_size(const ssd_selective_dims_t* dims,
+                                                   ssd_dtype_t dtype, size_t* bytes) {
+    ssd::clear_error_detail();
+    if (!bytes) return fail(SSD_ERR_INVALID_ARG, "bytes is NULL");
+    ssd::SelectiveDims d{}; ssd::Elt t = ssd::Elt::BF16;
+    ssd_status_t st = selective_dims(dims, dtype, &d, &t);
+    if (st != SSD_OK) return st;
+    *bytes = ssd::selective_fwd_workspace_bytes(d);
+    return SSD_OK;
+}
+
+ssd_status_t ssd_selective_scan_fwd(const void* x, const void* dt, const float* A, const void* B,
+                                    const void* C, const float* D, const void* z,
+                                    const float* dt_bias, int softplus,
+                                    const float* init_states, const int32_t* seq_lens, void* y,
+                                    float* final_states, const ssd_selective_strides_t* strides,
+                                    const ssd_selective_dims_t* dims, ssd_dtype_t dtype,
+                                    void* workspace, size_t workspace_bytes, void* stream) {
+    ssd::clear_error_detail();
+    ssd::SelectiveDims d{}; ssd::Elt t = ssd::Elt::BF16;
+    ssd_status_t st = selective_dims(dims, dtype, &d, &t);
+    if (st != SSD_OK) return st;
+    OPTIONAL_PTR(D); OPTIONAL_PTR(dt_bias); OPTIONAL_PTR(init_states); OPTIONAL_PTR(final_states);
+    REQUIRE_LENS(seq_lens);
+    REQUIRE_STRIDE(strides);
+    if (d.b == 0 || (d.L == 0 && !final_states)) return SSD_OK;
+    REQUIRE_PTR(A);
+    if (d.L > 0) {
+        REQUIRE_VIEW(x); REQUIRE_VIEW(dt); REQUIRE_VIEW(B); REQUIRE_VIEW(C);
+        if (z) REQUIRE_VIEW(z);
+        REQUIRE_PTR(y);
+    }
+    const size_t need = ssd::selective_fwd_workspace_bytes(d);
+    if (workspace_bytes < need)
+        return fail(SSD_ERR_INVALID_ARG, "workspace too small: %zu bytes given, %zu needed",
+                    workspace_bytes, need);
+    if (need > 0) REQUIRE_PTR(workspace);
+    REQUIRE_DEVICE(A);
+    cudaError_t e = ssd::launch_selective_fwd(
+        selective_args(x, dt, A, B, C, D, z, dt_bias, softplus, init_states, seq_lens, *strides),
+        y, final_states, static_cast<float*>(workspace), d, t, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? SSD_OK : cuda_fail(e, "selective scan kernels");
+}
+
+ssd_status_t ssd_selective_scan_bwd_workspace_size(const ssd_selective_dims_t* dims,
+                                                   ssd_dtype_t dtype, size_t* bytes) {
+    ssd::clear_error_detail();
+    if (!bytes) return fail(SSD_ERR_INVALID_ARG, "bytes is NULL");
+    ssd::SelectiveDims d{}; ssd::Elt t = ssd::Elt::BF16;
+    ssd_status_t st = selective_dims(dims, dtype, &d, &t);
+    if (st != SSD_OK) return st;
+    *bytes = ssd::selective_bwd_workspace_bytes(d);
+    return SSD_OK;
+}
+
+ssd_status_t ssd_selective_scan_bwd(const void* x, const void* dt, const float* A, const void* B,
+                                    const void* C, const float* D, const void* z,
+                                    const float* dt_bias, int softplus,
+                                    const float* init_states, const int32_t* seq_lens,
+                                    const void* dy, const float* dfinal_states, void* dx,
+                                    void* ddt, float* dA, void* dB, void* dC, float* dD, void* dz,
+                                    float* ddt_bias, float* dinit_states,
+                                    const ssd_selective_strides_t* strides,
+                                    const ssd_selective_dims_t* dims, ssd_dtype_t dtype,
+                                    void* workspace, size_t workspace_bytes, void* stream) {
+    ssd::clear_error_detail();
+    ssd::SelectiveDims d{}; ssd::Elt t = ssd::Elt::BF16;
+    ssd_status_t st = selective_dims(dims, dtype, &d, &t);
+    if (st != SSD_OK) return st;
+    OPTIONAL_PTR(D); OPTIONAL_PTR(dt_bias); OPTIONAL_PTR(init_states);
+    OPTIONAL_PTR(dfinal_states); OPTIONAL_PTR(dD); OPTIONAL_PTR(ddt_bias);
+    OPTIONAL_PTR(dinit_states);
+    REQUIRE_LENS(seq_lens);
+    REQUIRE_STRIDE(strides);
+    REQUIRE_PTR(A); REQUIRE_PTR(dA);
+    if (d.b > 0 && d.L > 0) {
+        REQUIRE_VIEW(x); REQUIRE_VIEW(dt); REQUIRE_VIEW(B); REQUIRE_VIEW(C);
+        REQUIRE_PTR(dy); REQUIRE_PTR(dx); REQUIRE_PTR(ddt); REQUIRE_PTR(dB); REQUIRE_PTR(dC);
+        if (z) { REQUIRE_VIEW(z); REQUIRE_PTR(dz); }
+    }
+    const size_t need = ssd::selective_bwd_workspace_bytes(d);
+    if (workspace_bytes < need)
+        return fail(SSD_ERR_INVALID_ARG, "workspace too small: %zu bytes given, %zu needed",
+                    workspace_bytes, need);
+    if (need > 0) REQUIRE_PTR(workspace);
+    REQUIRE_DEVICE(A);
+    const ssd::SelectiveGrads g{dy, dfinal_states, dx, ddt, dB, dC, dz,
+                                dA, dD, ddt_bias, dinit_states};
+    cudaError_t e = ssd::launch_selective_bwd(
+        selective_args(x, dt, A, B, C, D, z, dt_bias, softplus, init_states, seq_lens, *strides),
+        g, static_cast<float*>(workspace), d, t, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? SSD_OK : cuda_fail(e, "selective scan gradient kernels");
+}
+
+ssd_status_t ssd_selective_step(float* state, const void* x, const void* dt, const float* A,
+                                const void* B, const void* C, const float* D, const void* z,
+                                const float* dt_bias, int softplus, void* y,
+                                const ssd_selective_strides_t* strides,
+                                const ssd_selective_dims_t* dims, ssd_dtype_t dtype,
+                                void* stream) {
+    ssd::clear_error_detail();
+    ssd::SelectiveDims d{}; ssd::Elt t = ssd::Elt::BF16;
+    ssd_selective_dims_t one{};
+    if (dims) one = *dims;
+    one.seqlen = 1;
+    ssd_status_t st = selective_dims(dims ? &one : nullptr, dtype, &d, &t);
+    if (st != SSD_OK) return st;
+    OPTIONAL_PTR(D); OPTIONAL_PTR(dt_bias);
+    REQUIRE_STRIDE(strides);
+    if (d.b == 0) return SSD_OK;
+    REQUIRE_PTR(state); REQUIRE_PTR(A); REQUIRE_PTR(y);
+    REQUIRE_VIEW(x); REQUIRE_VIEW(dt); REQUIRE_VIEW(B); REQUIRE_VIEW(C);
+    if (z) REQUIRE_VIEW(z);
+    REQUIRE_DEVICE(state);
+    cudaError_t e = ssd::launch_selective_step(
+        state, selective_args(x, dt, A, B, C, D, z, dt_bias, softplus, nullptr, nullptr, *strides),
+        y, d, t, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? SSD_OK : cuda_fail(e, "selective step kernel");
 }
 
 // ---------------------------------------------------------------- norm and rotation of B and C

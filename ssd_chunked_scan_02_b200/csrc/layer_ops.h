@@ -29,6 +29,32 @@ cudaError_t launch_conv_step(void* state, const void* x, int64_t x_batch, const 
                              const float* bias, bool silu, void* y, const ConvDims& d, Elt t,
                              cudaStream_t s);
 
+// ------------------------------------------------------------------ selective scan
+struct SelectiveDims {
+    int64_t b, L, D, N, G;
+};
+struct SelectiveArgs {
+    const void *x, *dt, *B, *C, *z;
+    Stride xs, dts, Bs, Cs, zs;
+    const float *A, *D, *dt_bias, *init;
+    const int32_t* lens;
+    bool softplus;
+};
+size_t selective_fwd_workspace_bytes(const SelectiveDims& d);
+cudaError_t launch_selective_fwd(const SelectiveArgs& a, void* y, float* final_states, float* ws,
+                                 const SelectiveDims& d, Elt t, cudaStream_t s);
+struct SelectiveGrads {
+    const void* dy;
+    const float* dfinal;
+    void *dx, *ddt, *dB, *dC, *dz;
+    float *dA, *dD, *ddt_bias, *dinit;
+};
+size_t selective_bwd_workspace_bytes(const SelectiveDims& d);
+cudaError_t launch_selective_bwd(const SelectiveArgs& a, const SelectiveGrads& g, float* ws,
+                                 const SelectiveDims& d, Elt t, cudaStream_t s);
+cudaError_t launch_selective_step(float* state, const SelectiveArgs& a, void* y,
+                                  const SelectiveDims& d, Elt t, cudaStream_t s);
+
 // ------------------------------------------------------------------ norm and rotation of B and C
 struct RotateDims {
     int64_t b, L, G, N, R;

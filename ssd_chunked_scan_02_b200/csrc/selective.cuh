@@ -1,0 +1,145 @@
+// selective.cuh -- what the selective scan's kernels share: how channels and
+// states lie over a warp's lanes, sums across lanes, and a tile's loads.
+#pragma once
+#include <cuda_bf16.h>
+#include <stdint.h>
+
+#include "common.cuh"
+#include "layer_ops.h"
+#include "vec_io.cuh"
+
+namespace ssd {
+
+constexpr float kLog2E = 1.4426950408889634f;
+
+// 2^v; results below 2^-126 are zero (a decay that small leaves nothing of a state).
+__device__ __forceinline__ float ex2(float v) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+
+// softplus(v) = log(1 + exp(v)); above 20 the difference to v is below half a
+// rounding of v.
+__device__ __forceinline__ float softplus_f32(float v) {
+    return v > 20.f ? v : log1pf(__expf(v));
+}
+
+__device__ __forceinline__ int64_t own_length(const int32_t* lens, int64_t b, int64_t L) {
+    if (!lens) return L;
+    const int64_t n = lens[b];
+    return n < 0 ? 0 : (n > L ? L : n);
+}
+
+// Adds v[i] over LANES lanes that lie STRIDE apart, `lane` being this one's place
+// among them, for all NV values at once: each step gives half of the values away and keeps the sums of the
+// other half, so NV values cost NV - NV / LANES shuffles instead of
+// NV * log2(LANES).  Lane l ends with values l * NV / LANES + i in v[i]
+// (NV >= LANES), or with value l * NV / LANES in v[0] (NV < LANES).
+template <int NV, int LANES, int STRIDE = 1>
+__device__ __forceinline__ void fold(float* v, int lane) {
+    int n = NV;
+#pragma unroll
+    for (int o = LANES / 2; o > 0; o >>= 1) {
+        if (n > 1) {
+            n /= 2;
+            const bool up = (lane & o) != 0;
+#pragma unroll
+            for (int i = 0; i < NV / 2; ++i) {
+                if (i < n) {
+                    const float keep = up ? v[n + i] : v[i], give = up ? v[i] : v[n + i];
+                    v[i] = keep + __shfl_xor_sync(0xffffffffu, give, o * STRIDE);
+                }
+            }
+        } else {
+            v[0] += __shfl_xor_sync(0xffffffffu, v[0], o * STRIDE);
+        }
+    }
+}
+
+// Layout of (channel, state) over a block of 128 threads: LPC lanes a channel,
+// SPL neighbouring states a lane.  Few states a lane give more threads, many
+// spare the work that every lane of a channel repeats (loads of dt and u, sums
+// across lanes).
+template <int SPL_, int LPC_>
+struct Layout {
+    static constexpr int SPL = SPL_, LPC = LPC_, NP = SPL_ * LPC_;   // NP: N rounded up
+    static constexpr int CH = 128 / LPC_;                            // channels of a block
+    static constexpr int TT = NP <= 64 ? 32 : (NP == 128 ? 16 : 8);  // tokens of a tile
+};
+
+inline int padded_states(int64_t N) {
+    int n = 8;
+    while (n < N) n *= 2;
+    return n;
+}
+
+// Calls f with the layout for N states.
+template <typename F>
+void with_layout(int64_t N, F f) {
+    switch (padded_states(N)) {
+        case 8: f(Layout<4, 2>{}); break;
+        case 16: f(Layout<4, 4>{}); break;
+        case 32: f(Layout<8, 4>{}); break;
+        case 64: f(Layout<8, 8>{}); break;
+        case 128: f(Layout<8, 16>{}); break;
+        default: f(Layout<8, 32>{}); break;
+    }
+}
+template <typename T> struct TypeOf { using type = T; };
+template <typename F>
+void with_elt(Elt t, F f) {
+    if (t == Elt::F32) f(TypeOf<float>{});
+    else f(TypeOf<__nv_bfloat16>{});
+}
+
+// The block's place: 128 / LPC channels of one group, one sequence.
+struct Place {
+    int64_t b, c0;      // sequence, first channel
+    int g, count;       // group, channels of the block that exist
+};
+template <int CH>
+__device__ __forceinline__ Place place_of(int64_t index, const SelectiveDims& d) {
+    const int64_t per = d.D / d.G, nb = (per + CH - 1) / CH;
+    Place p;
+    const int64_t k = index % nb, rest = index / nb;
+    p.g = (int)(rest % d.G);
+    p.b = rest / d.G;
+    p.c0 = p.g * per + k * CH;
+    const int64_t left = per - k * CH;
+    p.count = left < CH ? (int)left : CH;
+    return p;
+}
+template <int CH>
+int64_t channel_blocks(const SelectiveDims& d) {
+    return d.G * ((d.D / d.G + CH - 1) / CH);
+}
+
+// VW neighbouring channels of one token: `n` of them exist; vec: one aligned
+// load where all do.
+template <typename T, int VW>
+__device__ __forceinline__ Raw<T, VW> load_channels(const T* p, int n, bool vec) {
+    if (vec && n >= VW) return raw_load<T, VW>(p);
+    Raw<T, VW> r;
+#pragma unroll
+    for (int i = 0; i < VW; ++i) r.v[i] = i < n ? p[i] : from_f32<T>(0.f);
+    return r;
+}
+template <typename T, int VW>
+__device__ __forceinline__ void store_channels(T* p, const Raw<T, VW>& r, int n, bool vec) {
+    if (vec && n >= VW) {
+        raw_store<T, VW>(p, r);
+    } else {
+#pragma unroll
+        for (int i = 0; i < VW; ++i)
+            if (i < n) p[i] = r.v[i];
+    }
+}
+
+// Channels of one load: 16 bytes, or a block's channels where those are fewer.
+template <typename T, int CH>
+constexpr int load_width() {
+    return CH < (int)(16 / sizeof(T)) ? CH : (int)(16 / sizeof(T));
+}
+
+}  // namespace ssd

@@ -32,7 +32,9 @@ EXPORTED = ("ssd_status_string", "ssd_last_error_detail", "ssd_chunk_scan_fwd_wo
             "ssd_state_correction_workspace_size", "ssd_state_correction_fwd",
             "ssd_chunk_scan_fwd_flow_workspace_size", "ssd_chunk_scan_fwd_with_flow",
             "ssd_causal_conv_fwd", "ssd_causal_conv_bwd_workspace_size", "ssd_causal_conv_bwd",
-            "ssd_causal_conv_step", "ssd_bc_norm_rotate_fwd",
+            "ssd_causal_conv_step", "ssd_selective_scan_fwd_workspace_size",
+            "ssd_selective_scan_fwd", "ssd_selective_scan_bwd_workspace_size",
+            "ssd_selective_scan_bwd", "ssd_selective_step", "ssd_bc_norm_rotate_fwd",
             "ssd_bc_norm_rotate_bwd_workspace_size", "ssd_bc_norm_rotate_bwd")
 
 # ssd_chunk_scan_fwd_data_flow results
@@ -58,6 +60,16 @@ class ssd_stride_t(ctypes.Structure):
 class ssd_conv_dims_t(ctypes.Structure):
     _fields_ = [("batch", ctypes.c_int64), ("seqlen", ctypes.c_int64),
                 ("channels", ctypes.c_int64), ("width", ctypes.c_int64)]
+
+
+class ssd_selective_dims_t(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("seqlen", ctypes.c_int64),
+                ("channels", ctypes.c_int64), ("dstate", ctypes.c_int64),
+                ("ngroups", ctypes.c_int64)]
+
+
+class ssd_selective_strides_t(ctypes.Structure):
+    _fields_ = [(k, ssd_stride_t) for k in ("x", "dt", "B", "C", "z")]
 
 
 class ssd_rotate_dims_t(ctypes.Structure):
@@ -144,6 +156,14 @@ def load(path: str = LIB_PATH):
     _declare(lib, "ssd_causal_conv_bwd", _vp, stride_p, *[_vp] * 4, ci, _vp, ci, *[_vp] * 5, conv_p,
              ci, _vp, cs, _vp)
     _declare(lib, "ssd_causal_conv_step", _vp, _vp, stride_p, _vp, _vp, ci, _vp, conv_p, ci, _vp)
+    sel_p, sst_p = ctypes.POINTER(ssd_selective_dims_t), ctypes.POINTER(ssd_selective_strides_t)
+    for which in ("fwd", "bwd"):
+        _declare(lib, f"ssd_selective_scan_{which}_workspace_size", sel_p, ci, size_p)
+    _declare(lib, "ssd_selective_scan_fwd", *[_vp] * 8, ci, *[_vp] * 4, sst_p, sel_p, ci, _vp, cs,
+             _vp)
+    _declare(lib, "ssd_selective_scan_bwd", *[_vp] * 8, ci, *[_vp] * 13, sst_p, sel_p, ci, _vp, cs,
+             _vp)
+    _declare(lib, "ssd_selective_step", *[_vp] * 9, ci, _vp, sst_p, sel_p, ci, _vp)
     rot_p, rot = ctypes.POINTER(ssd_rotate_dims_t), [_vp, stride_p] * 2 + [_vp, _vp, ci, _vp, _vp,
                                                                            ctypes.c_float, ci]
     _declare(lib, "ssd_bc_norm_rotate_fwd", *rot, _vp, _vp, rot_p, ci, _vp)
@@ -711,8 +731,127 @@ def ssd_causal_conv_step(state, x, weight, bias=None, silu: bool = True, y=None,
             py = y.data_ptr()
         _check(load().ssd_causal_conv_step(ps, px, sx, pw, pb, int(silu), py,
                                            ssd_conv_dims_t(b, 1, D, W), code, st),
-               "ssd_causal_conv_step", "ssd_bc_norm_rotate_fwd",
-            "ssd_bc_norm_rotate_bwd_workspace_size", "ssd_bc_norm_rotate_bwd")
+               "ssd_causal_conv_step")
+    return y
+
+
+def _selective_args(x, dt, A, B, C, D, z, dt_bias, softplus, tokens=True):
+    """Checks the inputs that the selective scan's calls share; returns their C
+    arguments, strides, dims, device and dtype code."""
+    lead = 2 if tokens else 1
+    if x.dim() != lead + 1 or B.dim() != lead + 2 or A.dim() != 2:
+        raise ValueError("x must be (b, L, D), B (b, L, G, N) and A (D, N)" if tokens else
+                         "x must be (b, D), B (b, G, N) and A (D, N)")
+    shape, bc = tuple(x.shape), tuple(B.shape)
+    b, ch, G, N = shape[0], shape[-1], bc[-2], bc[-1]
+    L = shape[1] if tokens else 1
+    dev, T, f32 = x.device, x.dtype, torch.float32
+    code = _dtype_code(T)
+    bc = shape[:lead] + (G, N)
+    px, sx = _view("x", x, shape, T, dev, tokens)
+    pdt, sdt = _view("dt", dt, shape, T, dev, tokens)
+    pB, sB = _view("B", B, bc, T, dev, tokens)
+    pC, sC = _view("C", C, bc, T, dev, tokens)
+    pz, sz = _view("z", z, shape, T, dev, tokens)
+    args = (px, pdt, _dense("A", A, (ch, N), f32, dev), pB, pC, _dense("D", D, (ch,), f32, dev), pz,
+            _dense("dt_bias", dt_bias, (ch,), f32, dev), int(softplus))
+    return (args, ssd_selective_strides_t(sx, sdt, sB, sC, sz), ssd_selective_dims_t(b, L, ch, N, G),
+            dev, code)
+
+
+def ssd_selective_scan_fwd_workspace_size(dims: ssd_selective_dims_t, dtype: torch.dtype) -> int:
+    n = ctypes.c_size_t(0)
+    _check(load().ssd_selective_scan_fwd_workspace_size(dims, _dtype_code(dtype), n),
+           "ssd_selective_scan_fwd_workspace_size")
+    return int(n.value)
+
+
+def ssd_selective_scan_fwd(x, dt, A, B, C, D=None, z=None, dt_bias=None, softplus: bool = True,
+                           init_states=None, seq_lens=None, return_final_states: bool = False,
+                           y=None, final_states=None, workspace=None, stream=None):
+    """Selective scan with a decay per (channel, state): x, dt and the gate z
+    (b,L,D), B, C (b,L,G,N), all of one dtype and each possibly a view with
+    strided tokens; A (D,N), D and dt_bias (D) fp32.  dt is
+    softplus(dt + dt_bias), or dt + dt_bias without ``softplus``.  seq_lens (b,)
+    int32: the sequences' own lengths in a padded batch; rows of y behind them
+    are zero.  Returns y (b,L,D) [, final_states (b,D,N) fp32]."""
+    args, strides, dims, dev, code = _selective_args(x, dt, A, B, C, D, z, dt_bias, softplus)
+    b, L, ch = x.shape
+    N, T, f32 = A.shape[1], x.dtype, torch.float32
+    pi = _dense("init_states", init_states, (b, ch, N), f32, dev)
+    pl = _dense("seq_lens", seq_lens, (b,), torch.int32, dev)
+    py = _dense("y", y, (b, L, ch), T, dev)
+    pf = _dense("final_states", final_states, (b, ch, N), f32, dev)
+    with _scope(_device_of(x), stream) as st:
+        if y is None:
+            y = torch.empty((b, L, ch), device=dev, dtype=T)
+            py = y.data_ptr()
+        if return_final_states and final_states is None:
+            final_states = torch.empty((b, ch, N), device=dev, dtype=f32)
+            pf = final_states.data_ptr()
+        need = ssd_selective_scan_fwd_workspace_size(dims, T)
+        pws, nws = None, 0
+        if need or workspace is not None:
+            workspace, pws, nws = _workspace(workspace, need, dev)
+        _check(load().ssd_selective_scan_fwd(*args, pi, pl, py, pf, strides, dims, code, pws, nws,
+                                             st), "ssd_selective_scan_fwd")
+    return (y, final_states) if final_states is not None else y
+
+
+def ssd_selective_scan_bwd_workspace_size(dims: ssd_selective_dims_t, dtype: torch.dtype) -> int:
+    n = ctypes.c_size_t(0)
+    _check(load().ssd_selective_scan_bwd_workspace_size(dims, _dtype_code(dtype), n),
+           "ssd_selective_scan_bwd_workspace_size")
+    return int(n.value)
+
+
+def ssd_selective_scan_bwd(x, dt, A, B, C, D, dy, z=None, dt_bias=None, softplus: bool = True,
+                           init_states=None, dfinal_states=None, seq_lens=None,
+                           want_dinit: bool = True, workspace=None, stream=None):
+    """Gradients of ssd_selective_scan_fwd for dL/dy = dy (b,L,D; x's dtype) and
+    dL/dfinal_states ((b,D,N) fp32 or None).  Returns a dict: dx, ddt, dB, dC and
+    dz in x's dtype, dA, dD, ddt_bias and dinit fp32; None for an input that
+    was None (and for dinit without want_dinit)."""
+    args, strides, dims, dev, code = _selective_args(x, dt, A, B, C, D, z, dt_bias, softplus)
+    b, L, ch = x.shape
+    N, T, f32 = A.shape[1], x.dtype, torch.float32
+    pi = _dense("init_states", init_states, (b, ch, N), f32, dev)
+    pl = _dense("seq_lens", seq_lens, (b,), torch.int32, dev)
+    pdy = _dense("dy", dy, (b, L, ch), T, dev)
+    pdf = _dense("dfinal_states", dfinal_states, (b, ch, N), f32, dev)
+    with _scope(_device_of(x), stream) as st:
+        new = lambda shape, t, want=True: (torch.empty(shape, device=dev, dtype=t)    # noqa: E731
+                                           if want else None)
+        out = {"dx": new(x.shape, T), "ddt": new(x.shape, T), "dA": new(A.shape, f32),
+               "dB": new(B.shape, T), "dC": new(C.shape, T), "dD": new((ch,), f32, D is not None),
+               "dz": new(x.shape, T, z is not None),
+               "ddt_bias": new((ch,), f32, dt_bias is not None),
+               "dinit": new((b, ch, N), f32, want_dinit)}
+        workspace, pws, nws = _workspace(workspace,
+                                         ssd_selective_scan_bwd_workspace_size(dims, T), dev)
+        _check(load().ssd_selective_scan_bwd(*args, pi, pl, pdy, pdf,
+                                             *(None if v is None else v.data_ptr()
+                                               for v in out.values()),
+                                             strides, dims, code, pws, nws, st),
+               "ssd_selective_scan_bwd")
+    return out
+
+
+def ssd_selective_step(state, x, dt, A, B, C, D=None, z=None, dt_bias=None, softplus: bool = True,
+                       y=None, stream=None):
+    """One token: ``state`` (b,D,N) fp32 is updated in place; x, dt, z (b,D), B, C
+    (b,G,N).  Returns y (b,D)."""
+    args, strides, dims, dev, code = _selective_args(x, dt, A, B, C, D, z, dt_bias, softplus,
+                                                     tokens=False)
+    b, ch = x.shape
+    ps = _dense("state", state, (b, ch, A.shape[1]), torch.float32, dev)
+    py = _dense("y", y, (b, ch), x.dtype, dev)
+    with _scope(_device_of(x), stream) as st:
+        if y is None:
+            y = torch.empty((b, ch), device=dev, dtype=x.dtype)
+            py = y.data_ptr()
+        _check(load().ssd_selective_step(ps, *args, py, strides, dims, code, st),
+               "ssd_selective_step")
     return y
 
 
