@@ -61,11 +61,9 @@ ssd_status_t selective_dims(const ssd_selective_dims_t* dims, ssd_dtype_t dtype,
         return fail(SSD_ERR_INVALID_ARG, "channels (%lld) must be a multiple of ngroups (%lld)",
                     (long long)dims->channels, (long long)dims->ngroups);
     if (dims->dstate > 256) return fail(SSD_ERR_UNSUPPORTED, "dstate must be <= 256");
-    // at least one block of 128 threads for every four channels of a sequence, in
-    // the widest layout; 32-token pieces of a sequence run side by side at most
-    if ((double)dims->batch * (double)dims->channels * ((double)dims->seqlen / 32 + 1) >
-        (double)kMaxSize * 4)
-        return fail(SSD_ERR_UNSUPPORTED, "batch * channels * seqlen exceeds the launch grid");
+    // at most a block a channel and sequence
+    if ((double)dims->batch * (double)dims->channels > (double)kMaxSize)
+        return fail(SSD_ERR_UNSUPPORTED, "batch * channels exceeds the launch grid");
     *d = ssd::SelectiveDims{dims->batch, dims->seqlen, dims->channels, dims->dstate,
                             dims->ngroups};
     return check_dtype(dtype, t);

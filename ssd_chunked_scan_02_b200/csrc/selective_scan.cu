@@ -10,135 +10,372 @@
 // channel's states lie over a few lanes, the terms dt A and the exponentials
 // do not depend on the state and run ahead of it.
 //
-// A block takes tiles of 32 tokens: its threads first load the tile with wide
-// loads and put dt, dt x, B and C as fp32 into shared memory, then every lane
-// walks the tile, then the threads that loaded x and z finish y (skip, gate)
-// and write it.  The next tile's loads are in flight meanwhile.
+// A block has two kinds of warps.  Four carriers load a tile of 32 tokens with
+// wide loads, put dt, dt x, B and C as fp32 into shared memory, and finish y (skip, gate)
+// from the x and z that they still hold.  Four walkers do nothing but the
+// recurrence and the sum over states.  While the walkers are on one tile, the
+// carriers finish the one before and put down the one behind, with the loads
+// of the next in flight: one barrier a tile, and the exponential units are fed
+// while the rest of the work goes on beside them.
+//
+// Where batch and channels are too few blocks for the GPU, a sequence is cut
+// into spans (blockIdx.y).  A first launch walks all spans but the last from a
+// zero state and leaves the state S each one reaches and its sum of dt; the
+// decay over a span is exp(A sum dt), so the second launch finds the state that
+// enters span s by h <- exp(A sum dt_k) h + S_k over the spans k before it, and
+// walks it for y.  That doubles the exponentials.
 #include "selective.cuh"
 
 namespace ssd {
 namespace {
 
-constexpr int kThreads = 128;
+constexpr int kWalkers = 128;      // threads of the walking warps
+
+// A span's result: state (b, spans - 1, D, NP), then sums of dt log2(e)
+// (b, spans - 1, D).
+struct Spans {
+    int count;            // spans of a sequence
+    int64_t tokens;       // tokens of a span, a multiple of the tile
+    float *state, *sum;
+};
 
 template <typename T, typename Lay>
-__global__ void __launch_bounds__(kThreads)
+struct Fwd {
+    static constexpr int TT = Lay::TT, CH = Lay::CH, NP = Lay::NP;
+    static constexpr int PY = CH + 8;                               // s_y's row: no bank twice
+    static constexpr int KC = 128;                                  // threads of the carriers
+    static constexpr int THREADS = kWalkers + KC;
+    static constexpr int VW = load_width<T, CH>();
+    static constexpr int NI = (TT * CH / VW + KC - 1) / KC;               // loads a thread and tile
+    static constexpr int VB = 16 / sizeof(T);
+    static constexpr int NB = (TT * NP * 2 / VB + KC - 1) / KC;
+    static constexpr int RAW = KC * (3 * NI * VW + NB * VB) * (int)sizeof(T);   // a tile as it comes
+    static constexpr int SMEM = 4 * RAW + 2 * (TT * CH * 8 + TT * PY * 4 + TT * NP * 8) + 2 * CH * 4;
+    static constexpr int BLOCKS = SMEM <= 75 * 1024 ? 3 : 2;   // of an SM
+};
+
+// Output: y and the final states; else the span's state from zero.  Vec: x, dt and z
+// can be loaded VW channels, B and C VB states at a time.  The next tile's loads are then free of
+// branches (rows and channels that do not exist read ones that do, and are
+// replaced by zeros when the tile is staged), because the join behind a branch
+// would wait for them.
+template <typename T, typename Lay, bool Output, bool Vec>
+__global__ void __launch_bounds__((Fwd<T, Lay>::THREADS), (Fwd<T, Lay>::BLOCKS))
 scan_fwd_kernel(const SelectiveArgs a, T* __restrict__ y, float* __restrict__ final_states,
-                const SelectiveDims d, bool vec) {
+                const Spans sp, const SelectiveDims d) {
+    using F = Fwd<T, Lay>;
     constexpr int SPL = Lay::SPL, LPC = Lay::LPC, NP = Lay::NP, CH = Lay::CH, TT = Lay::TT;
-    constexpr int VW = load_width<T, CH>();
-    constexpr int NI = (TT * CH / VW + kThreads - 1) / kThreads;    // loads a thread and tile
+    constexpr int VW = F::VW, NI = F::NI, VB = F::VB, NB = F::NB, PY = F::PY, KC = F::KC;
     constexpr int TG = LPC < 8 ? LPC : 8;                           // tokens summed at once
-    __shared__ float2 s_du[TT][CH];                                 // dt, dt x
-    __shared__ float s_y[TT][CH];
-    __shared__ __align__(16) float s_B[TT][NP], s_C[TT][NP];
+    // s_du's columns are permuted by the number of the load that brings them, so
+    // that neither the eight lanes that store side by side nor those that read
+    // meet a bank twice
+    constexpr int SWZ = (CH < 8 ? CH : 8) - 1, PER = CH / VW;       // PER: loads of a token
+    static_assert(8 * PER % (SWZ + 1) == 0, "the permutation repeats after eight tokens");
+    extern __shared__ __align__(16) unsigned char smem[];
+    using RV = Raw<T, VW>;
+    using RB = Raw<T, VB>;
+    // four tiles as they come: every carrier copies and reads its own elements
+    RB* r_bc = reinterpret_cast<RB*>(smem);                         // [4][NB][KC]
+    RV* r_x = reinterpret_cast<RV*>(r_bc + 4 * NB * KC);            // [4][NI][KC] each
+    RV* r_dt = r_x + 4 * NI * KC;
+    RV* r_z = r_dt + 4 * NI * KC;
+    float2* s_du = reinterpret_cast<float2*>(r_z + 4 * NI * KC);    // [2][TT][CH]: dt, u
+    float* s_B = reinterpret_cast<float*>(s_du + 2 * TT * CH);      // [2][TT][NP]
+    float* s_C = s_B + 2 * TT * NP;
+    float* s_y = s_C + 2 * TT * NP;                                 // [2][TT][PY]
+    float* s_bias = s_y + 2 * TT * PY;                              // [CH] each
+    float* s_skip = s_bias + CH;
 
     const Place pl = place_of<CH>(blockIdx.x, d);
-    const int tid = threadIdx.x, lane = tid % LPC, ch = tid / LPC;
-    const int64_t len = own_length(a.lens, pl.b, d.L);
+    const bool walker = threadIdx.x < kWalkers;
+    const int tid = walker ? threadIdx.x : threadIdx.x - kWalkers;
+    const int64_t own = own_length(a.lens, pl.b, d.L);
+    const int span = blockIdx.y;
+    const int64_t first = span * sp.tokens;
+    const int64_t last = span + 1 == sp.count ? d.L : first + sp.tokens;
+    const int64_t len = own < last ? own : last;                    // rows read: [first, len)
+    const int rows = (int)(last - first);                           // of y
     const T* x = static_cast<const T*>(a.x) + pl.b * a.xs.batch + pl.c0;
     const T* dt = static_cast<const T*>(a.dt) + pl.b * a.dts.batch + pl.c0;
-    const T* z = a.z ? static_cast<const T*>(a.z) + pl.b * a.zs.batch + pl.c0 : nullptr;
+    const T* z = Output && a.z ? static_cast<const T*>(a.z) + pl.b * a.zs.batch + pl.c0 : nullptr;
     const T* Bp = static_cast<const T*>(a.B) + pl.b * a.Bs.batch + pl.g * d.N;
     const T* Cp = static_cast<const T*>(a.C) + pl.b * a.Cs.batch + pl.g * d.N;
-    y += pl.b * d.L * d.D + pl.c0;
+    if (Output) y += pl.b * d.L * d.D + pl.c0;
 
-    float A2[SPL], h[SPL];
-    const int64_t row = pl.b * d.D + pl.c0 + ch;
-#pragma unroll
-    for (int i = 0; i < SPL; ++i) {
-        const int n = lane * SPL + i;
-        const bool on = ch < pl.count && n < d.N;
-        A2[i] = on ? a.A[(pl.c0 + ch) * d.N + n] * kLog2E : 0.f;
-        h[i] = on && a.init ? a.init[row * d.N + n] : 0.f;
+    for (int i = threadIdx.x; i < 4 * TT * NP; i += F::THREADS) s_B[i] = 0.f;   // states beyond N
+    for (int c = threadIdx.x; c < CH; c += F::THREADS) {
+        s_bias[c] = a.dt_bias && c < pl.count ? a.dt_bias[pl.c0 + c] : 0.f;
+        s_skip[c] = Output && a.D && c < pl.count ? a.D[pl.c0 + c] : 0.f;
     }
+    __syncthreads();
 
-    Raw<T, VW> rx[NI], rdt[NI], rz[NI], nx[NI], ndt[NI], nz[NI];
-    auto load = [&](int64_t t0, Raw<T, VW>* px, Raw<T, VW>* pdt, Raw<T, VW>* pz) {
+    if (walker) {
+        const int lane = tid % LPC, ch = tid / LPC;
+        F2 A[SPL / 2], h[SPL / 2];
+        const int64_t row = pl.b * d.D + pl.c0 + ch;
+        {
+            float av[SPL], hv[SPL];
 #pragma unroll
-        for (int k = 0; k < NI; ++k) {
-            const int i = k * kThreads + tid, t = i / (CH / VW), c = i % (CH / VW) * VW;
-            const int n = t < TT && t0 + t < len ? pl.count - c : 0;
-            px[k] = load_channels<T, VW>(x + (t0 + t) * a.xs.token + c, n, vec);
-            pdt[k] = load_channels<T, VW>(dt + (t0 + t) * a.dts.token + c, n, vec);
-            if (z) pz[k] = load_channels<T, VW>(z + (t0 + t) * a.zs.token + c, n, vec);
-        }
-    };
-    load(0, rx, rdt, rz);
-
-    for (int64_t t0 = 0; t0 < d.L; t0 += TT) {
-        // the tile into shared memory; rows behind the sequence: dt = 0, no input
+            for (int i = 0; i < SPL; ++i) {
+                const int n = lane * SPL + i;
+                const bool on = ch < pl.count && n < d.N;
+                av[i] = on ? a.A[(pl.c0 + ch) * d.N + n] : 0.f;
+                hv[i] = on && Output && a.init ? a.init[row * d.N + n] : 0.f;
+            }
+            if (Output && ch < pl.count) {
+                for (int k = 0; k < span; ++k) {                        // the spans before this one
+                    const int64_t at = (pl.b * (sp.count - 1) + k) * d.D + pl.c0 + ch;
+                    const float sum = sp.sum[at];
+                    const float* S = sp.state + at * NP + lane * SPL;
 #pragma unroll
-        for (int k = 0; k < NI; ++k) {
-            const int i = k * kThreads + tid, t = i / (CH / VW), c = i % (CH / VW) * VW;
-            if (t < TT) {
-#pragma unroll
-                for (int j = 0; j < VW; ++j) {
-                    float v = 0.f;
-                    if (t0 + t < len && c + j < pl.count) {
-                        v = to_f32(rdt[k].v[j]) + (a.dt_bias ? a.dt_bias[pl.c0 + c + j] : 0.f);
-                        if (a.softplus) v = softplus_f32(v);
-                    }
-                    s_du[t][c + j] = make_float2(v, v * to_f32(rx[k].v[j]));
+                    for (int i = 0; i < SPL; ++i) hv[i] = fmaf(ex2(sum * av[i]), hv[i], S[i]);
                 }
             }
+#pragma unroll
+            for (int i = 0; i < SPL / 2; ++i) {
+                A[i] = pack2(av[2 * i], av[2 * i + 1]);
+                h[i] = pack2(hv[2 * i], hv[2 * i + 1]);
+            }
         }
-        for (int i = tid; i < TT * NP; i += kThreads) {
-            const int t = i / NP, n = i % NP;
-            const bool on = n < d.N && t0 + t < len;
-            s_B[t][n] = on ? to_f32(Bp[(t0 + t) * a.Bs.token + n]) : 0.f;
-            s_C[t][n] = on ? to_f32(Cp[(t0 + t) * a.Cs.token + n]) : 0.f;
-        }
-        __syncthreads();
-        if (t0 + TT < d.L) load(t0 + TT, nx, ndt, nz);
-
+        auto walk = [&](int w) {
+            const float2* du = s_du + w * TT * CH;
+            const float* Bt = s_B + w * TT * NP + lane * SPL;
+            const float* Ct = s_C + w * TT * NP + lane * SPL;
 #pragma unroll 1
-        for (int tt = 0; tt < TT; tt += TG) {
-            float ys[TG];
+            for (int tt = 0; tt < TT; tt += 8) {
+                float ys[TG];
 #pragma unroll
-            for (int k = 0; k < TG; ++k) {
-                const float2 du = s_du[tt + k][ch];
-                ys[k] = 0.f;
+                for (int k = 0; k < 8; ++k) {
+                    const float2 q = du[(tt + k) * CH + (ch ^ ((k * PER + ch / VW) & SWZ))];
+                    const F2 dd = pack2(q.x, q.x), uu = pack2(q.y, q.y);
+                    F2 yy = 0;
 #pragma unroll
-                for (int i = 0; i < SPL; ++i) {
-                    const float e = ex2(du.x * A2[i]);
-                    h[i] = fmaf(e, h[i], du.y * s_B[tt + k][lane * SPL + i]);
-                    ys[k] = fmaf(s_C[tt + k][lane * SPL + i], h[i], ys[k]);
-                }
-            }
-            fold<TG, LPC>(ys, lane);
-            if (lane % (LPC / TG) == 0) s_y[tt + lane / (LPC / TG)][ch] = ys[0];
-        }
-        __syncthreads();
-
-#pragma unroll
-        for (int k = 0; k < NI; ++k) {
-            const int i = k * kThreads + tid, t = i / (CH / VW), c = i % (CH / VW) * VW;
-            if (t < TT && t0 + t < d.L) {
-                float o[VW];
-#pragma unroll
-                for (int j = 0; j < VW; ++j) {
-                    o[j] = 0.f;
-                    if (t0 + t < len && c + j < pl.count) {
-                        const float Dv = a.D ? a.D[pl.c0 + c + j] : 0.f;
-                        o[j] = fmaf(Dv, to_f32(rx[k].v[j]), s_y[t][c + j]);
-                        if (z) {
-                            const float zv = to_f32(rz[k].v[j]);
-                            o[j] *= zv * sigmoid_f32(zv);
+                    for (int i = 0; i < SPL; i += 4) {
+                        const float4 bv = *reinterpret_cast<const float4*>(Bt + (tt + k) * NP + i);
+                        const F2 e0 = ex2_2(mul2(dd, A[i / 2])), e1 = ex2_2(mul2(dd, A[i / 2 + 1]));
+                        h[i / 2] = fma2(e0, h[i / 2], mul2(uu, pack2(bv.x, bv.y)));
+                        h[i / 2 + 1] = fma2(e1, h[i / 2 + 1], mul2(uu, pack2(bv.z, bv.w)));
+                        if (Output) {
+                            const float4 cv = *reinterpret_cast<const float4*>(Ct + (tt + k) * NP + i);
+                            yy = i == 0 ? mul2(pack2(cv.x, cv.y), h[0])
+                                        : fma2(pack2(cv.x, cv.y), h[i / 2], yy);
+                            yy = fma2(pack2(cv.z, cv.w), h[i / 2 + 1], yy);
                         }
                     }
+                    const float2 f = unpack2(yy);
+                    ys[k % TG] = f.x + f.y;
+                    if (Output && k % TG == TG - 1) {
+                        fold<TG, LPC>(ys, lane);
+                        if (lane % (LPC / TG) == 0)
+                            s_y[(w * TT + tt + k + 1 - TG + lane / (LPC / TG)) * PY + ch] = ys[0];
+                    }
                 }
-                store_channels<T, VW>(y + (t0 + t) * d.D + c, raw_from_f32<T, VW>(o),
-                                      pl.count - c, vec);
             }
-            rx[k] = nx[k]; rdt[k] = ndt[k];
-            if (z) rz[k] = nz[k];
+        };
+        __syncthreads();                                             // the first tile is down
+        for (int at = 0; at < rows; at += 2 * TT) {
+            walk(0);
+            __syncthreads();
+            if (at + TT < rows) {
+                walk(1);
+                __syncthreads();
+            }
+        }
+        float hv[SPL];
+#pragma unroll
+        for (int i = 0; i < SPL / 2; ++i) {
+            const float2 f = unpack2(h[i]);
+            hv[2 * i] = f.x;
+            hv[2 * i + 1] = f.y;
+        }
+        if (Output) {
+            if (final_states && span + 1 == sp.count && ch < pl.count) {
+#pragma unroll
+                for (int i = 0; i < SPL; ++i)
+                    if (lane * SPL + i < d.N) final_states[row * d.N + lane * SPL + i] = hv[i];
+            }
+        } else {
+            const int64_t at = (pl.b * (sp.count - 1) + span) * d.D + pl.c0;
+            if (ch < pl.count) {
+#pragma unroll
+                for (int i = 0; i < SPL; ++i) sp.state[(at + ch) * NP + lane * SPL + i] = hv[i];
+            }
+        }
+    } else {
+        // where this thread's loads of a tile come from and go to; positions `at`
+        // of a tile are tokens from the span's first on
+        const int own_rows = (int)(len - first > 0 ? len - first : 0);
+        const T *px[NI], *pdt[NI], *pz[NI], *pbc[NB];
+        int bc_token[NB], bc_to[NB];
+        bool is_b[NB];
+#pragma unroll
+        for (int k = 0; k < NI; ++k) {
+            const int i = k * KC + tid, t = i / PER, c = i % PER * VW < pl.count ? i % PER * VW : 0;
+            px[k] = x + (first + t) * a.xs.token + c;
+            pdt[k] = dt + (first + t) * a.dts.token + c;
+            pz[k] = z ? z + (first + t) * a.zs.token + c : px[k];
+        }
+        const int nvb = Vec ? (int)d.N / VB : 1;
+#pragma unroll
+        for (int k = 0; k < NB; ++k) {
+            const int i = k * KC + tid, t = i / (2 * nvb), v = i % (2 * nvb);
+            is_b[k] = v < nvb;
+            bc_token[k] = t;
+            bc_to[k] = (is_b[k] ? v * VB : 2 * TT * NP + (v - nvb) * VB) + t * NP;
+            pbc[k] = is_b[k] ? Bp + (first + t) * a.Bs.token + v * VB
+                             : Cp + (first + t) * a.Cs.token + (v - nvb) * VB;
+        }
+        const int64_t x_step = TT * a.xs.token, dt_step = TT * a.dts.token,
+                      z_step = TT * (z ? a.zs.token : a.xs.token);
+        auto load = [&](int at) {                                   // into ring place at / TT % 4
+            const int ring = at / TT & 3;
+            if (at < own_rows) {
+#pragma unroll
+                for (int k = 0; k < NI; ++k) {
+                    const int i = k * KC + tid, t = i / PER, c = i % PER * VW, o = (ring * NI + k) * KC + tid;
+                    if constexpr (Vec) {
+                        const bool in = t < TT && at + t < own_rows && c < pl.count;
+                        copy_async(r_x + o, px[k], in);
+                        copy_async(r_dt + o, pdt[k], in);
+                        if (z) copy_async(r_z + o, pz[k], in);
+                    } else {
+                        const int n = t < TT && at + t < own_rows ? pl.count - c : 0;
+                        r_x[o] = load_channels<T, VW>(px[k], n, false);
+                        r_dt[o] = load_channels<T, VW>(pdt[k], n, false);
+                        if (z) r_z[o] = load_channels<T, VW>(pz[k], n, false);
+                    }
+                    px[k] += x_step;
+                    pdt[k] += dt_step;
+                    pz[k] += z_step;
+                }
+                if constexpr (Vec) {
+#pragma unroll
+                    for (int k = 0; k < NB; ++k) {
+                        copy_async(r_bc + (ring * NB + k) * KC + tid, pbc[k],
+                                   bc_token[k] < TT && at + bc_token[k] < own_rows);
+                        pbc[k] += TT * (is_b[k] ? a.Bs.token : a.Cs.token);
+                    }
+                }
+            }
+            if constexpr (Vec) copies_commit();
+        };
+        float sum_dt[NI][VW];
+#pragma unroll
+        for (int k = 0; k < NI; ++k)
+#pragma unroll
+            for (int j = 0; j < VW; ++j) sum_dt[k][j] = 0.f;
+        // the loaded tile into buffer w; rows behind the sequence: dt = 0, no input
+        auto stage = [&](int at, int w) {
+            float2* du = s_du + w * TT * CH;
+            const int ring = at / TT & 3;
+            if constexpr (Vec) copies_pending<1>();                 // the tile behind may be under way
+#pragma unroll
+            for (int k = 0; k < NI; ++k) {
+                const int i = k * KC + tid, t = i / PER, c = i % PER * VW, o = (ring * NI + k) * KC + tid;
+                if (t < TT) {
+                    const int n = at + t < own_rows ? pl.count - c : 0;
+                    const RV rx = r_x[o], rdt = r_dt[o];
+#pragma unroll
+                    for (int j = 0; j < VW; ++j) {
+                        float v = to_f32(rdt.v[j]) + s_bias[c + j];
+                        if (a.softplus) v = softplus_f32(v);
+                        float u = v * to_f32(rx.v[j]);
+                        if (j >= n) v = u = 0.f;
+                        v *= kLog2E;                      // the decays are powers of two
+                        if (!Output) sum_dt[k][j] += v;
+                        du[t * CH + ((c + j) ^ (i & SWZ))] = make_float2(v, u);
+                    }
+                }
+            }
+            if constexpr (Vec) {
+#pragma unroll
+                for (int k = 0; k < NB; ++k) {
+                    if (bc_token[k] < TT) {
+                        float f[VB];
+                        raw_to_f32(at + bc_token[k] < own_rows ? r_bc[(ring * NB + k) * KC + tid]
+                                                               : raw_zero<T, VB>(), f);
+                        float* q = s_B + w * TT * NP + bc_to[k];
+#pragma unroll
+                        for (int j = 0; j < VB; j += 4)
+                            *reinterpret_cast<float4*>(q + j) = make_float4(f[j], f[j + 1], f[j + 2], f[j + 3]);
+                    }
+                }
+            } else {
+                for (int i = tid; i < TT * NP; i += KC) {
+                    const int t = i / NP, n = i % NP;
+                    const bool on = n < d.N && at + t < own_rows;
+                    s_B[w * TT * NP + i] = on ? to_f32(Bp[(first + at + t) * a.Bs.token + n]) : 0.f;
+                    if (Output)
+                        s_C[w * TT * NP + i] = on ? to_f32(Cp[(first + at + t) * a.Cs.token + n]) : 0.f;
+                }
+            }
+        };
+        T* py = y + first * d.D;
+        auto finish = [&](int at, int w) {
+#pragma unroll
+            for (int k = 0; k < NI; ++k) {
+                const int i = k * KC + tid, t = i / PER, c = i % PER * VW;
+                if (t < TT && at + t < rows) {
+                    const int n = at + t < own_rows ? pl.count - c : 0;
+                    const int q = ((at / TT & 3) * NI + k) * KC + tid;
+                    const RV kx = r_x[q];
+                    RV kz;
+                    if (z) kz = r_z[q];
+                    float o[VW];
+#pragma unroll
+                    for (int j = 0; j < VW; ++j) {
+                        o[j] = fmaf(s_skip[c + j], to_f32(kx.v[j]), s_y[(w * TT + t) * PY + c + j]);
+                        if (z) {
+                            const float zv = to_f32(kz.v[j]);
+                            o[j] *= zv * sigmoid_fast(zv);
+                        }
+                        if (j >= n) o[j] = 0.f;
+                    }
+                    store_channels<T, VW>(py + (int64_t)(at + t) * d.D + c, raw_from_f32<T, VW>(o),
+                                          pl.count - c, Vec);
+                }
+            }
+        };
+
+        load(0);
+        load(TT);
+        if (rows > 0) stage(0, 0);
+        load(2 * TT);
+        __syncthreads();                                             // the first tile is down
+        auto tile = [&](int at, int w) {
+            if (Output && at > 0) finish(at - TT, w ^ 1);
+            if (at + TT < rows) {
+                stage(at + TT, w ^ 1);
+                load(at + 3 * TT);
+            }
+            __syncthreads();
+            if (Output && at + TT >= rows) finish(at, w);
+        };
+        for (int at = 0; at < rows; at += 2 * TT) {
+            tile(at, 0);
+            if (at + TT < rows) tile(at + TT, 1);
+        }
+        if (!Output) {
+#pragma unroll
+            for (int k = 0; k < NI; ++k) {
+                const int i = k * KC + tid, t = i / PER, c = i % PER * VW;
+                if (t < TT) {
+#pragma unroll
+                    for (int j = 0; j < VW; ++j) s_y[t * PY + c + j] = sum_dt[k][j];
+                }
+            }
         }
     }
-    if (final_states && ch < pl.count) {
-#pragma unroll
-        for (int i = 0; i < SPL; ++i)
-            if (lane * SPL + i < d.N) final_states[row * d.N + lane * SPL + i] = h[i];
+    if (!Output) {
+        // sums of dt: the threads of a channel, in order
+        __syncthreads();
+        const int64_t at = (pl.b * (sp.count - 1) + span) * d.D + pl.c0;
+        for (int c = threadIdx.x; c < pl.count; c += F::THREADS) {
+            float v = 0.f;
+            for (int t = 0; t < TT; ++t) v += s_y[t * PY + c];
+            sp.sum[at + c] = v;
+        }
     }
 }
 
@@ -191,7 +428,7 @@ step_kernel(float* __restrict__ state, const SelectiveArgs a, T* __restrict__ y,
             }
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                hs[i] = fmaf(ex2(v * (As[i] * kLog2E)), hs[i], u * Bs[i]);
+                hs[i] = fmaf(ex2(v * kLog2E * As[i]), hs[i], u * Bs[i]);
                 acc = fmaf(Cs[i], hs[i], acc);
             }
             if constexpr (Vec) {
@@ -232,21 +469,62 @@ bool selective_vec(const SelectiveArgs& a, const SelectiveDims& d, int w) {
 template bool selective_vec<float>(const SelectiveArgs&, const SelectiveDims&, int);
 template bool selective_vec<__nv_bfloat16>(const SelectiveArgs&, const SelectiveDims&, int);
 
-size_t selective_fwd_workspace_bytes(const SelectiveDims&) { return 0; }
+// Spans of a sequence: one where the blocks of (batch, channels) fill half of
+// what 148 SMs hold (four blocks each); else as many as fill it, of at least 8
+// tiles.
+Spans spans_of(const SelectiveDims& d, float* ws) {
+    Spans sp{1, d.L, nullptr, nullptr};
+    with_layout(d.N, [&](auto lay) {
+        using Lay = decltype(lay);
+        const int64_t blocks = d.b * channel_blocks<Lay::CH>(d), tiles = (d.L + Lay::TT - 1) / Lay::TT;
+        if (blocks == 0 || blocks >= 148 * 2) return;
+        int64_t want = 148 * 4 / blocks;
+        if (want > tiles / 8) want = tiles / 8;
+        if (want < 3) return;                       // two spans cost what they gain
+        const int64_t per = (tiles + want - 1) / want;
+        sp.tokens = per * Lay::TT;
+        sp.count = (int)((tiles + per - 1) / per);
+        sp.state = ws;
+        sp.sum = ws + d.b * (sp.count - 1) * d.D * Lay::NP;
+    });
+    return sp;
+}
 
-cudaError_t launch_selective_fwd(const SelectiveArgs& a, void* y, float* final_states, float*,
+size_t selective_fwd_workspace_bytes(const SelectiveDims& d) {
+    const Spans sp = spans_of(d, nullptr);
+    return (size_t)(d.b * (sp.count - 1) * d.D * (padded_states(d.N) + 1)) * 4;
+}
+
+cudaError_t launch_selective_fwd(const SelectiveArgs& a, void* y, float* final_states, float* ws,
                                  const SelectiveDims& d, Elt t, cudaStream_t s) {
+    const Spans sp = spans_of(d, ws);
+    cudaError_t err = cudaSuccess;
     with_elt(t, [&](auto ty) {
         using T = typename decltype(ty)::type;
         with_layout(d.N, [&](auto lay) {
             using Lay = decltype(lay);
-            const int64_t blocks = d.b * channel_blocks<Lay::CH>(d);
-            scan_fwd_kernel<T, Lay><<<(unsigned)blocks, kThreads, 0, s>>>(
-                a, static_cast<T*>(y), final_states, d,
-                selective_vec<T>(a, d, load_width<T, Lay::CH>()));
+            using F = Fwd<T, Lay>;
+            const unsigned blocks = (unsigned)(d.b * channel_blocks<Lay::CH>(d));
+            const bool vec = selective_vec<T>(a, d, F::VW) && d.N % F::VB == 0 &&
+                             rows_fit<T>(a.B, a.Bs, F::VB) && rows_fit<T>(a.C, a.Cs, F::VB);
+            auto go = [&](auto kernel, unsigned spans) {
+                err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                           F::SMEM);
+                if (err == cudaSuccess)
+                    kernel<<<dim3(blocks, spans), F::THREADS, F::SMEM, s>>>(
+                        a, static_cast<T*>(y), final_states, sp, d);
+            };
+            auto both = [&](auto state_only, auto whole) {
+                if (sp.count > 1) go(state_only, (unsigned)sp.count - 1);
+                if (err == cudaSuccess) go(whole, (unsigned)sp.count);
+            };
+            if (vec)
+                both(scan_fwd_kernel<T, Lay, false, true>, scan_fwd_kernel<T, Lay, true, true>);
+            else
+                both(scan_fwd_kernel<T, Lay, false, false>, scan_fwd_kernel<T, Lay, true, false>);
         });
     });
-    return cudaGetLastError();
+    return err != cudaSuccess ? err : cudaGetLastError();
 }
 
 cudaError_t launch_selective_step(float* state, const SelectiveArgs& a, void* y,

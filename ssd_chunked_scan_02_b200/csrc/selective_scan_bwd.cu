@@ -30,6 +30,7 @@ bool selective_vec(const SelectiveArgs& a, const SelectiveDims& d, int w);
 
 namespace {
 
+constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kThreads = 128, kWarps = kThreads / 32;
 
 template <typename Lay>
@@ -61,12 +62,12 @@ checkpoint_kernel(const SelectiveArgs a, float* __restrict__ ckpt, const Selecti
     const T* x = static_cast<const T*>(a.x) + pl.b * a.xs.batch + pl.c0;
     const T* dt = static_cast<const T*>(a.dt) + pl.b * a.dts.batch + pl.c0;
     const T* Bp = static_cast<const T*>(a.B) + pl.b * a.Bs.batch + pl.g * d.N;
-    float A2[SPL], h[SPL];
+    float A[SPL], h[SPL];
 #pragma unroll
     for (int i = 0; i < SPL; ++i) {
         const int n = lane * SPL + i;
         const bool on = ch < pl.count && n < d.N;
-        A2[i] = on ? a.A[(pl.c0 + ch) * d.N + n] * kLog2E : 0.f;
+        A[i] = on ? a.A[(pl.c0 + ch) * d.N + n] : 0.f;
         h[i] = on && a.init ? a.init[(pl.b * d.D + pl.c0 + ch) * d.N + n] : 0.f;
     }
     for (int64_t t0 = 0; t0 < d.L; t0 += TT) {
@@ -79,7 +80,7 @@ checkpoint_kernel(const SelectiveArgs a, float* __restrict__ ckpt, const Selecti
 #pragma unroll
             for (int j = 0; j < VW; ++j) {
                 const float v = j < n ? step_of(rdt.v[j], a, pl.c0 + c + j) : 0.f;
-                s_du[t][c + j] = make_float2(v, v * to_f32(rx.v[j]));
+                s_du[t][c + j] = make_float2(v * kLog2E, v * to_f32(rx.v[j]));
             }
         }
         for (int i = tid; i < TT * NP; i += kThreads) {
@@ -101,7 +102,7 @@ checkpoint_kernel(const SelectiveArgs a, float* __restrict__ ckpt, const Selecti
                 const float2 du = s_du[tt + k][ch];
 #pragma unroll
                 for (int i = 0; i < SPL; ++i)
-                    h[i] = fmaf(ex2(du.x * A2[i]), h[i], du.y * s_B[tt + k][lane * SPL + i]);
+                    h[i] = fmaf(ex2(du.x * A[i]), h[i], du.y * s_B[tt + k][lane * SPL + i]);
             }
         }
     }
@@ -118,7 +119,7 @@ scan_bwd_kernel(const SelectiveArgs a, const SelectiveGrads gr, const float* __r
     constexpr int CPW = 32 / LPC;                               // channels of a warp
     constexpr int IT = (TT * CH / VW + kThreads - 1) / kThreads;
     extern __shared__ __align__(16) float smem[];
-    float* s_dt = smem;                                         // [TT][CH] each
+    float* s_dt = smem;                                         // [TT][CH] each; dt log2(e)
     float* s_u = s_dt + TT * CH;
     float* s_g = s_u + TT * CH;
     float* s_y = s_g + TT * CH;
@@ -143,13 +144,13 @@ scan_bwd_kernel(const SelectiveArgs a, const SelectiveGrads gr, const float* __r
     T* dz = z ? static_cast<T*>(gr.dz) + dense : nullptr;
     const int64_t cb = blockIdx.x % (gridDim.x / d.b);          // channel block over all groups
 
-    float A2[SPL], g[SPL], dA[SPL];
+    float A[SPL], g[SPL], dA[SPL];
     const int64_t row = pl.b * d.D + pl.c0 + ch;
 #pragma unroll
     for (int i = 0; i < SPL; ++i) {
         const int n = lane * SPL + i;
         const bool on = ch < pl.count && n < d.N;
-        A2[i] = on ? a.A[(pl.c0 + ch) * d.N + n] * kLog2E : 0.f;
+        A[i] = on ? a.A[(pl.c0 + ch) * d.N + n] : 0.f;
         g[i] = on && gr.dfinal ? gr.dfinal[row * d.N + n] : 0.f;
         dA[i] = 0.f;
     }
@@ -180,7 +181,7 @@ scan_bwd_kernel(const SelectiveArgs a, const SelectiveGrads gr, const float* __r
                     const float zv = to_f32(rz[k].v[j]);
                     gy *= zv * sigmoid_f32(zv);
                 }
-                s_dt[t * CH + c + j] = v;
+                s_dt[t * CH + c + j] = v * kLog2E;
                 s_u[t * CH + c + j] = v * to_f32(rx[k].v[j]);
                 s_g[t * CH + c + j] = gy;
             }
@@ -212,7 +213,7 @@ scan_bwd_kernel(const SelectiveArgs a, const SelectiveGrads gr, const float* __r
                 const float v = s_dt[(tt + k) * CH + ch], u = s_u[(tt + k) * CH + ch];
 #pragma unroll
                 for (int i = 0; i < SPL; ++i) {
-                    e[k][i] = ex2(v * A2[i]);
+                    e[k][i] = ex2(v * A[i]);
                     eh[k][i] = e[k][i] * h[i];
                     h[i] = fmaf(u, s_B[(tt + k) * NP + lane * SPL + i], eh[k][i]);
                 }
@@ -236,7 +237,7 @@ scan_bwd_kernel(const SelectiveArgs a, const SelectiveGrads gr, const float* __r
                     pu[k] = fmaf(Bv, g[i], pu[k]);
                     pB[k * SPL + i] = u * g[i];
                     const float qv = g[i] * eh[k][i];
-                    pq[k] = fmaf(A2[i], qv, pq[k]);
+                    pq[k] = fmaf(A[i], qv, pq[k]);
                     at[i] = fmaf(v, qv, at[i]);
                     g[i] *= e[k][i];
                 }
@@ -254,7 +255,7 @@ scan_bwd_kernel(const SelectiveArgs a, const SelectiveGrads gr, const float* __r
                     const int t = tt + lane / SH * NT + i;
                     s_y[t * CH + ch] = py[i];
                     s_du[t * CH + ch] = pu[i];
-                    s_q[t * CH + ch] = pq[i] * 0.6931471805599453f;      // A2 = A log2(e)
+                    s_q[t * CH + ch] = pq[i];
                 }
             }
             // over a warp's channels: the lanes of one place in the channel differ by LPC
@@ -291,7 +292,7 @@ scan_bwd_kernel(const SelectiveArgs a, const SelectiveGrads gr, const float* __r
                 const int q = t * CH + c + j;
                 const float xv = to_f32(rx[k].v[j]), gy = s_g[q], du = s_du[q];
                 const float Dv = a.D ? a.D[pl.c0 + c + j] : 0.f;
-                ox[j] = fmaf(s_dt[q], du, Dv * gy);
+                ox[j] = fmaf(s_dt[q] * kLn2, du, Dv * gy);
                 ot[j] = fmaf(du, xv, s_q[q]);
                 if (a.softplus) {
                     const float v = to_f32(rdt[k].v[j]) + (a.dt_bias ? a.dt_bias[pl.c0 + c + j] : 0.f);
@@ -318,7 +319,7 @@ scan_bwd_kernel(const SelectiveArgs a, const SelectiveGrads gr, const float* __r
         for (int i = 0; i < SPL; ++i) {
             const int n = lane * SPL + i;
             if (n < d.N) {
-                part_a[row * d.N + n] = dA[i];
+                part_a[row * d.N + n] = dA[i] * kLn2;
                 if (gr.dinit) gr.dinit[row * d.N + n] = g[i];
             }
         }

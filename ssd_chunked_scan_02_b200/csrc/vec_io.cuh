@@ -13,15 +13,20 @@ struct alignas(sizeof(T) * V) Raw {      // one load of 2..16 bytes
     T v[V];
 };
 
+// Read-only data.  Volatile, so that a load that is issued early for later use is
+// not moved down to its use.
 template <typename T, int V>
 __device__ __forceinline__ Raw<T, V> raw_load(const T* p) {
     Raw<T, V> r;
     constexpr int kBytes = sizeof(T) * V;
     if constexpr (kBytes == 16) {
-        const uint4 q = __ldg(reinterpret_cast<const uint4*>(p));
+        uint4 q;
+        asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(q.x), "=r"(q.y), "=r"(q.z), "=r"(q.w) : "l"(p));
         r = *reinterpret_cast<const Raw<T, V>*>(&q);
     } else if constexpr (kBytes == 8) {
-        const uint2 q = __ldg(reinterpret_cast<const uint2*>(p));
+        uint2 q;
+        asm volatile("ld.global.nc.v2.u32 {%0, %1}, [%2];" : "=r"(q.x), "=r"(q.y) : "l"(p));
         r = *reinterpret_cast<const Raw<T, V>*>(&q);
     } else {
 #pragma unroll
@@ -55,6 +60,22 @@ __device__ __forceinline__ Raw<T, V> raw_from_f32(const float (&f)[V]) {
 template <typename T, int V>
 __device__ __forceinline__ void raw_store(T* p, const Raw<T, V>& r) {
     *reinterpret_cast<Raw<T, V>*>(p) = r;
+}
+
+// Copies sizeof(R) bytes (4, 8 or 16, both sides aligned) to shared memory
+// without a register in between, or writes zeros where there is nothing to copy
+// (p is then not read).  Complete after copies_pending<..> in the same thread.
+template <typename R, typename T>
+__device__ __forceinline__ void copy_async(R* to, const T* p, bool exists) {
+    const uint32_t s = (uint32_t)__cvta_generic_to_shared(to);
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;"
+                 :: "r"(s), "l"(p), "n"((int)sizeof(R)), "r"(exists ? (int)sizeof(R) : 0) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// Waits until at most N of this thread's committed groups are still under way.
+template <int N>
+__device__ __forceinline__ void copies_pending() {
+    asm volatile("cp.async.wait_group %0;" :: "n"(N) : "memory");
 }
 
 // sigmoid(v) = 1 / (1 + exp(-v)); exp overflows to +inf for v < -88, whose
