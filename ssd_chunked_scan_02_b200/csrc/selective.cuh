@@ -42,6 +42,11 @@ __device__ __forceinline__ F2 mul2(F2 a, F2 b) {
     asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
     return r;
 }
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+    F2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
 __device__ __forceinline__ F2 ex2_2(F2 v) {
     const float2 f = unpack2(v);
     return pack2(ex2(f.x), ex2(f.y));
@@ -114,6 +119,7 @@ struct Layout {
     static constexpr int SPL = SPL_, LPC = LPC_, NP = SPL_ * LPC_;   // NP: N rounded up
     static constexpr int CH = 128 / LPC_;                            // channels of a block
     static constexpr int TT = NP <= 64 ? 32 : (NP == 128 ? 16 : 8);  // tokens of a tile
+    static constexpr int TS = 32 / SPL_;     // tokens whose states the backward holds in registers
 };
 
 inline int padded_states(int64_t N) {
@@ -182,6 +188,13 @@ __device__ __forceinline__ void store_channels(T* p, const Raw<T, VW>& r, int n,
         for (int i = 0; i < VW; ++i)
             if (i < n) p[i] = r.v[i];
     }
+}
+
+// Whether all rows of a view can be read w elements at a time.
+template <typename T>
+bool rows_fit(const void* p, Stride s, int w) {
+    return reinterpret_cast<uintptr_t>(p) % (w * sizeof(T)) == 0 && s.batch % w == 0 &&
+           s.token % w == 0;
 }
 
 // Channels of one load: 16 bytes, or a block's channels where those are fewer.

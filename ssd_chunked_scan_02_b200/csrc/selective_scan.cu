@@ -39,6 +39,8 @@ struct Spans {
     float *state, *sum;
 };
 
+enum class What { SpanState, Output, Checkpoints };
+
 template <typename T, typename Lay>
 struct Fwd {
     static constexpr int TT = Lay::TT, CH = Lay::CH, NP = Lay::NP;
@@ -54,16 +56,18 @@ struct Fwd {
     static constexpr int BLOCKS = SMEM <= 75 * 1024 ? 3 : 2;   // of an SM
 };
 
-// Output: y and the final states; else the span's state from zero.  Vec: x, dt and z
-// can be loaded VW channels, B and C VB states at a time.  The next tile's loads are then free of
+// What: the state a span reaches from zero; y and the final states; or the
+// states before every TS-th token, for the gradients.  Vec: x, dt and z can be
+// loaded VW channels, B and C VB states at a time.  The next tile's loads are then free of
 // branches (rows and channels that do not exist read ones that do, and are
 // replaced by zeros when the tile is staged), because the join behind a branch
 // would wait for them.
-template <typename T, typename Lay, bool Output, bool Vec>
+template <typename T, typename Lay, What W, bool Vec>
 __global__ void __launch_bounds__((Fwd<T, Lay>::THREADS), (Fwd<T, Lay>::BLOCKS))
 scan_fwd_kernel(const SelectiveArgs a, T* __restrict__ y, float* __restrict__ final_states,
                 const Spans sp, const SelectiveDims d) {
     using F = Fwd<T, Lay>;
+    constexpr bool Output = W == What::Output, Sum = W == What::SpanState;
     constexpr int SPL = Lay::SPL, LPC = Lay::LPC, NP = Lay::NP, CH = Lay::CH, TT = Lay::TT;
     constexpr int VW = F::VW, NI = F::NI, VB = F::VB, NB = F::NB, PY = F::PY, KC = F::KC;
     constexpr int TG = LPC < 8 ? LPC : 8;                           // tokens summed at once
@@ -121,9 +125,9 @@ scan_fwd_kernel(const SelectiveArgs a, T* __restrict__ y, float* __restrict__ fi
                 const int n = lane * SPL + i;
                 const bool on = ch < pl.count && n < d.N;
                 av[i] = on ? a.A[(pl.c0 + ch) * d.N + n] : 0.f;
-                hv[i] = on && Output && a.init ? a.init[row * d.N + n] : 0.f;
+                hv[i] = on && !Sum && a.init ? a.init[row * d.N + n] : 0.f;
             }
-            if (Output && ch < pl.count) {
+            if (!Sum && ch < pl.count) {
                 for (int k = 0; k < span; ++k) {                        // the spans before this one
                     const int64_t at = (pl.b * (sp.count - 1) + k) * d.D + pl.c0 + ch;
                     const float sum = sp.sum[at];
@@ -138,6 +142,12 @@ scan_fwd_kernel(const SelectiveArgs a, T* __restrict__ y, float* __restrict__ fi
                 h[i] = pack2(hv[2 * i], hv[2 * i + 1]);
             }
         }
+        constexpr int TS = Lay::TS;
+        const int64_t nck = (d.L + TS - 1) / TS;
+        float* ck = W == What::Checkpoints
+                        ? final_states + ((pl.b * nck + first / TS) * d.D + pl.c0 + ch) * NP + lane * SPL
+                        : nullptr;
+        int ck_left = (rows + TS - 1) / TS;
         auto walk = [&](int w) {
             const float2* du = s_du + w * TT * CH;
             const float* Bt = s_B + w * TT * NP + lane * SPL;
@@ -147,6 +157,17 @@ scan_fwd_kernel(const SelectiveArgs a, T* __restrict__ y, float* __restrict__ fi
                 float ys[TG];
 #pragma unroll
                 for (int k = 0; k < 8; ++k) {
+                    if (W == What::Checkpoints && k % TS == 0) {
+                        if (ch < pl.count && ck_left > 0) {
+#pragma unroll
+                            for (int i = 0; i < SPL; i += 4) {
+                                const float2 lo = unpack2(h[i / 2]), hi = unpack2(h[i / 2 + 1]);
+                                *reinterpret_cast<float4*>(ck + i) = make_float4(lo.x, lo.y, hi.x, hi.y);
+                            }
+                        }
+                        ck += d.D * NP;
+                        --ck_left;
+                    }
                     const float2 q = du[(tt + k) * CH + (ch ^ ((k * PER + ch / VW) & SWZ))];
                     const F2 dd = pack2(q.x, q.x), uu = pack2(q.y, q.y);
                     F2 yy = 0;
@@ -195,7 +216,7 @@ scan_fwd_kernel(const SelectiveArgs a, T* __restrict__ y, float* __restrict__ fi
                 for (int i = 0; i < SPL; ++i)
                     if (lane * SPL + i < d.N) final_states[row * d.N + lane * SPL + i] = hv[i];
             }
-        } else {
+        } else if (Sum) {
             const int64_t at = (pl.b * (sp.count - 1) + span) * d.D + pl.c0;
             if (ch < pl.count) {
 #pragma unroll
@@ -283,7 +304,7 @@ scan_fwd_kernel(const SelectiveArgs a, T* __restrict__ y, float* __restrict__ fi
                         float u = v * to_f32(rx.v[j]);
                         if (j >= n) v = u = 0.f;
                         v *= kLog2E;                      // the decays are powers of two
-                        if (!Output) sum_dt[k][j] += v;
+                        if (Sum) sum_dt[k][j] += v;
                         du[t * CH + ((c + j) ^ (i & SWZ))] = make_float2(v, u);
                     }
                 }
@@ -356,7 +377,7 @@ scan_fwd_kernel(const SelectiveArgs a, T* __restrict__ y, float* __restrict__ fi
             tile(at, 0);
             if (at + TT < rows) tile(at + TT, 1);
         }
-        if (!Output) {
+        if (Sum) {
 #pragma unroll
             for (int k = 0; k < NI; ++k) {
                 const int i = k * KC + tid, t = i / PER, c = i % PER * VW;
@@ -367,7 +388,7 @@ scan_fwd_kernel(const SelectiveArgs a, T* __restrict__ y, float* __restrict__ fi
             }
         }
     }
-    if (!Output) {
+    if (Sum) {
         // sums of dt: the threads of a channel, in order
         __syncthreads();
         const int64_t at = (pl.b * (sp.count - 1) + span) * d.D + pl.c0;
@@ -451,12 +472,6 @@ step_kernel(float* __restrict__ state, const SelectiveArgs a, T* __restrict__ y,
     }
 }
 
-template <typename T>
-bool rows_fit(const void* p, Stride s, int w) {
-    return reinterpret_cast<uintptr_t>(p) % (w * sizeof(T)) == 0 && s.batch % w == 0 &&
-           s.token % w == 0;
-}
-
 }  // namespace
 
 // Whether every token's channels can be loaded w elements at a time: all rows
@@ -495,8 +510,10 @@ size_t selective_fwd_workspace_bytes(const SelectiveDims& d) {
     return (size_t)(d.b * (sp.count - 1) * d.D * (padded_states(d.N) + 1)) * 4;
 }
 
-cudaError_t launch_selective_fwd(const SelectiveArgs& a, void* y, float* final_states, float* ws,
-                                 const SelectiveDims& d, Elt t, cudaStream_t s) {
+// The span states where there are several spans, then the walk for `W`.
+template <What W>
+cudaError_t run_fwd(const SelectiveArgs& a, void* y, float* out, float* ws, const SelectiveDims& d,
+                    Elt t, cudaStream_t s) {
     const Spans sp = spans_of(d, ws);
     cudaError_t err = cudaSuccess;
     with_elt(t, [&](auto ty) {
@@ -512,19 +529,29 @@ cudaError_t launch_selective_fwd(const SelectiveArgs& a, void* y, float* final_s
                                            F::SMEM);
                 if (err == cudaSuccess)
                     kernel<<<dim3(blocks, spans), F::THREADS, F::SMEM, s>>>(
-                        a, static_cast<T*>(y), final_states, sp, d);
+                        a, static_cast<T*>(y), out, sp, d);
             };
             auto both = [&](auto state_only, auto whole) {
                 if (sp.count > 1) go(state_only, (unsigned)sp.count - 1);
                 if (err == cudaSuccess) go(whole, (unsigned)sp.count);
             };
             if (vec)
-                both(scan_fwd_kernel<T, Lay, false, true>, scan_fwd_kernel<T, Lay, true, true>);
+                both(scan_fwd_kernel<T, Lay, What::SpanState, true>, scan_fwd_kernel<T, Lay, W, true>);
             else
-                both(scan_fwd_kernel<T, Lay, false, false>, scan_fwd_kernel<T, Lay, true, false>);
+                both(scan_fwd_kernel<T, Lay, What::SpanState, false>, scan_fwd_kernel<T, Lay, W, false>);
         });
     });
     return err != cudaSuccess ? err : cudaGetLastError();
+}
+
+cudaError_t launch_selective_fwd(const SelectiveArgs& a, void* y, float* final_states, float* ws,
+                                 const SelectiveDims& d, Elt t, cudaStream_t s) {
+    return run_fwd<What::Output>(a, y, final_states, ws, d, t, s);
+}
+
+cudaError_t launch_selective_checkpoints(const SelectiveArgs& a, float* ckpt, float* ws,
+                                         const SelectiveDims& d, Elt t, cudaStream_t s) {
+    return run_fwd<What::Checkpoints>(a, nullptr, ckpt, ws, d, t, s);
 }
 
 cudaError_t launch_selective_step(float* state, const SelectiveArgs& a, void* y,

@@ -14,7 +14,8 @@
 // in the workspace; the second takes the tokens in reverse, TS at a time: it
 // computes their TS states again from the state before them, in registers, and
 // then walks them backwards.  What the exponentials of the first walk cost is
-// what keeping every state would cost in memory several times over.
+// what keeping every state would cost in memory several times over.  a_t g_t is
+// both the next g and, times h_{t-1}, q_t.
 //
 // Sums over a group's channels (dB, dC) go over the channels of a warp by
 // shuffles, over a block's warps in shared memory, and over the blocks through
@@ -33,105 +34,58 @@ namespace {
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kThreads = 128, kWarps = kThreads / 32;
 
-template <typename Lay>
+template <typename T, typename Lay>
 struct Bwd {
-    static constexpr int TS = 32 / Lay::SPL;                     // tokens in registers
-    static constexpr int TT = Lay::NP <= 32 ? 32 : (Lay::NP == 64 ? 16 : 8);
-    static constexpr int SMEM = TT * Lay::CH * 6 * 4 + TT * Lay::NP * 2 * 4 * (1 + kWarps);
+    static constexpr int NP = Lay::NP, CH = Lay::CH;
+    static constexpr int TT = NP <= 32 ? 32 : (NP == 64 ? 16 : 8);   // tokens of a tile
+    static constexpr int VW = load_width<T, CH>(), PER = CH / VW;
+    static constexpr int IT = (TT * PER + kThreads - 1) / kThreads;  // loads a thread and tile
+    static constexpr int VB = 16 / sizeof(T);
+    static constexpr int NB = (TT * NP * 2 / VB + kThreads - 1) / kThreads;
+    static constexpr int PY = CH + 8;                                // a row of results
+    static constexpr int RAW = kThreads * (4 * IT * VW + NB * VB) * (int)sizeof(T);
+    static constexpr int SMEM = 2 * RAW + TT * CH * 12 + 3 * TT * PY * 4 +
+                                TT * NP * 8 * (1 + kWarps) + 2 * kThreads * VW * 4;
+    static constexpr int BLOCKS = SMEM <= 75 * 1024 ? 3 : 2;         // of an SM
 };
 
-// dt (after bias and softplus) of token t, channel c of the block.
-template <typename T>
-__device__ __forceinline__ float step_of(T raw, const SelectiveArgs& a, int64_t c) {
-    const float v = to_f32(raw) + (a.dt_bias ? a.dt_bias[c] : 0.f);
-    return a.softplus ? softplus_f32(v) : v;
-}
-
-// ------------------------------------------------------------------ states at every TS-th token
-// ckpt (b, ceil(L / TS), D, NP): the state before token TS * j.
-template <typename T, typename Lay>
-__global__ void __launch_bounds__(kThreads)
-checkpoint_kernel(const SelectiveArgs a, float* __restrict__ ckpt, const SelectiveDims d, bool vec) {
-    constexpr int SPL = Lay::SPL, LPC = Lay::LPC, NP = Lay::NP, CH = Lay::CH, TT = Lay::TT;
-    constexpr int TS = Bwd<Lay>::TS, VW = load_width<T, CH>();
-    __shared__ float2 s_du[TT][CH];
-    __shared__ __align__(16) float s_B[TT][NP];
-    const Place pl = place_of<CH>(blockIdx.x, d);
-    const int tid = threadIdx.x, lane = tid % LPC, ch = tid / LPC;
-    const int64_t len = own_length(a.lens, pl.b, d.L), nck = (d.L + TS - 1) / TS;
-    const T* x = static_cast<const T*>(a.x) + pl.b * a.xs.batch + pl.c0;
-    const T* dt = static_cast<const T*>(a.dt) + pl.b * a.dts.batch + pl.c0;
-    const T* Bp = static_cast<const T*>(a.B) + pl.b * a.Bs.batch + pl.g * d.N;
-    float A[SPL], h[SPL];
-#pragma unroll
-    for (int i = 0; i < SPL; ++i) {
-        const int n = lane * SPL + i;
-        const bool on = ch < pl.count && n < d.N;
-        A[i] = on ? a.A[(pl.c0 + ch) * d.N + n] : 0.f;
-        h[i] = on && a.init ? a.init[(pl.b * d.D + pl.c0 + ch) * d.N + n] : 0.f;
-    }
-    for (int64_t t0 = 0; t0 < d.L; t0 += TT) {
-        __syncthreads();
-        for (int i = tid; i < TT * CH / VW; i += kThreads) {
-            const int t = i / (CH / VW), c = i % (CH / VW) * VW;
-            const int n = t0 + t < len ? pl.count - c : 0;
-            const auto rx = load_channels<T, VW>(x + (t0 + t) * a.xs.token + c, n, vec);
-            const auto rdt = load_channels<T, VW>(dt + (t0 + t) * a.dts.token + c, n, vec);
-#pragma unroll
-            for (int j = 0; j < VW; ++j) {
-                const float v = j < n ? step_of(rdt.v[j], a, pl.c0 + c + j) : 0.f;
-                s_du[t][c + j] = make_float2(v * kLog2E, v * to_f32(rx.v[j]));
-            }
-        }
-        for (int i = tid; i < TT * NP; i += kThreads) {
-            const int t = i / NP, n = i % NP;
-            s_B[t][n] = n < d.N && t0 + t < len ? to_f32(Bp[(t0 + t) * a.Bs.token + n]) : 0.f;
-        }
-        __syncthreads();
-#pragma unroll 1
-        for (int tt = 0; tt < TT; tt += TS) {
-            if (t0 + tt >= d.L) break;
-            if (ch < pl.count) {
-                float* q = ckpt + ((pl.b * nck + (t0 + tt) / TS) * d.D + pl.c0 + ch) * NP + lane * SPL;
-#pragma unroll
-                for (int i = 0; i < SPL; i += 4)
-                    *reinterpret_cast<float4*>(q + i) = make_float4(h[i], h[i + 1], h[i + 2], h[i + 3]);
-            }
-#pragma unroll
-            for (int k = 0; k < TS; ++k) {
-                const float2 du = s_du[tt + k][ch];
-#pragma unroll
-                for (int i = 0; i < SPL; ++i)
-                    h[i] = fmaf(ex2(du.x * A[i]), h[i], du.y * s_B[tt + k][lane * SPL + i]);
-            }
-        }
-    }
-}
-
 // ------------------------------------------------------------------ the reverse walk
-template <typename T, typename Lay>
-__global__ void __launch_bounds__(kThreads)
+// ckpt (b, ceil(L / TS), D, NP): the state before token TS * j.
+template <typename T, typename Lay, bool Vec>
+__global__ void __launch_bounds__(kThreads, (Bwd<T, Lay>::BLOCKS))
 scan_bwd_kernel(const SelectiveArgs a, const SelectiveGrads gr, const float* __restrict__ ckpt,
                 float* __restrict__ part_bc, float* __restrict__ part_a,
-                float* __restrict__ part_d, const SelectiveDims d, bool vec) {
-    constexpr int SPL = Lay::SPL, LPC = Lay::LPC, NP = Lay::NP, CH = Lay::CH;
-    constexpr int TS = Bwd<Lay>::TS, TT = Bwd<Lay>::TT, VW = load_width<T, CH>();
+                float* __restrict__ part_d, const SelectiveDims d) {
+    using S = Bwd<T, Lay>;
+    constexpr int SPL = Lay::SPL, LPC = Lay::LPC, NP = Lay::NP, CH = Lay::CH, TS = Lay::TS;
+    constexpr int TT = S::TT, VW = S::VW, PER = S::PER, IT = S::IT, VB = S::VB, NB = S::NB;
+    constexpr int PY = S::PY, SWZ = (CH < 8 ? CH : 8) - 1;
     constexpr int CPW = 32 / LPC;                               // channels of a warp
-    constexpr int IT = (TT * CH / VW + kThreads - 1) / kThreads;
-    extern __shared__ __align__(16) float smem[];
-    float* s_dt = smem;                                         // [TT][CH] each; dt log2(e)
-    float* s_u = s_dt + TT * CH;
-    float* s_g = s_u + TT * CH;
-    float* s_y = s_g + TT * CH;
-    float* s_du = s_y + TT * CH;
-    float* s_q = s_du + TT * CH;
-    float* s_B = s_q + TT * CH;                                 // [TT][NP]
+    constexpr int FG = 16 / SPL;                                // tokens of a sum over channels
+    constexpr int NG = 4;                                       // tokens of a sum over states
+    using RV = Raw<T, VW>;
+    using RB = Raw<T, VB>;
+    extern __shared__ __align__(16) unsigned char smem[];
+    // two tiles as they come: a thread copies and reads its own elements
+    RB* r_bc = reinterpret_cast<RB*>(smem);                     // [2][NB][threads]
+    RV* r_x = reinterpret_cast<RV*>(r_bc + 2 * NB * kThreads);  // [2][IT][threads] each
+    RV* r_dt = r_x + 2 * IT * kThreads;
+    RV* r_z = r_dt + 2 * IT * kThreads;
+    RV* r_dy = r_z + 2 * IT * kThreads;
+    float2* s_du = reinterpret_cast<float2*>(r_dy + 2 * IT * kThreads);   // [TT][CH]: dt log2(e), u
+    float* s_B = reinterpret_cast<float*>(s_du + TT * CH);      // [TT][NP] each
     float* s_C = s_B + TT * NP;
     float* s_red = s_C + TT * NP;                               // [warps][TT][2][NP]
+    float* s_sum = s_red + kWarps * TT * 2 * NP;                // [2][threads][VW]: dD, ddt_bias
+    float* s_y = s_sum + 2 * kThreads * VW;                     // [TT][PY] each
+    float* s_dtg = s_y + TT * PY;                               // du = sum B g
+    float* s_q = s_dtg + TT * PY;
+    float* s_g = s_q + TT * PY;                                 // [TT][CH]: dyg
 
     const Place pl = place_of<CH>(blockIdx.x, d);
     const int tid = threadIdx.x, lane = tid % LPC, ch = tid / LPC, warp = tid / 32;
     const int64_t len = own_length(a.lens, pl.b, d.L), nck = (d.L + TS - 1) / TS;
+    const int L = (int)d.L, own = (int)len;
     const T* x = static_cast<const T*>(a.x) + pl.b * a.xs.batch + pl.c0;
     const T* dt = static_cast<const T*>(a.dt) + pl.b * a.dts.batch + pl.c0;
     const T* z = a.z ? static_cast<const T*>(a.z) + pl.b * a.zs.batch + pl.c0 : nullptr;
@@ -143,172 +97,267 @@ scan_bwd_kernel(const SelectiveArgs a, const SelectiveGrads gr, const float* __r
     T* ddt = static_cast<T*>(gr.ddt) + dense;
     T* dz = z ? static_cast<T*>(gr.dz) + dense : nullptr;
     const int64_t cb = blockIdx.x % (gridDim.x / d.b);          // channel block over all groups
-
-    float A[SPL], g[SPL], dA[SPL];
     const int64_t row = pl.b * d.D + pl.c0 + ch;
-#pragma unroll
-    for (int i = 0; i < SPL; ++i) {
-        const int n = lane * SPL + i;
-        const bool on = ch < pl.count && n < d.N;
-        A[i] = on ? a.A[(pl.c0 + ch) * d.N + n] : 0.f;
-        g[i] = on && gr.dfinal ? gr.dfinal[row * d.N + n] : 0.f;
-        dA[i] = 0.f;
-    }
-    float sumD[IT][VW], sumB[IT][VW];
-#pragma unroll
-    for (int k = 0; k < IT; ++k)
-#pragma unroll
-        for (int j = 0; j < VW; ++j) sumD[k][j] = sumB[k][j] = 0.f;
 
-    const int64_t ntile = (d.L + TT - 1) / TT;
-    for (int64_t tile = ntile - 1; tile >= 0; --tile) {
-        const int64_t t0 = tile * TT;
-        Raw<T, VW> rx[IT], rdt[IT], rz[IT], rdy[IT];
+    for (int i = tid; i < 2 * TT * NP; i += kThreads) s_B[i] = 0.f;       // states beyond N
+    for (int i = tid; i < 2 * kThreads * VW; i += kThreads) s_sum[i] = 0.f;
+    auto bias = [&](int c) { return a.dt_bias && c < pl.count ? __ldg(a.dt_bias + pl.c0 + c) : 0.f; };
+    auto skip = [&](int c) { return a.D && c < pl.count ? __ldg(a.D + pl.c0 + c) : 0.f; };
+
+    F2 A[SPL / 2], g[SPL / 2], dA[SPL / 2];
+    {
+        float av[SPL], gv[SPL];
+#pragma unroll
+        for (int i = 0; i < SPL; ++i) {
+            const int n = lane * SPL + i;
+            const bool on = ch < pl.count && n < d.N;
+            av[i] = on ? a.A[(pl.c0 + ch) * d.N + n] : 0.f;
+            gv[i] = on && gr.dfinal ? gr.dfinal[row * d.N + n] : 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < SPL / 2; ++i) {
+            A[i] = pack2(av[2 * i], av[2 * i + 1]);
+            g[i] = pack2(gv[2 * i], gv[2 * i + 1]);
+            dA[i] = 0;
+        }
+    }
+
+    const int nvb = Vec ? (int)d.N / VB : 1;
+    auto load = [&](int t0, int w) {
+        if constexpr (Vec) {
+#pragma unroll
+            for (int k = 0; k < IT; ++k) {
+                const int i = k * kThreads + tid, t = t0 + i / PER, c = i % PER * VW;
+                const int o = (w * IT + k) * kThreads + tid;
+                const bool in = i / PER < TT && t < own && c < pl.count;
+                const int64_t r = in ? t : 0;
+                const int cc = in ? c : 0;
+                copy_async(r_x + o, x + r * a.xs.token + cc, in);
+                copy_async(r_dt + o, dt + r * a.dts.token + cc, in);
+                copy_async(r_dy + o, dy + r * d.D + cc, in);
+                if (z) copy_async(r_z + o, z + r * a.zs.token + cc, in);
+            }
+#pragma unroll
+            for (int k = 0; k < NB; ++k) {
+                const int i = k * kThreads + tid, t = t0 + i / (2 * nvb), v = i % (2 * nvb);
+                const bool in = i / (2 * nvb) < TT && t < own;
+                const int64_t r = in ? t : 0;
+                copy_async(r_bc + (w * NB + k) * kThreads + tid,
+                           v < nvb ? Bp + r * a.Bs.token + v * VB : Cp + r * a.Cs.token + (v - nvb) * VB,
+                           in);
+            }
+            copies_commit();
+        }
+    };
+    auto stage = [&](int t0, int w) {
+        if constexpr (Vec) copies_pending<0>();
 #pragma unroll
         for (int k = 0; k < IT; ++k) {
-            const int i = k * kThreads + tid, t = i / (CH / VW), c = i % (CH / VW) * VW;
-            if (t >= TT) continue;
-            const int n = t0 + t < len ? pl.count - c : 0;
-            rx[k] = load_channels<T, VW>(x + (t0 + t) * a.xs.token + c, n, vec);
-            rdt[k] = load_channels<T, VW>(dt + (t0 + t) * a.dts.token + c, n, vec);
-            rdy[k] = load_channels<T, VW>(dy + (t0 + t) * d.D + c, n, vec);
-            if (z) rz[k] = load_channels<T, VW>(z + (t0 + t) * a.zs.token + c, n, vec);
+            const int i = k * kThreads + tid, tl = i / PER, t = t0 + tl, c = i % PER * VW;
+            const int o = (w * IT + k) * kThreads + tid;
+            if (tl >= TT) continue;
+            const int n = t < own ? pl.count - c : 0;
+            if constexpr (!Vec) {
+                r_x[o] = load_channels<T, VW>(x + (int64_t)t * a.xs.token + c, n, false);
+                r_dt[o] = load_channels<T, VW>(dt + (int64_t)t * a.dts.token + c, n, false);
+                r_dy[o] = load_channels<T, VW>(dy + (int64_t)t * d.D + c, n, false);
+                if (z) r_z[o] = load_channels<T, VW>(z + (int64_t)t * a.zs.token + c, n, false);
+            }
+            const RV rx = r_x[o], rdt = r_dt[o], rdy = r_dy[o];
+            RV rz;
+            if (z) rz = r_z[o];
 #pragma unroll
             for (int j = 0; j < VW; ++j) {
-                const float v = j < n ? step_of(rdt[k].v[j], a, pl.c0 + c + j) : 0.f;
-                float gy = j < n ? to_f32(rdy[k].v[j]) : 0.f;
-                if (z && j < n) {
-                    const float zv = to_f32(rz[k].v[j]);
-                    gy *= zv * sigmoid_f32(zv);
+                float v = to_f32(rdt.v[j]) + bias(c + j), gy = to_f32(rdy.v[j]);
+                if (a.softplus) v = softplus_f32(v);
+                if (z) {
+                    const float zv = to_f32(rz.v[j]);
+                    gy *= zv * sigmoid_fast(zv);
                 }
-                s_dt[t * CH + c + j] = v * kLog2E;
-                s_u[t * CH + c + j] = v * to_f32(rx[k].v[j]);
-                s_g[t * CH + c + j] = gy;
+                float u = v * to_f32(rx.v[j]);
+                if (j >= n) v = u = gy = 0.f;
+                s_du[tl * CH + ((c + j) ^ (i & SWZ))] = make_float2(v * kLog2E, u);
+                s_g[tl * CH + c + j] = gy;
             }
         }
-        for (int i = tid; i < TT * NP; i += kThreads) {
-            const int t = i / NP, n = i % NP;
-            const bool on = n < d.N && t0 + t < len;
-            s_B[i] = on ? to_f32(Bp[(t0 + t) * a.Bs.token + n]) : 0.f;
-            s_C[i] = on ? to_f32(Cp[(t0 + t) * a.Cs.token + n]) : 0.f;
+        if constexpr (Vec) {
+#pragma unroll
+            for (int k = 0; k < NB; ++k) {
+                const int i = k * kThreads + tid, tl = i / (2 * nvb), v = i % (2 * nvb);
+                if (tl < TT) {
+                    float f[VB];
+                    raw_to_f32(t0 + tl < own ? r_bc[(w * NB + k) * kThreads + tid] : raw_zero<T, VB>(), f);
+                    float* q = v < nvb ? s_B + tl * NP + v * VB : s_C + tl * NP + (v - nvb) * VB;
+#pragma unroll
+                    for (int j = 0; j < VB; j += 4)
+                        *reinterpret_cast<float4*>(q + j) = make_float4(f[j], f[j + 1], f[j + 2], f[j + 3]);
+                }
+            }
+        } else {
+            for (int i = tid; i < TT * NP; i += kThreads) {
+                const int t = t0 + i / NP, n = i % NP;
+                const bool on = n < d.N && t < own;
+                s_B[i] = on ? to_f32(Bp[(int64_t)t * a.Bs.token + n]) : 0.f;
+                s_C[i] = on ? to_f32(Cp[(int64_t)t * a.Cs.token + n]) : 0.f;
+            }
         }
+    };
+    // the states before token t0 (a multiple of TS), a step ahead of their use
+    Raw<float, 4> hn[SPL / 4];
+    const float* ck = ckpt + (pl.b * nck * d.D + pl.c0 + (ch < pl.count ? ch : 0)) * NP + lane * SPL;
+    auto fetch = [&](int t0) {
+        const int64_t j = t0 <= 0 ? 0 : t0 / TS < nck ? t0 / TS : nck - 1;
+#pragma unroll
+        for (int i = 0; i < SPL / 4; ++i) hn[i] = raw_load<float, 4>(ck + j * d.D * NP + 4 * i);
+    };
+
+    const int ntile = (L + TT - 1) / TT;
+    if (ntile > 0) {
+        load((ntile - 1) * TT, (ntile - 1) & 1);
+        fetch(ntile * TT - TS);
+        __syncthreads();                                        // s_B's zeros
+    }
+    for (int tile = ntile - 1; tile >= 0; --tile) {
+        const int t0 = tile * TT, w = tile & 1;
+        stage(t0, w);
         __syncthreads();
+        if (tile > 0) load(t0 - TT, w ^ 1);
 
 #pragma unroll 1
         for (int tt = TT - TS; tt >= 0; tt -= TS) {
-            // the states of TS tokens: a_t and a_t h_{t-1} (h_t is that plus u B)
-            float e[TS][SPL], eh[TS][SPL], h[SPL];
+            // a_t and h_t of TS tokens; h[0] is the state before them.  (Behind the
+            // last token dt = 0 keeps whatever state is loaded, and u, dyg, B and C
+            // are zero: nothing of it is used.)
+            F2 e[TS][SPL / 2], h[TS + 1][SPL / 2];
 #pragma unroll
-            for (int i = 0; i < SPL; ++i) h[i] = 0.f;
-            if (ch < pl.count && t0 + tt < d.L) {
-                const float* q = ckpt + ((pl.b * nck + (t0 + tt) / TS) * d.D + pl.c0 + ch) * NP + lane * SPL;
-#pragma unroll
-                for (int i = 0; i < SPL; i += 4) {
-                    const float4 f = *reinterpret_cast<const float4*>(q + i);
-                    h[i] = f.x; h[i + 1] = f.y; h[i + 2] = f.z; h[i + 3] = f.w;
-                }
-            }
+            for (int i = 0; i < SPL / 2; ++i) h[0][i] = pack2(hn[i / 2].v[i % 2 * 2], hn[i / 2].v[i % 2 * 2 + 1]);
+            fetch(t0 + tt - TS);
 #pragma unroll
             for (int k = 0; k < TS; ++k) {
-                const float v = s_dt[(tt + k) * CH + ch], u = s_u[(tt + k) * CH + ch];
+                const float2 q = s_du[(tt + k) * CH + (ch ^ (((tt + k) * PER + ch / VW) & SWZ))];
+                const F2 dd = pack2(q.x, q.x), uu = pack2(q.y, q.y);
+                const float* Bt = s_B + (tt + k) * NP + lane * SPL;
 #pragma unroll
-                for (int i = 0; i < SPL; ++i) {
-                    e[k][i] = ex2(v * A[i]);
-                    eh[k][i] = e[k][i] * h[i];
-                    h[i] = fmaf(u, s_B[(tt + k) * NP + lane * SPL + i], eh[k][i]);
+                for (int i = 0; i < SPL / 2; i += 2) {
+                    const float4 bv = *reinterpret_cast<const float4*>(Bt + 2 * i);
+                    e[k][i] = ex2_2(mul2(dd, A[i]));
+                    e[k][i + 1] = ex2_2(mul2(dd, A[i + 1]));
+                    h[k + 1][i] = fma2(e[k][i], h[k][i], mul2(uu, pack2(bv.x, bv.y)));
+                    h[k + 1][i + 1] = fma2(e[k][i + 1], h[k][i + 1], mul2(uu, pack2(bv.z, bv.w)));
                 }
             }
-            float py[TS], pu[TS], pq[TS], pB[TS * SPL], pC[TS * SPL], at[SPL];
+            F2 at[SPL / 2];
 #pragma unroll
-            for (int i = 0; i < SPL; ++i) at[i] = 0.f;
+            for (int i = 0; i < SPL / 2; ++i) at[i] = 0;
+            float py[NG], pu[NG], pq[NG], pB[16], pC[16];
 #pragma unroll
             for (int k = TS - 1; k >= 0; --k) {
-                const float v = s_dt[(tt + k) * CH + ch], u = s_u[(tt + k) * CH + ch];
+                const float2 q = s_du[(tt + k) * CH + (ch ^ (((tt + k) * PER + ch / VW) & SWZ))];
                 const float gy = s_g[(tt + k) * CH + ch];
-                py[k] = pu[k] = pq[k] = 0.f;
+                const F2 dd = pack2(q.x, q.x), uu = pack2(q.y, q.y), gg = pack2(gy, gy);
+                const float* Bt = s_B + (tt + k) * NP + lane * SPL;
+                const float* Ct = s_C + (tt + k) * NP + lane * SPL;
+                F2 sy = 0, su = 0, sq = 0;
 #pragma unroll
-                for (int i = 0; i < SPL; ++i) {
-                    const float Bv = s_B[(tt + k) * NP + lane * SPL + i];
-                    const float Cv = s_C[(tt + k) * NP + lane * SPL + i];
-                    const float ht = fmaf(u, Bv, eh[k][i]);
-                    g[i] = fmaf(gy, Cv, g[i]);
-                    py[k] = fmaf(Cv, ht, py[k]);
-                    pC[k * SPL + i] = gy * ht;
-                    pu[k] = fmaf(Bv, g[i], pu[k]);
-                    pB[k * SPL + i] = u * g[i];
-                    const float qv = g[i] * eh[k][i];
-                    pq[k] = fmaf(A[i], qv, pq[k]);
-                    at[i] = fmaf(v, qv, at[i]);
-                    g[i] *= e[k][i];
+                for (int i = 0; i < SPL / 2; ++i) {
+                    const float2 b2 = *reinterpret_cast<const float2*>(Bt + 2 * i);
+                    const float2 c2 = *reinterpret_cast<const float2*>(Ct + 2 * i);
+                    const F2 Bv = pack2(b2.x, b2.y), Cv = pack2(c2.x, c2.y);
+                    g[i] = fma2(gg, Cv, g[i]);
+                    sy = i == 0 ? mul2(Cv, h[k + 1][0]) : fma2(Cv, h[k + 1][i], sy);
+                    su = i == 0 ? mul2(Bv, g[0]) : fma2(Bv, g[i], su);
+                    const float2 dc = unpack2(mul2(gg, h[k + 1][i])), db = unpack2(mul2(uu, g[i]));
+                    pC[k % FG * SPL + 2 * i] = dc.x;
+                    pC[k % FG * SPL + 2 * i + 1] = dc.y;
+                    pB[k % FG * SPL + 2 * i] = db.x;
+                    pB[k % FG * SPL + 2 * i + 1] = db.y;
+                    g[i] = mul2(g[i], e[k][i]);
+                    const F2 qv = mul2(g[i], h[k][i]);
+                    sq = i == 0 ? mul2(A[0], qv) : fma2(A[i], qv, sq);
+                    at[i] = fma2(dd, qv, at[i]);
+                }
+                const float2 fy = unpack2(sy), fu = unpack2(su), fq = unpack2(sq);
+                py[k % NG] = fy.x + fy.y;
+                pu[k % NG] = fu.x + fu.y;
+                pq[k % NG] = fq.x + fq.y;
+                if (k % FG == 0) {
+                    // over a warp's channels: the lanes of one place in the channel lie LPC apart
+                    const int place = tid % 32 / LPC;
+                    fold<16, CPW, LPC>(pB, place);
+                    fold<16, CPW, LPC>(pC, place);
+                    constexpr int NV = 16 / CPW;
+#pragma unroll
+                    for (int i = 0; i < NV; ++i) {
+                        const int v = place * NV + i, t = tt + k + v / SPL, n = lane * SPL + v % SPL;
+                        s_red[((warp * TT + t) * 2 + 0) * NP + n] = pB[i];
+                        s_red[((warp * TT + t) * 2 + 1) * NP + n] = pC[i];
+                    }
+                }
+                if (k % NG == 0) {
+                    // over a channel's lanes
+                    fold<NG, LPC>(py, lane);
+                    fold<NG, LPC>(pu, lane);
+                    fold<NG, LPC>(pq, lane);
+                    constexpr int NT = NG >= LPC ? NG / LPC : 1, SH = NG >= LPC ? 1 : LPC / NG;
+                    if (lane % SH == 0) {
+#pragma unroll
+                        for (int i = 0; i < NT; ++i) {
+                            const int o = (tt + k + lane / SH * NT + i) * PY + ch;
+                            s_y[o] = py[i];
+                            s_dtg[o] = pu[i];
+                            s_q[o] = pq[i];
+                        }
+                    }
                 }
             }
 #pragma unroll
-            for (int i = 0; i < SPL; ++i) dA[i] += at[i];
-            // over a channel's lanes: lane l holds token l * TS / LPC of y, du and A q
-            fold<TS, LPC>(py, lane);
-            fold<TS, LPC>(pu, lane);
-            fold<TS, LPC>(pq, lane);
-            constexpr int NT = TS >= LPC ? TS / LPC : 1, SH = TS >= LPC ? 1 : LPC / TS;
-            if (lane % SH == 0) {
-#pragma unroll
-                for (int i = 0; i < NT; ++i) {
-                    const int t = tt + lane / SH * NT + i;
-                    s_y[t * CH + ch] = py[i];
-                    s_du[t * CH + ch] = pu[i];
-                    s_q[t * CH + ch] = pq[i];
-                }
-            }
-            // over a warp's channels: the lanes of one place in the channel differ by LPC
-            fold<TS * SPL, CPW, LPC>(pB, tid % 32 / LPC);
-            fold<TS * SPL, CPW, LPC>(pC, tid % 32 / LPC);
-            constexpr int NV = TS * SPL / CPW;
-#pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                const int v = tid % 32 / LPC * NV + i, t = tt + v / SPL, n = lane * SPL + v % SPL;
-                s_red[((warp * TT + t) * 2 + 0) * NP + n] = pB[i];
-                s_red[((warp * TT + t) * 2 + 1) * NP + n] = pC[i];
-            }
+            for (int i = 0; i < SPL / 2; ++i) dA[i] = add2(dA[i], at[i]);
         }
         __syncthreads();
 
         for (int i = tid; i < TT * 2 * NP; i += kThreads) {
-            const int t = i / (2 * NP), n = i % NP, which = i / NP % 2;
+            const int t = t0 + i / (2 * NP), n = i % NP, which = i / NP % 2;
             float v = 0.f;
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) v += s_red[w * TT * 2 * NP + i];
-            if (t0 + t < d.L && n < d.N)
-                part_bc[(((cb * d.b + pl.b) * d.L + t0 + t) * 2 + which) * d.N + n] = v;
+            for (int k = 0; k < kWarps; ++k) v += s_red[k * TT * 2 * NP + i];
+            if (t < L && n < d.N)
+                part_bc[(((cb * d.b + pl.b) * d.L + t) * 2 + which) * d.N + n] = v;
         }
 #pragma unroll
         for (int k = 0; k < IT; ++k) {
-            const int i = k * kThreads + tid, t = i / (CH / VW), c = i % (CH / VW) * VW;
-            if (t >= TT || t0 + t >= d.L) continue;
-            const int n = t0 + t < len ? pl.count - c : 0;
+            const int i = k * kThreads + tid, tl = i / PER, t = t0 + tl, c = i % PER * VW;
+            if (tl >= TT || t >= L) continue;
+            const int n = t < own ? pl.count - c : 0, o = (w * IT + k) * kThreads + tid;
+            const RV rx = r_x[o], rdt = r_dt[o], rdy = r_dy[o];
+            RV rz;
+            if (z) rz = r_z[o];
             float ox[VW], ot[VW], oz[VW];
 #pragma unroll
             for (int j = 0; j < VW; ++j) {
-                ox[j] = ot[j] = oz[j] = 0.f;
-                if (j >= n) continue;
-                const int q = t * CH + c + j;
-                const float xv = to_f32(rx[k].v[j]), gy = s_g[q], du = s_du[q];
-                const float Dv = a.D ? a.D[pl.c0 + c + j] : 0.f;
-                ox[j] = fmaf(s_dt[q] * kLn2, du, Dv * gy);
-                ot[j] = fmaf(du, xv, s_q[q]);
-                if (a.softplus) {
-                    const float v = to_f32(rdt[k].v[j]) + (a.dt_bias ? a.dt_bias[pl.c0 + c + j] : 0.f);
-                    ot[j] *= sigmoid_f32(v);
-                }
+                const float xv = to_f32(rx.v[j]), gy = s_g[tl * CH + c + j], Dv = skip(c + j);
+                const float dl = s_du[tl * CH + ((c + j) ^ (i & SWZ))].x;
+                const float du = s_dtg[tl * PY + c + j];
+                ox[j] = fmaf(dl * kLn2, du, Dv * gy);
+                ot[j] = fmaf(du, xv, s_q[tl * PY + c + j]);
+                if (a.softplus) ot[j] *= sigmoid_fast(to_f32(rdt.v[j]) + bias(c + j));
+                oz[j] = 0.f;
                 if (z) {
-                    const float zv = to_f32(rz[k].v[j]), sg = sigmoid_f32(zv);
-                    oz[j] = to_f32(rdy[k].v[j]) * fmaf(Dv, xv, s_y[q]) * sg * fmaf(zv, 1.f - sg, 1.f);
+                    const float zv = to_f32(rz.v[j]), sg = sigmoid_fast(zv);
+                    oz[j] = to_f32(rdy.v[j]) * fmaf(Dv, xv, s_y[tl * PY + c + j]) * sg *
+                            fmaf(zv, 1.f - sg, 1.f);
                 }
-                sumD[k][j] = fmaf(gy, xv, sumD[k][j]);
-                sumB[k][j] += ot[j];
+                if (j >= n) {
+                    ox[j] = ot[j] = oz[j] = 0.f;
+                } else {
+                    s_sum[tid * VW + j] = fmaf(gy, xv, s_sum[tid * VW + j]);
+                    s_sum[(kThreads + tid) * VW + j] += ot[j];
+                }
             }
             const int left = pl.count - c;
-            store_channels<T, VW>(dx + (t0 + t) * d.D + c, raw_from_f32<T, VW>(ox), left, vec);
-            store_channels<T, VW>(ddt + (t0 + t) * d.D + c, raw_from_f32<T, VW>(ot), left, vec);
-            if (z) store_channels<T, VW>(dz + (t0 + t) * d.D + c, raw_from_f32<T, VW>(oz), left, vec);
+            const int64_t at = (int64_t)t * d.D + c;
+            store_channels<T, VW>(dx + at, raw_from_f32<T, VW>(ox), left, Vec);
+            store_channels<T, VW>(ddt + at, raw_from_f32<T, VW>(ot), left, Vec);
+            if (z) store_channels<T, VW>(dz + at, raw_from_f32<T, VW>(oz), left, Vec);
         }
         __syncthreads();
     }
@@ -316,24 +365,17 @@ scan_bwd_kernel(const SelectiveArgs a, const SelectiveGrads gr, const float* __r
     // sums over the tokens: dA by lane; dD and ddt_bias over the threads of a channel
     if (ch < pl.count) {
 #pragma unroll
-        for (int i = 0; i < SPL; ++i) {
-            const int n = lane * SPL + i;
+        for (int i = 0; i < SPL / 2; ++i) {
+            const float2 da = unpack2(dA[i]), gv = unpack2(g[i]);
+            const int n = lane * SPL + 2 * i;
             if (n < d.N) {
-                part_a[row * d.N + n] = dA[i] * kLn2;
-                if (gr.dinit) gr.dinit[row * d.N + n] = g[i];
+                part_a[row * d.N + n] = da.x * kLn2;
+                if (gr.dinit) gr.dinit[row * d.N + n] = gv.x;
             }
-        }
-    }
-    float* s_sum = smem;                                        // [2][TT][CH]
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < IT; ++k) {
-        const int i = k * kThreads + tid, t = i / (CH / VW), c = i % (CH / VW) * VW;
-        if (t >= TT) continue;
-#pragma unroll
-        for (int j = 0; j < VW; ++j) {
-            s_sum[t * CH + c + j] = sumD[k][j];
-            s_sum[(TT + t) * CH + c + j] = sumB[k][j];
+            if (n + 1 < d.N) {
+                part_a[row * d.N + n + 1] = da.y * kLn2;
+                if (gr.dinit) gr.dinit[row * d.N + n + 1] = gv.y;
+            }
         }
     }
     __syncthreads();
@@ -341,7 +383,7 @@ scan_bwd_kernel(const SelectiveArgs a, const SelectiveGrads gr, const float* __r
         const int c = i % CH, which = i / CH;
         if (c >= pl.count) continue;
         float v = 0.f;
-        for (int t = 0; t < TT; ++t) v += s_sum[(which * TT + t) * CH + c];
+        for (int q = c / VW; q < kThreads; q += PER) v += s_sum[(which * kThreads + q) * VW + c % VW];
         part_d[((int64_t)which * d.b + pl.b) * d.D + pl.c0 + c] = v;
     }
 }
@@ -373,18 +415,19 @@ reduce_batch_kernel(const float* __restrict__ part, float* __restrict__ out, int
 }
 
 struct Work {
-    size_t ckpt, bc, a, d, total;       // floats
+    size_t ckpt, bc, a, d, fwd, total;       // floats; fwd: the checkpoint walk's own
 };
 Work work_of(const SelectiveDims& d) {
     Work w{};
     with_layout(d.N, [&](auto lay) {
         using Lay = decltype(lay);
-        const int64_t TS = Bwd<Lay>::TS;
+        const int64_t TS = Lay::TS;
         w.ckpt = 0;
         w.bc = w.ckpt + (size_t)(d.b * ((d.L + TS - 1) / TS) * d.D * Lay::NP);
         w.a = w.bc + (size_t)(channel_blocks<Lay::CH>(d) * d.b * d.L * 2 * d.N);
         w.d = w.a + (size_t)(d.b * d.D * d.N);
-        w.total = w.d + (size_t)(2 * d.b * d.D);
+        w.fwd = (w.d + (size_t)(2 * d.b * d.D) + 3) / 4 * 4;
+        w.total = w.fwd + selective_fwd_workspace_bytes(d) / 4;
     });
     return w;
 }
@@ -397,26 +440,30 @@ cudaError_t launch_selective_bwd(const SelectiveArgs& a, const SelectiveGrads& g
                                  const SelectiveDims& d, Elt t, cudaStream_t s) {
     const Work w = work_of(d);
     cudaError_t err = cudaSuccess;
+    if (d.b > 0 && d.L > 0) err = launch_selective_checkpoints(a, ws + w.ckpt, ws + w.fwd, d, t, s);
+    if (err != cudaSuccess) return err;
     with_elt(t, [&](auto ty) {
         using T = typename decltype(ty)::type;
         with_layout(d.N, [&](auto lay) {
             using Lay = decltype(lay);
+            using S = Bwd<T, Lay>;
             const int64_t nb = channel_blocks<Lay::CH>(d), blocks = d.b * nb;
-            const bool vec = selective_vec<T>(a, d, load_width<T, Lay::CH>());
-            if (blocks > 0) {
-                constexpr int smem = Bwd<Lay>::SMEM;
-                err = cudaFuncSetAttribute(scan_bwd_kernel<T, Lay>,
-                                           cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-                if (err != cudaSuccess) return;
-                if (d.L > 0)
-                    checkpoint_kernel<T, Lay><<<(unsigned)blocks, kThreads, 0, s>>>(a, ws + w.ckpt, d, vec);
-                scan_bwd_kernel<T, Lay><<<(unsigned)blocks, kThreads, smem, s>>>(
-                    a, g, ws + w.ckpt, ws + w.bc, ws + w.a, ws + w.d, d, vec);
-                if (d.L > 0) {
-                    const int64_t total = d.b * d.L * d.G * 2 * d.N, nblk = (total + 255) / 256;
-                    reduce_bc_kernel<T><<<(unsigned)(nblk < 148 * 16 ? nblk : 148 * 16), 256, 0, s>>>(
-                        ws + w.bc, static_cast<T*>(g.dB), static_cast<T*>(g.dC), d, nb / d.G);
-                }
+            if (blocks == 0) return;
+            auto go = [&](auto kernel) {
+                err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
+                if (err == cudaSuccess)
+                    kernel<<<(unsigned)blocks, kThreads, S::SMEM, s>>>(
+                        a, g, ws + w.ckpt, ws + w.bc, ws + w.a, ws + w.d, d);
+            };
+            if (selective_vec<T>(a, d, S::VW) && d.N % S::VB == 0 && rows_fit<T>(a.B, a.Bs, S::VB) &&
+                rows_fit<T>(a.C, a.Cs, S::VB))
+                go(scan_bwd_kernel<T, Lay, true>);
+            else
+                go(scan_bwd_kernel<T, Lay, false>);
+            if (err == cudaSuccess && d.L > 0) {
+                const int64_t total = d.b * d.L * d.G * 2 * d.N, nblk = (total + 255) / 256;
+                reduce_bc_kernel<T><<<(unsigned)(nblk < 148 * 16 ? nblk : 148 * 16), 256, 0, s>>>(
+                    ws + w.bc, static_cast<T*>(g.dB), static_cast<T*>(g.dC), d, nb / d.G);
             }
         });
     });
