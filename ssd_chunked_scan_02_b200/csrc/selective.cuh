@@ -110,6 +110,10 @@ __device__ __forceinline__ void fold(float* v, int lane) {
     }
 }
 
+// Tokens whose states the backward holds in registers at once; the states before
+// every TS-th token are its checkpoints.
+constexpr int kTS = 4;
+
 // Layout of (channel, state) over a block of 128 threads: LPC lanes a channel,
 // SPL neighbouring states a lane.  Few states a lane give more threads, many
 // spare the work that every lane of a channel repeats (loads of dt and u, sums
@@ -119,7 +123,6 @@ struct Layout {
     static constexpr int SPL = SPL_, LPC = LPC_, NP = SPL_ * LPC_;   // NP: N rounded up
     static constexpr int CH = 128 / LPC_;                            // channels of a block
     static constexpr int TT = NP <= 64 ? 32 : (NP == 128 ? 16 : 8);  // tokens of a tile
-    static constexpr int TS = 32 / SPL_;     // tokens whose states the backward holds in registers
 };
 
 inline int padded_states(int64_t N) {

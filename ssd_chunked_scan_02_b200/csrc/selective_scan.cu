@@ -142,7 +142,7 @@ scan_fwd_kernel(const SelectiveArgs a, T* __restrict__ y, float* __restrict__ fi
                 h[i] = pack2(hv[2 * i], hv[2 * i + 1]);
             }
         }
-        constexpr int TS = Lay::TS;
+        constexpr int TS = kTS;
         const int64_t nck = (d.L + TS - 1) / TS;
         float* ck = W == What::Checkpoints
                         ? final_states + ((pl.b * nck + first / TS) * d.D + pl.c0 + ch) * NP + lane * SPL

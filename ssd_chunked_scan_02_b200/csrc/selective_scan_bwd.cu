@@ -37,8 +37,12 @@ constexpr int kThreads = 128, kWarps = kThreads / 32;
 template <typename T, typename Lay>
 struct Bwd {
     static constexpr int NP = Lay::NP, CH = Lay::CH;
-    static constexpr int TT = NP <= 32 ? 32 : (NP == 64 ? 16 : 8);   // tokens of a tile
-    static constexpr int VW = load_width<T, CH>(), PER = CH / VW;
+    static constexpr int TT = NP <= 64 ? 16 : 8;                     // tokens of a tile
+    // channels of a load: as many as keep every thread busy
+    static constexpr int VW = TT * CH / kThreads < load_width<T, CH>()
+                                  ? (TT * CH / kThreads < 4 ? 4 : TT * CH / kThreads)
+                                  : load_width<T, CH>();
+    static constexpr int PER = CH / VW;
     static constexpr int IT = (TT * PER + kThreads - 1) / kThreads;  // loads a thread and tile
     static constexpr int VB = 16 / sizeof(T);
     static constexpr int NB = (TT * NP * 2 / VB + kThreads - 1) / kThreads;
@@ -46,7 +50,9 @@ struct Bwd {
     static constexpr int RAW = kThreads * (4 * IT * VW + NB * VB) * (int)sizeof(T);
     static constexpr int SMEM = 2 * RAW + TT * CH * 12 + 3 * TT * PY * 4 +
                                 TT * NP * 8 * (1 + kWarps) + 2 * kThreads * VW * 4;
-    static constexpr int BLOCKS = SMEM <= 75 * 1024 ? 3 : 2;         // of an SM
+    // blocks of an SM: five (102 registers a thread) hold the four states a lane of
+    // the smaller layouts, three the eight of the larger
+    static constexpr int BLOCKS = Lay::SPL == 4 && SMEM <= 44 * 1024 ? 5 : SMEM <= 75 * 1024 ? 3 : 2;
 };
 
 // ------------------------------------------------------------------ the reverse walk
@@ -57,11 +63,11 @@ scan_bwd_kernel(const SelectiveArgs a, const SelectiveGrads gr, const float* __r
                 float* __restrict__ part_bc, float* __restrict__ part_a,
                 float* __restrict__ part_d, const SelectiveDims d) {
     using S = Bwd<T, Lay>;
-    constexpr int SPL = Lay::SPL, LPC = Lay::LPC, NP = Lay::NP, CH = Lay::CH, TS = Lay::TS;
+    constexpr int SPL = Lay::SPL, LPC = Lay::LPC, NP = Lay::NP, CH = Lay::CH, TS = kTS;
     constexpr int TT = S::TT, VW = S::VW, PER = S::PER, IT = S::IT, VB = S::VB, NB = S::NB;
-    constexpr int PY = S::PY, SWZ = (CH < 8 ? CH : 8) - 1;
+    constexpr int PY = S::PY;
     constexpr int CPW = 32 / LPC;                               // channels of a warp
-    constexpr int FG = 16 / SPL;                                // tokens of a sum over channels
+    constexpr int FG = 2;                                       // tokens of a sum over channels
     constexpr int NG = 4;                                       // tokens of a sum over states
     using RV = Raw<T, VW>;
     using RB = Raw<T, VB>;
@@ -76,7 +82,7 @@ scan_bwd_kernel(const SelectiveArgs a, const SelectiveGrads gr, const float* __r
     float* s_B = reinterpret_cast<float*>(s_du + TT * CH);      // [TT][NP] each
     float* s_C = s_B + TT * NP;
     float* s_red = s_C + TT * NP;                               // [warps][TT][2][NP]
-    float* s_sum = s_red + kWarps * TT * 2 * NP;                // [2][threads][VW]: dD, ddt_bias
+    float* s_sum = s_red + kWarps * TT * 2 * NP;                // [2][VW][threads]: dD, ddt_bias
     float* s_y = s_sum + 2 * kThreads * VW;                     // [TT][PY] each
     float* s_dtg = s_y + TT * PY;                               // du = sum B g
     float* s_q = s_dtg + TT * PY;
@@ -166,18 +172,27 @@ scan_bwd_kernel(const SelectiveArgs a, const SelectiveGrads gr, const float* __r
             const RV rx = r_x[o], rdt = r_dt[o], rdy = r_dy[o];
             RV rz;
             if (z) rz = r_z[o];
+            float dl[VW], u[VW], gy[VW];
 #pragma unroll
             for (int j = 0; j < VW; ++j) {
-                float v = to_f32(rdt.v[j]) + bias(c + j), gy = to_f32(rdy.v[j]);
+                float v = to_f32(rdt.v[j]) + bias(c + j);
+                gy[j] = to_f32(rdy.v[j]);
                 if (a.softplus) v = softplus_f32(v);
                 if (z) {
                     const float zv = to_f32(rz.v[j]);
-                    gy *= zv * sigmoid_fast(zv);
+                    gy[j] *= zv * sigmoid_fast(zv);
                 }
-                float u = v * to_f32(rx.v[j]);
-                if (j >= n) v = u = gy = 0.f;
-                s_du[tl * CH + ((c + j) ^ (i & SWZ))] = make_float2(v * kLog2E, u);
-                s_g[tl * CH + c + j] = gy;
+                u[j] = v * to_f32(rx.v[j]);
+                if (j >= n) v = u[j] = gy[j] = 0.f;
+                dl[j] = v * kLog2E;
+            }
+#pragma unroll
+            for (int j = 0; j < VW; j += 4) {
+                float4* q = reinterpret_cast<float4*>(s_du + tl * CH + c + j);
+                q[0] = make_float4(dl[j], u[j], dl[j + 1], u[j + 1]);
+                q[1] = make_float4(dl[j + 2], u[j + 2], dl[j + 3], u[j + 3]);
+                *reinterpret_cast<float4*>(s_g + tl * CH + c + j) =
+                    make_float4(gy[j], gy[j + 1], gy[j + 2], gy[j + 3]);
             }
         }
         if constexpr (Vec) {
@@ -234,7 +249,7 @@ scan_bwd_kernel(const SelectiveArgs a, const SelectiveGrads gr, const float* __r
             fetch(t0 + tt - TS);
 #pragma unroll
             for (int k = 0; k < TS; ++k) {
-                const float2 q = s_du[(tt + k) * CH + (ch ^ (((tt + k) * PER + ch / VW) & SWZ))];
+                const float2 q = s_du[(tt + k) * CH + ch];
                 const F2 dd = pack2(q.x, q.x), uu = pack2(q.y, q.y);
                 const float* Bt = s_B + (tt + k) * NP + lane * SPL;
 #pragma unroll
@@ -249,32 +264,37 @@ scan_bwd_kernel(const SelectiveArgs a, const SelectiveGrads gr, const float* __r
             F2 at[SPL / 2];
 #pragma unroll
             for (int i = 0; i < SPL / 2; ++i) at[i] = 0;
-            float py[NG], pu[NG], pq[NG], pB[16], pC[16];
+            float py[NG], pu[NG], pq[NG], pB[FG * SPL], pC[FG * SPL];
 #pragma unroll
             for (int k = TS - 1; k >= 0; --k) {
-                const float2 q = s_du[(tt + k) * CH + (ch ^ (((tt + k) * PER + ch / VW) & SWZ))];
+                const float2 q = s_du[(tt + k) * CH + ch];
                 const float gy = s_g[(tt + k) * CH + ch];
                 const F2 dd = pack2(q.x, q.x), uu = pack2(q.y, q.y), gg = pack2(gy, gy);
                 const float* Bt = s_B + (tt + k) * NP + lane * SPL;
                 const float* Ct = s_C + (tt + k) * NP + lane * SPL;
                 F2 sy = 0, su = 0, sq = 0;
 #pragma unroll
-                for (int i = 0; i < SPL / 2; ++i) {
-                    const float2 b2 = *reinterpret_cast<const float2*>(Bt + 2 * i);
-                    const float2 c2 = *reinterpret_cast<const float2*>(Ct + 2 * i);
-                    const F2 Bv = pack2(b2.x, b2.y), Cv = pack2(c2.x, c2.y);
-                    g[i] = fma2(gg, Cv, g[i]);
-                    sy = i == 0 ? mul2(Cv, h[k + 1][0]) : fma2(Cv, h[k + 1][i], sy);
-                    su = i == 0 ? mul2(Bv, g[0]) : fma2(Bv, g[i], su);
-                    const float2 dc = unpack2(mul2(gg, h[k + 1][i])), db = unpack2(mul2(uu, g[i]));
-                    pC[k % FG * SPL + 2 * i] = dc.x;
-                    pC[k % FG * SPL + 2 * i + 1] = dc.y;
-                    pB[k % FG * SPL + 2 * i] = db.x;
-                    pB[k % FG * SPL + 2 * i + 1] = db.y;
-                    g[i] = mul2(g[i], e[k][i]);
-                    const F2 qv = mul2(g[i], h[k][i]);
-                    sq = i == 0 ? mul2(A[0], qv) : fma2(A[i], qv, sq);
-                    at[i] = fma2(dd, qv, at[i]);
+                for (int i4 = 0; i4 < SPL; i4 += 4) {
+                    const float4 b4 = *reinterpret_cast<const float4*>(Bt + i4);
+                    const float4 c4 = *reinterpret_cast<const float4*>(Ct + i4);
+                    const F2 Bv[2] = {pack2(b4.x, b4.y), pack2(b4.z, b4.w)};
+                    const F2 Cv[2] = {pack2(c4.x, c4.y), pack2(c4.z, c4.w)};
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const int i = i4 / 2 + j;
+                        g[i] = fma2(gg, Cv[j], g[i]);
+                        sy = i == 0 ? mul2(Cv[j], h[k + 1][i]) : fma2(Cv[j], h[k + 1][i], sy);
+                        su = i == 0 ? mul2(Bv[j], g[i]) : fma2(Bv[j], g[i], su);
+                        const float2 dc = unpack2(mul2(gg, h[k + 1][i])), db = unpack2(mul2(uu, g[i]));
+                        pC[k % FG * SPL + 2 * i] = dc.x;
+                        pC[k % FG * SPL + 2 * i + 1] = dc.y;
+                        pB[k % FG * SPL + 2 * i] = db.x;
+                        pB[k % FG * SPL + 2 * i + 1] = db.y;
+                        g[i] = mul2(g[i], e[k][i]);
+                        const F2 qv = mul2(g[i], h[k][i]);
+                        sq = i == 0 ? mul2(A[i], qv) : fma2(A[i], qv, sq);
+                        at[i] = fma2(dd, qv, at[i]);
+                    }
                 }
                 const float2 fy = unpack2(sy), fu = unpack2(su), fq = unpack2(sq);
                 py[k % NG] = fy.x + fy.y;
@@ -283,14 +303,18 @@ scan_bwd_kernel(const SelectiveArgs a, const SelectiveGrads gr, const float* __r
                 if (k % FG == 0) {
                     // over a warp's channels: the lanes of one place in the channel lie LPC apart
                     const int place = tid % 32 / LPC;
-                    fold<16, CPW, LPC>(pB, place);
-                    fold<16, CPW, LPC>(pC, place);
-                    constexpr int NV = 16 / CPW;
+                    constexpr int ALL = FG * SPL, NV = ALL >= CPW ? ALL / CPW : 1;
+                    constexpr int SH = ALL >= CPW ? 1 : CPW / ALL;
+                    fold<ALL, CPW, LPC>(pB, place);
+                    fold<ALL, CPW, LPC>(pC, place);
+                    if (place % SH == 0) {
 #pragma unroll
-                    for (int i = 0; i < NV; ++i) {
-                        const int v = place * NV + i, t = tt + k + v / SPL, n = lane * SPL + v % SPL;
-                        s_red[((warp * TT + t) * 2 + 0) * NP + n] = pB[i];
-                        s_red[((warp * TT + t) * 2 + 1) * NP + n] = pC[i];
+                        for (int i = 0; i < NV; ++i) {
+                            const int v = place / SH * NV + i, t = tt + k + v / SPL, n = lane * SPL + v % SPL;
+                            float* q = s_red + (warp * TT + t) * 2 * NP + n;
+                            q[(t & 1) * NP] = pB[i];            // odd tokens: dC first, so that
+                            q[(t & 1 ^ 1) * NP] = pC[i];        // two tokens meet no bank twice
+                        }
                     }
                 }
                 if (k % NG == 0) {
@@ -315,13 +339,18 @@ scan_bwd_kernel(const SelectiveArgs a, const SelectiveGrads gr, const float* __r
         }
         __syncthreads();
 
-        for (int i = tid; i < TT * 2 * NP; i += kThreads) {
-            const int t = t0 + i / (2 * NP), n = i % NP, which = i / NP % 2;
-            float v = 0.f;
+        for (int i = tid * 4; i < TT * 2 * NP; i += 4 * kThreads) {
+            const int t = t0 + i / (2 * NP), col = i % (2 * NP);
+            if (t < L) {
+                float4 v = *reinterpret_cast<const float4*>(s_red + i);
 #pragma unroll
-            for (int k = 0; k < kWarps; ++k) v += s_red[k * TT * 2 * NP + i];
-            if (t < L && n < d.N)
-                part_bc[(((cb * d.b + pl.b) * d.L + t) * 2 + which) * d.N + n] = v;
+                for (int k = 1; k < kWarps; ++k) {
+                    const float4 o = *reinterpret_cast<const float4*>(s_red + k * TT * 2 * NP + i);
+                    v.x += o.x; v.y += o.y; v.z += o.z; v.w += o.w;
+                }
+                *reinterpret_cast<float4*>(part_bc + ((cb * d.b + pl.b) * d.L + t) * 2 * NP +
+                                           (col ^ (t & 1) * NP)) = v;
+            }
         }
 #pragma unroll
         for (int k = 0; k < IT; ++k) {
@@ -333,24 +362,32 @@ scan_bwd_kernel(const SelectiveArgs a, const SelectiveGrads gr, const float* __r
             if (z) rz = r_z[o];
             float ox[VW], ot[VW], oz[VW];
 #pragma unroll
-            for (int j = 0; j < VW; ++j) {
-                const float xv = to_f32(rx.v[j]), gy = s_g[tl * CH + c + j], Dv = skip(c + j);
-                const float dl = s_du[tl * CH + ((c + j) ^ (i & SWZ))].x;
-                const float du = s_dtg[tl * PY + c + j];
-                ox[j] = fmaf(dl * kLn2, du, Dv * gy);
-                ot[j] = fmaf(du, xv, s_q[tl * PY + c + j]);
-                if (a.softplus) ot[j] *= sigmoid_fast(to_f32(rdt.v[j]) + bias(c + j));
-                oz[j] = 0.f;
-                if (z) {
-                    const float zv = to_f32(rz.v[j]), sg = sigmoid_fast(zv);
-                    oz[j] = to_f32(rdy.v[j]) * fmaf(Dv, xv, s_y[tl * PY + c + j]) * sg *
-                            fmaf(zv, 1.f - sg, 1.f);
-                }
-                if (j >= n) {
-                    ox[j] = ot[j] = oz[j] = 0.f;
-                } else {
-                    s_sum[tid * VW + j] = fmaf(gy, xv, s_sum[tid * VW + j]);
-                    s_sum[(kThreads + tid) * VW + j] += ot[j];
+            for (int j4 = 0; j4 < VW; j4 += 4) {
+                const float4 du4 = *reinterpret_cast<const float4*>(s_dtg + tl * PY + c + j4);
+                const float4 q4 = *reinterpret_cast<const float4*>(s_q + tl * PY + c + j4);
+                const float4 g4 = *reinterpret_cast<const float4*>(s_g + tl * CH + c + j4);
+                const float4 y4 = *reinterpret_cast<const float4*>(s_y + tl * PY + c + j4);
+                const float4 d0 = reinterpret_cast<const float4*>(s_du + tl * CH + c + j4)[0];
+                const float4 d1 = reinterpret_cast<const float4*>(s_du + tl * CH + c + j4)[1];
+                const float du[4] = {du4.x, du4.y, du4.z, du4.w}, q[4] = {q4.x, q4.y, q4.z, q4.w};
+                const float gy[4] = {g4.x, g4.y, g4.z, g4.w}, yv[4] = {y4.x, y4.y, y4.z, y4.w};
+                const float dl[4] = {d0.x, d0.z, d1.x, d1.z};
+#pragma unroll
+                for (int jj = 0; jj < 4; ++jj) {
+                    const int j = j4 + jj;
+                    const float xv = to_f32(rx.v[j]), Dv = skip(c + j);
+                    ox[j] = fmaf(dl[jj] * kLn2, du[jj], Dv * gy[jj]);
+                    ot[j] = fmaf(du[jj], xv, q[jj]);
+                    if (a.softplus) ot[j] *= sigmoid_fast(to_f32(rdt.v[j]) + bias(c + j));
+                    oz[j] = 0.f;
+                    if (z) {
+                        const float zv = to_f32(rz.v[j]), sg = sigmoid_fast(zv);
+                        oz[j] = to_f32(rdy.v[j]) * fmaf(Dv, xv, yv[jj]) * sg * fmaf(zv, 1.f - sg, 1.f);
+                    }
+                    float gx = gy[jj] * xv;
+                    if (j >= n) ox[j] = ot[j] = oz[j] = gx = 0.f;
+                    s_sum[j * kThreads + tid] += gx;
+                    s_sum[(VW + j) * kThreads + tid] += ot[j];
                 }
             }
             const int left = pl.count - c;
@@ -383,24 +420,34 @@ scan_bwd_kernel(const SelectiveArgs a, const SelectiveGrads gr, const float* __r
         const int c = i % CH, which = i / CH;
         if (c >= pl.count) continue;
         float v = 0.f;
-        for (int q = c / VW; q < kThreads; q += PER) v += s_sum[(which * kThreads + q) * VW + c % VW];
+        for (int q = c / VW; q < kThreads; q += PER) v += s_sum[(which * VW + c % VW) * kThreads + q];
         part_d[((int64_t)which * d.b + pl.b) * d.D + pl.c0 + c] = v;
     }
 }
 
-// dB, dC (b,L,G,N): the sum of a group's channel blocks' partial rows.
+// dB, dC (b,L,G,N): the sum of a group's channel blocks' partial rows
+// (blocks, b, L, 2, NP), four states a thread, several rows in flight.
 template <typename T>
 __global__ void __launch_bounds__(256)
 reduce_bc_kernel(const float* __restrict__ part, T* __restrict__ dB, T* __restrict__ dC,
-                 const SelectiveDims d, int64_t per_group) {
-    const int64_t tokens = d.b * d.L, total = tokens * d.G * 2 * d.N;
+                 const SelectiveDims d, int64_t per_group, int NP) {
+    const int64_t tokens = d.b * d.L, row = 2 * NP, total = tokens * d.G * row / 4;
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
-        const int64_t n = i % d.N, which = i / d.N % 2, tok = i / (2 * d.N) % tokens,
-                      g = i / (2 * d.N * tokens);
-        float v = 0.f;
-        for (int64_t k = 0; k < per_group; ++k)
-            v += part[(((g * per_group + k) * tokens + tok) * 2 + which) * d.N + n];
-        (which ? dC : dB)[(tok * d.G + g) * d.N + n] = from_f32<T>(v);
+        const int64_t at = i * 4 % (tokens * row), g = i * 4 / (tokens * row);
+        const int64_t tok = at / row, n = at % NP;
+        const bool isC = at % row >= NP;
+        const float4* p = reinterpret_cast<const float4*>(part + g * per_group * tokens * row + at);
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+        for (int64_t k = 0; k < per_group; ++k) {
+            const float4 o = __ldcs(p + k * (tokens * row / 4));
+            v.x += o.x; v.y += o.y; v.z += o.z; v.w += o.w;
+        }
+        T* out = (isC ? dC : dB) + (tok * d.G + g) * d.N + n;
+        if (n < d.N) out[0] = from_f32<T>(v.x);
+        if (n + 1 < d.N) out[1] = from_f32<T>(v.y);
+        if (n + 2 < d.N) out[2] = from_f32<T>(v.z);
+        if (n + 3 < d.N) out[3] = from_f32<T>(v.w);
     }
 }
 
@@ -421,10 +468,10 @@ Work work_of(const SelectiveDims& d) {
     Work w{};
     with_layout(d.N, [&](auto lay) {
         using Lay = decltype(lay);
-        const int64_t TS = Lay::TS;
+        const int64_t TS = kTS;
         w.ckpt = 0;
         w.bc = w.ckpt + (size_t)(d.b * ((d.L + TS - 1) / TS) * d.D * Lay::NP);
-        w.a = w.bc + (size_t)(channel_blocks<Lay::CH>(d) * d.b * d.L * 2 * d.N);
+        w.a = w.bc + (size_t)(channel_blocks<Lay::CH>(d) * d.b * d.L * 2 * Lay::NP);
         w.d = w.a + (size_t)(d.b * d.D * d.N);
         w.fwd = (w.d + (size_t)(2 * d.b * d.D) + 3) / 4 * 4;
         w.total = w.fwd + selective_fwd_workspace_bytes(d) / 4;
@@ -461,9 +508,10 @@ cudaError_t launch_selective_bwd(const SelectiveArgs& a, const SelectiveGrads& g
             else
                 go(scan_bwd_kernel<T, Lay, false>);
             if (err == cudaSuccess && d.L > 0) {
-                const int64_t total = d.b * d.L * d.G * 2 * d.N, nblk = (total + 255) / 256;
+                const int64_t total = d.b * d.L * d.G * 2 * Lay::NP / 4, nblk = (total + 255) / 256;
                 reduce_bc_kernel<T><<<(unsigned)(nblk < 148 * 16 ? nblk : 148 * 16), 256, 0, s>>>(
-                    ws + w.bc, static_cast<T*>(g.dB), static_cast<T*>(g.dC), d, nb / d.G);
+                    ws + w.bc, static_cast<T*>(g.dB), static_cast<T*>(g.dC), d, nb / d.G,
+                    Lay::NP);
             }
         });
     });
