@@ -61,6 +61,8 @@ ssd_status_t selective_dims(const ssd_selective_dims_t* dims, ssd_dtype_t dtype,
         return fail(SSD_ERR_INVALID_ARG, "channels (%lld) must be a multiple of ngroups (%lld)",
                     (long long)dims->channels, (long long)dims->ngroups);
     if (dims->dstate > 256) return fail(SSD_ERR_UNSUPPORTED, "dstate must be <= 256");
+    if (dims->channels > kMaxSize)
+        return fail(SSD_ERR_UNSUPPORTED, "channels must be below 2^31");
     // at most a block a channel and sequence
     if ((double)dims->batch * (double)dims->channels > (double)kMaxSize)
         return fail(SSD_ERR_UNSUPPORTED, "batch * channels exceeds the launch grid");
@@ -112,6 +114,22 @@ ssd_status_t check_view(const void* p, const char* name, ssd::Elt t) {
 
 ssd::Stride stride_of(const ssd_stride_t& s) { return ssd::Stride{s.batch, s.token}; }
 
+// Tokens of a view lie less than 2^31 elements apart (kernels keep the distance
+// in 32 bits), and not in descending order.
+ssd_status_t check_stride(const ssd_stride_t& s, const char* name) {
+    if (s.token < 0 || s.batch < 0)
+        return fail(SSD_ERR_INVALID_ARG, "%s strides must be >= 0", name);
+    if (s.token > kMaxSize)
+        return fail(SSD_ERR_UNSUPPORTED, "%s token stride must be below 2^31", name);
+    return SSD_OK;
+}
+
+#define CHECK_STRIDE(s, name)                                                            \
+    do {                                                                                 \
+        ssd_status_t st_stride_ = check_stride((s), name);                               \
+        if (st_stride_ != SSD_OK) return st_stride_;                                     \
+    } while (0)
+
 }  // namespace
 
 extern "C" {
@@ -128,6 +146,7 @@ ssd_status_t ssd_causal_conv_fwd(const void* x, const ssd_stride_t* x_stride,
     OPTIONAL_PTR(bias); OPTIONAL_PTR(init_state); OPTIONAL_PTR(final_state);
     REQUIRE_LENS(seq_lens);
     REQUIRE_STRIDE(x_stride);
+    CHECK_STRIDE(*x_stride, "x");
     if (d.b == 0 || (d.L == 0 && !final_state)) return SSD_OK;
     REQUIRE_PTR(weight);
     if (d.L > 0) {
@@ -167,6 +186,7 @@ ssd_status_t ssd_causal_conv_bwd(const void* x, const ssd_stride_t* x_stride,
     OPTIONAL_PTR(dinit_state);
     REQUIRE_LENS(seq_lens);
     REQUIRE_STRIDE(x_stride);
+    CHECK_STRIDE(*x_stride, "x");
     REQUIRE_PTR(weight); REQUIRE_PTR(dweight); REQUIRE_PTR(dbias);
     if (d.b > 0 && d.L > 0) {
         REQUIRE_VIEW(x);
@@ -199,6 +219,7 @@ ssd_status_t ssd_causal_conv_step(void* state, const void* x, const ssd_stride_t
     if (st != SSD_OK) return st;
     OPTIONAL_PTR(bias);
     REQUIRE_STRIDE(x_stride);
+    CHECK_STRIDE(*x_stride, "x");
     if (d.b == 0) return SSD_OK;
     REQUIRE_PTR(state); REQUIRE_PTR(weight); REQUIRE_PTR(y);
     REQUIRE_VIEW(x);
@@ -245,6 +266,9 @@ ssd_status_t ssd_selective_scan_fwd(const void* x, const void* dt, const float* 
     OPTIONAL_PTR(D); OPTIONAL_PTR(dt_bias); OPTIONAL_PTR(init_states); OPTIONAL_PTR(final_states);
     REQUIRE_LENS(seq_lens);
     REQUIRE_STRIDE(strides);
+    CHECK_STRIDE(strides->x, "x"); CHECK_STRIDE(strides->dt, "dt");
+    CHECK_STRIDE(strides->B, "B"); CHECK_STRIDE(strides->C, "C");
+    if (z) CHECK_STRIDE(strides->z, "z");
     if (d.b == 0 || (d.L == 0 && !final_states)) return SSD_OK;
     REQUIRE_PTR(A);
     if (d.L > 0) {
@@ -294,6 +318,9 @@ ssd_status_t ssd_selective_scan_bwd(const void* x, const void* dt, const float* 
     OPTIONAL_PTR(dinit_states);
     REQUIRE_LENS(seq_lens);
     REQUIRE_STRIDE(strides);
+    CHECK_STRIDE(strides->x, "x"); CHECK_STRIDE(strides->dt, "dt");
+    CHECK_STRIDE(strides->B, "B"); CHECK_STRIDE(strides->C, "C");
+    if (z) CHECK_STRIDE(strides->z, "z");
     REQUIRE_PTR(A); REQUIRE_PTR(dA);
     if (d.b > 0 && d.L > 0) {
         REQUIRE_VIEW(x); REQUIRE_VIEW(dt); REQUIRE_VIEW(B); REQUIRE_VIEW(C);
@@ -329,6 +356,9 @@ ssd_status_t ssd_selective_step(float* state, const void* x, const void* dt, con
     if (st != SSD_OK) return st;
     OPTIONAL_PTR(D); OPTIONAL_PTR(dt_bias);
     REQUIRE_STRIDE(strides);
+    CHECK_STRIDE(strides->x, "x"); CHECK_STRIDE(strides->dt, "dt");
+    CHECK_STRIDE(strides->B, "B"); CHECK_STRIDE(strides->C, "C");
+    if (z) CHECK_STRIDE(strides->z, "z");
     if (d.b == 0) return SSD_OK;
     REQUIRE_PTR(state); REQUIRE_PTR(A); REQUIRE_PTR(y);
     REQUIRE_VIEW(x); REQUIRE_VIEW(dt); REQUIRE_VIEW(B); REQUIRE_VIEW(C);
@@ -354,6 +384,7 @@ ssd_status_t ssd_bc_norm_rotate_fwd(const void* B, const ssd_stride_t* B_stride,
     if (st != SSD_OK) return st;
     if (!(eps >= 0.f)) return fail(SSD_ERR_INVALID_ARG, "eps must be >= 0");
     REQUIRE_STRIDE(B_stride); REQUIRE_STRIDE(C_stride);
+    CHECK_STRIDE(*B_stride, "B"); CHECK_STRIDE(*C_stride, "C");
     if (d.b == 0 || d.L == 0) return SSD_OK;
     REQUIRE_VIEW(B); REQUIRE_VIEW(C);
     REQUIRE_PTR(B_weight); REQUIRE_PTR(C_weight); REQUIRE_PTR(B_out); REQUIRE_PTR(C_out);
@@ -392,6 +423,7 @@ ssd_status_t ssd_bc_norm_rotate_bwd(const void* B, const ssd_stride_t* B_stride,
     if (st != SSD_OK) return st;
     if (!(eps >= 0.f)) return fail(SSD_ERR_INVALID_ARG, "eps must be >= 0");
     REQUIRE_STRIDE(B_stride); REQUIRE_STRIDE(C_stride);
+    CHECK_STRIDE(*B_stride, "B"); CHECK_STRIDE(*C_stride, "C");
     REQUIRE_PTR(B_weight); REQUIRE_PTR(C_weight);
     REQUIRE_PTR(dB_weight); REQUIRE_PTR(dC_weight);
     if (d.b > 0 && d.L > 0) {

@@ -45,14 +45,15 @@ struct Bwd {
     static constexpr int PER = CH / VW;
     static constexpr int IT = (TT * PER + kThreads - 1) / kThreads;  // loads a thread and tile
     static constexpr int VB = 16 / sizeof(T);
-    static constexpr int NB = (TT * NP * 2 / VB + kThreads - 1) / kThreads;
+    static constexpr int BCV = TT * NP * 2 / VB;                     // loads of B and C
+    static constexpr int NB = (BCV + kThreads - 1) / kThreads;
     static constexpr int PY = CH + 8;                                // a row of results
-    static constexpr int RAW = kThreads * (4 * IT * VW + NB * VB) * (int)sizeof(T);
+    static constexpr int RAW = (kThreads * 4 * IT * VW + BCV * VB) * (int)sizeof(T);
     static constexpr int SMEM = 2 * RAW + TT * CH * 12 + 3 * TT * PY * 4 +
-                                TT * NP * 8 * (1 + kWarps) + 2 * kThreads * VW * 4;
+                                TT * NP * 8 * (1 + kWarps) + 2 * kThreads * VW * 4 + 2 * CH * 4;
     // blocks of an SM: five (102 registers a thread) hold the four states a lane of
     // the smaller layouts, three the eight of the larger
-    static constexpr int BLOCKS = Lay::SPL == 4 && SMEM <= 44 * 1024 ? 5 : SMEM <= 75 * 1024 ? 3 : 2;
+    static constexpr int BLOCKS = Lay::SPL == 4 && SMEM <= 45670 ? 5 : SMEM <= 75 * 1024 ? 3 : 2;
 };
 
 // ------------------------------------------------------------------ the reverse walk
@@ -73,20 +74,22 @@ scan_bwd_kernel(const SelectiveArgs a, const SelectiveGrads gr, const float* __r
     using RB = Raw<T, VB>;
     extern __shared__ __align__(16) unsigned char smem[];
     // two tiles as they come: a thread copies and reads its own elements
-    RB* r_bc = reinterpret_cast<RB*>(smem);                     // [2][NB][threads]
-    RV* r_x = reinterpret_cast<RV*>(r_bc + 2 * NB * kThreads);  // [2][IT][threads] each
+    RB* r_bc = reinterpret_cast<RB*>(smem);                     // [2][BCV]
+    RV* r_x = reinterpret_cast<RV*>(r_bc + 2 * S::BCV);  // [2][IT][threads] each
     RV* r_dt = r_x + 2 * IT * kThreads;
     RV* r_z = r_dt + 2 * IT * kThreads;
     RV* r_dy = r_z + 2 * IT * kThreads;
     float2* s_du = reinterpret_cast<float2*>(r_dy + 2 * IT * kThreads);   // [TT][CH]: dt log2(e), u
-    float* s_B = reinterpret_cast<float*>(s_du + TT * CH);      // [TT][NP] each
+    float* s_g = reinterpret_cast<float*>(s_du + TT * CH);      // [TT][CH]: dyg
+    float* s_B = s_g + TT * CH;                                 // [TT][NP] each
     float* s_C = s_B + TT * NP;
     float* s_red = s_C + TT * NP;                               // [warps][TT][2][NP]
     float* s_sum = s_red + kWarps * TT * 2 * NP;                // [2][VW][threads]: dD, ddt_bias
     float* s_y = s_sum + 2 * kThreads * VW;                     // [TT][PY] each
     float* s_dtg = s_y + TT * PY;                               // du = sum B g
     float* s_q = s_dtg + TT * PY;
-    float* s_g = s_q + TT * PY;                                 // [TT][CH]: dyg
+    float* s_bias = s_q + TT * PY;                              // [CH] each
+    float* s_skip = s_bias + CH;
 
     const Place pl = place_of<CH>(blockIdx.x, d);
     const int tid = threadIdx.x, lane = tid % LPC, ch = tid / LPC, warp = tid / 32;
@@ -107,8 +110,10 @@ scan_bwd_kernel(const SelectiveArgs a, const SelectiveGrads gr, const float* __r
 
     for (int i = tid; i < 2 * TT * NP; i += kThreads) s_B[i] = 0.f;       // states beyond N
     for (int i = tid; i < 2 * kThreads * VW; i += kThreads) s_sum[i] = 0.f;
-    auto bias = [&](int c) { return a.dt_bias && c < pl.count ? __ldg(a.dt_bias + pl.c0 + c) : 0.f; };
-    auto skip = [&](int c) { return a.D && c < pl.count ? __ldg(a.D + pl.c0 + c) : 0.f; };
+    for (int c = tid; c < CH; c += kThreads) {
+        s_bias[c] = a.dt_bias && c < pl.count ? a.dt_bias[pl.c0 + c] : 0.f;
+        s_skip[c] = a.D && c < pl.count ? a.D[pl.c0 + c] : 0.f;
+    }
 
     F2 A[SPL / 2], g[SPL / 2], dA[SPL / 2];
     {
@@ -129,6 +134,9 @@ scan_bwd_kernel(const SelectiveArgs a, const SelectiveGrads gr, const float* __r
     }
 
     const int nvb = Vec ? (int)d.N / VB : 1;
+    // token strides below 2^31: one wide multiply-add an address
+    const int xt = (int)a.xs.token, dtt = (int)a.dts.token, zt = (int)a.zs.token,
+              Bt_ = (int)a.Bs.token, Ct_ = (int)a.Cs.token, Dt = (int)d.D;
     auto load = [&](int t0, int w) {
         if constexpr (Vec) {
 #pragma unroll
@@ -136,21 +144,21 @@ scan_bwd_kernel(const SelectiveArgs a, const SelectiveGrads gr, const float* __r
                 const int i = k * kThreads + tid, t = t0 + i / PER, c = i % PER * VW;
                 const int o = (w * IT + k) * kThreads + tid;
                 const bool in = i / PER < TT && t < own && c < pl.count;
-                const int64_t r = in ? t : 0;
-                const int cc = in ? c : 0;
-                copy_async(r_x + o, x + r * a.xs.token + cc, in);
-                copy_async(r_dt + o, dt + r * a.dts.token + cc, in);
-                copy_async(r_dy + o, dy + r * d.D + cc, in);
-                if (z) copy_async(r_z + o, z + r * a.zs.token + cc, in);
+                const int r = in ? t : 0, cc = in ? c : 0;
+                copy_async(r_x + o, x + (int64_t)r * xt + cc, in);
+                copy_async(r_dt + o, dt + (int64_t)r * dtt + cc, in);
+                copy_async(r_dy + o, dy + (int64_t)r * Dt + cc, in);
+                if (z) copy_async(r_z + o, z + (int64_t)r * zt + cc, in);
             }
 #pragma unroll
             for (int k = 0; k < NB; ++k) {
                 const int i = k * kThreads + tid, t = t0 + i / (2 * nvb), v = i % (2 * nvb);
                 const bool in = i / (2 * nvb) < TT && t < own;
-                const int64_t r = in ? t : 0;
-                copy_async(r_bc + (w * NB + k) * kThreads + tid,
-                           v < nvb ? Bp + r * a.Bs.token + v * VB : Cp + r * a.Cs.token + (v - nvb) * VB,
-                           in);
+                const int r = in ? t : 0;
+                if (i < S::BCV)
+                    copy_async(r_bc + w * S::BCV + i,
+                               v < nvb ? Bp + (int64_t)r * Bt_ + v * VB
+                                       : Cp + (int64_t)r * Ct_ + (v - nvb) * VB, in);
             }
             copies_commit();
         }
@@ -166,7 +174,7 @@ scan_bwd_kernel(const SelectiveArgs a, const SelectiveGrads gr, const float* __r
             if constexpr (!Vec) {
                 r_x[o] = load_channels<T, VW>(x + (int64_t)t * a.xs.token + c, n, false);
                 r_dt[o] = load_channels<T, VW>(dt + (int64_t)t * a.dts.token + c, n, false);
-                r_dy[o] = load_channels<T, VW>(dy + (int64_t)t * d.D + c, n, false);
+                r_dy[o] = load_channels<T, VW>(dy + (int64_t)t * Dt + c, n, false);
                 if (z) r_z[o] = load_channels<T, VW>(z + (int64_t)t * a.zs.token + c, n, false);
             }
             const RV rx = r_x[o], rdt = r_dt[o], rdy = r_dy[o];
@@ -175,7 +183,7 @@ scan_bwd_kernel(const SelectiveArgs a, const SelectiveGrads gr, const float* __r
             float dl[VW], u[VW], gy[VW];
 #pragma unroll
             for (int j = 0; j < VW; ++j) {
-                float v = to_f32(rdt.v[j]) + bias(c + j);
+                float v = to_f32(rdt.v[j]) + s_bias[c + j];
                 gy[j] = to_f32(rdy.v[j]);
                 if (a.softplus) v = softplus_f32(v);
                 if (z) {
@@ -201,7 +209,7 @@ scan_bwd_kernel(const SelectiveArgs a, const SelectiveGrads gr, const float* __r
                 const int i = k * kThreads + tid, tl = i / (2 * nvb), v = i % (2 * nvb);
                 if (tl < TT) {
                     float f[VB];
-                    raw_to_f32(t0 + tl < own ? r_bc[(w * NB + k) * kThreads + tid] : raw_zero<T, VB>(), f);
+                    raw_to_f32(t0 + tl < own ? r_bc[w * S::BCV + i] : raw_zero<T, VB>(), f);
                     float* q = v < nvb ? s_B + tl * NP + v * VB : s_C + tl * NP + (v - nvb) * VB;
 #pragma unroll
                     for (int j = 0; j < VB; j += 4)
@@ -230,7 +238,7 @@ scan_bwd_kernel(const SelectiveArgs a, const SelectiveGrads gr, const float* __r
     if (ntile > 0) {
         load((ntile - 1) * TT, (ntile - 1) & 1);
         fetch(ntile * TT - TS);
-        __syncthreads();                                        // s_B's zeros
+        __syncthreads();                                        // s_B's zeros, s_bias
     }
     for (int tile = ntile - 1; tile >= 0; --tile) {
         const int t0 = tile * TT, w = tile & 1;
@@ -365,8 +373,8 @@ scan_bwd_kernel(const SelectiveArgs a, const SelectiveGrads gr, const float* __r
             for (int j4 = 0; j4 < VW; j4 += 4) {
                 const float4 du4 = *reinterpret_cast<const float4*>(s_dtg + tl * PY + c + j4);
                 const float4 q4 = *reinterpret_cast<const float4*>(s_q + tl * PY + c + j4);
-                const float4 g4 = *reinterpret_cast<const float4*>(s_g + tl * CH + c + j4);
                 const float4 y4 = *reinterpret_cast<const float4*>(s_y + tl * PY + c + j4);
+                const float4 g4 = *reinterpret_cast<const float4*>(s_g + tl * CH + c + j4);
                 const float4 d0 = reinterpret_cast<const float4*>(s_du + tl * CH + c + j4)[0];
                 const float4 d1 = reinterpret_cast<const float4*>(s_du + tl * CH + c + j4)[1];
                 const float du[4] = {du4.x, du4.y, du4.z, du4.w}, q[4] = {q4.x, q4.y, q4.z, q4.w};
@@ -375,10 +383,10 @@ scan_bwd_kernel(const SelectiveArgs a, const SelectiveGrads gr, const float* __r
 #pragma unroll
                 for (int jj = 0; jj < 4; ++jj) {
                     const int j = j4 + jj;
-                    const float xv = to_f32(rx.v[j]), Dv = skip(c + j);
+                    const float xv = to_f32(rx.v[j]), Dv = s_skip[c + j];
                     ox[j] = fmaf(dl[jj] * kLn2, du[jj], Dv * gy[jj]);
                     ot[j] = fmaf(du[jj], xv, q[jj]);
-                    if (a.softplus) ot[j] *= sigmoid_fast(to_f32(rdt.v[j]) + bias(c + j));
+                    if (a.softplus) ot[j] *= sigmoid_fast(to_f32(rdt.v[j]) + s_bias[c + j]);
                     oz[j] = 0.f;
                     if (z) {
                         const float zv = to_f32(rz.v[j]), sg = sigmoid_fast(zv);
@@ -391,7 +399,7 @@ scan_bwd_kernel(const SelectiveArgs a, const SelectiveGrads gr, const float* __r
                 }
             }
             const int left = pl.count - c;
-            const int64_t at = (int64_t)t * d.D + c;
+            const int64_t at = (int64_t)t * Dt + c;
             store_channels<T, VW>(dx + at, raw_from_f32<T, VW>(ox), left, Vec);
             store_channels<T, VW>(ddt + at, raw_from_f32<T, VW>(ot), left, Vec);
             if (z) store_channels<T, VW>(dz + at, raw_from_f32<T, VW>(oz), left, Vec);
