@@ -21,16 +21,64 @@ namespace {
 
 constexpr int kThreads = 256;
 
-__device__ __forceinline__ int64_t own_length(const int32_t* lens, int64_t b, int64_t L) {
-    if (!lens) return L;
-    const int64_t n = lens[b];
-    return n < 0 ? 0 : (n > L ? L : n);
+// V fp32 values: pairs in 64-bit registers, one instruction for both (V even).
+template <int V>
+struct Vals {
+    F2 v[V / 2];
+    __device__ __forceinline__ void set(const float (&f)[V]) {
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) v[i] = pack2(f[2 * i], f[2 * i + 1]);
+    }
+    __device__ __forceinline__ void get(float (&f)[V]) const {
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) {
+            const float2 q = unpack2(v[i]);
+            f[2 * i] = q.x;
+            f[2 * i + 1] = q.y;
+        }
+    }
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) v[i] = 0;
+    }
+};
+template <>
+struct Vals<1> {
+    float v[1];
+    __device__ __forceinline__ void set(const float (&f)[1]) { v[0] = f[0]; }
+    __device__ __forceinline__ void get(float (&f)[1]) const { f[0] = v[0]; }
+    __device__ __forceinline__ void zero() { v[0] = 0.f; }
+};
+__device__ __forceinline__ F2 mad(F2 a, F2 b, F2 c) { return fma2(a, b, c); }
+__device__ __forceinline__ float mad(float a, float b, float c) { return fmaf(a, b, c); }
+// a * b + c
+template <int V>
+__device__ __forceinline__ Vals<V> mad(const Vals<V>& a, const Vals<V>& b, const Vals<V>& c) {
+    Vals<V> r;
+#pragma unroll
+    for (int i = 0; i < (int)(sizeof(r.v) / sizeof(r.v[0])); ++i) r.v[i] = mad(a.v[i], b.v[i], c.v[i]);
+    return r;
+}
+template <typename T, int V>
+__device__ __forceinline__ Vals<V> vals_of(const Raw<T, V>& r) {
+    float f[V];
+    raw_to_f32(r, f);
+    Vals<V> o;
+    o.set(f);
+    return o;
+}
+template <typename T, int V>
+__device__ __forceinline__ Raw<T, V> raw_of(const Vals<V>& a) {
+    float f[V];
+    a.get(f);
+    return raw_from_f32<T, V>(f);
 }
 
-// w[k][i], bias[i] of the V channels from c on (weights are (D, W) fp32).
+// w[k][i], bias[i] of the V channels from c on (weights are (D, W) fp32), as
+// operands of the arithmetic below.
 template <int V, int W>
 __device__ __forceinline__ void load_params(const float* w, const float* bias, int64_t c,
-                                            float (&wk)[W][V], float (&bv)[V]) {
+                                            Vals<V> (&wk)[W], Vals<V>& bv) {
     float flat[V * W];
     if constexpr (V * W % 4 == 0) {
 #pragma unroll
@@ -42,12 +90,16 @@ __device__ __forceinline__ void load_params(const float* w, const float* bias, i
 #pragma unroll
         for (int i = 0; i < V * W; ++i) flat[i] = __ldg(w + c * W + i);
     }
+    float f[V];
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
+    for (int k = 0; k < W; ++k) {
 #pragma unroll
-        for (int k = 0; k < W; ++k) wk[k][i] = flat[i * W + k];
-        bv[i] = bias ? __ldg(bias + c + i) : 0.f;
+        for (int i = 0; i < V; ++i) f[i] = flat[i * W + k];
+        wk[k].set(f);
     }
+#pragma unroll
+    for (int i = 0; i < V; ++i) f[i] = bias ? __ldg(bias + c + i) : 0.f;
+    bv.set(f);
 }
 
 // The inputs before token 0 come from the entering state (row W-1+t holds
@@ -77,7 +129,7 @@ conv_fwd_kernel(const T* __restrict__ x, Stride xs, const float* __restrict__ w,
     if (init) init += bb * (W - 1) * D + c;
     y += bb * L * D + c;
 
-    float wk[W][V], bv[V];
+    Vals<V> wk[W], bv;
     load_params<V, W>(w, bias, c, wk, bv);
 
     if (final_state && r == 0) {
@@ -90,41 +142,53 @@ conv_fwd_kernel(const T* __restrict__ x, Stride xs, const float* __restrict__ w,
 
     const int64_t t0 = r * run, t1 = t0 + run < L ? t0 + run : L;
     const int64_t te = t1 < len ? t1 : len;          // tokens of the sequence itself
-    int64_t t = t0;
-    if (t < te) {
-        float win[W][V];                             // win[k]: token t - W + 1 + k
+    y += t0 * D;
+    int left = (int)(t1 - t0), live = (int)(te - t0);
+    if (live > 0) {
+        // p[j]: what the inputs up to here give to the output j tokens ahead
+        Vals<V> p[W];
 #pragma unroll
-        for (int j = 0; j < W - 1; ++j)
-            raw_to_f32(load_row<T, V>(x, xs.token, init, D, W, t0 - (W - 1) + j), win[j + 1]);
+        for (int j = 0; j < W - 1; ++j) p[j] = bv;
+#pragma unroll
+        for (int i = 0; i < W - 1; ++i) {            // token t0 - (W-1) + i
+            const Vals<V> v = vals_of(load_row<T, V>(x, xs.token, init, D, W, t0 - (W - 1) + i));
+#pragma unroll
+            for (int j = 0; j <= i; ++j) p[j] = mad(wk[i - j], v, p[j]);
+        }
+        x += t0 * xs.token;
         constexpr int U = 8;                         // rows in flight
-        for (; t < te; t += U) {
+        for (; live > 0; live -= U, left -= U) {
             Raw<T, V> raw[U];
 #pragma unroll
-            for (int u = 0; u < U; ++u)
-                if (t + u < te) raw[u] = raw_load<T, V>(x + (t + u) * xs.token);
+            for (int u = 0; u < U; ++u) {
+                raw[u] = raw_load<T, V>(x);
+                if (u + 1 < live) x += xs.token;     // behind the last row: that row again
+            }
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                if (t + u < te) {
+                const Vals<V> v = vals_of(raw[u]);
+                const Vals<V> out = mad(wk[W - 1], v, p[0]);
 #pragma unroll
-                    for (int k = 0; k < W - 1; ++k)
+                for (int j = 0; j < W - 2; ++j) p[j] = mad(wk[W - 2 - j], v, p[j + 1]);
+                p[W - 2] = mad(wk[0], v, bv);
+                if (u < live) {
+                    float f[V];
+                    out.get(f);
+                    if (silu) {
 #pragma unroll
-                        for (int i = 0; i < V; ++i) win[k][i] = win[k + 1][i];
-                    raw_to_f32(raw[u], win[W - 1]);
-                    float p[V];
-#pragma unroll
-                    for (int i = 0; i < V; ++i) {
-                        p[i] = bv[i];
-#pragma unroll
-                        for (int k = 0; k < W; ++k) p[i] = fmaf(wk[k][i], win[k][i], p[i]);
-                        if (silu) p[i] *= sigmoid_f32(p[i]);
+                        for (int i = 0; i < V; ++i) f[i] *= sigmoid_fast(f[i]);
                     }
-                    raw_store<T, V>(y + (t + u) * D, raw_from_f32<T, V>(p));
+                    raw_store<T, V>(y, raw_from_f32<T, V>(f));
+                    y += D;
                 }
             }
+            if (live <= U) {
+                left -= live;
+                break;
+            }
         }
-        t = te;
     }
-    for (; t < t1; ++t) raw_store<T, V>(y + t * D, raw_zero<T, V>());
+    for (; left > 0; --left, y += D) raw_store<T, V>(y, raw_zero<T, V>());
 }
 
 // ------------------------------------------------------------------ backward
@@ -136,135 +200,162 @@ conv_fwd_kernel(const T* __restrict__ x, Stride xs, const float* __restrict__ w,
 constexpr int kRun = 32, kSlots = 8;
 constexpr int64_t kTile = (int64_t)kRun * kSlots;
 
+// g = dy silu'(p)
+template <int V, int W>
+__device__ __forceinline__ Vals<V> slope(const Vals<V> (&wk)[W], const Vals<V>& bv,
+                                         const Vals<V> (&win)[W], const Vals<V>& dy, bool silu) {
+    if (!silu) return dy;
+    Vals<V> p = bv;
+#pragma unroll
+    for (int k = 0; k < W; ++k) p = mad(wk[k], win[k], p);
+    float f[V], g[V];
+    p.get(f);
+    dy.get(g);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const float s = sigmoid_fast(f[i]);
+        g[i] *= s * fmaf(f[i], 1.f - s, 1.f);
+    }
+    Vals<V> r;
+    r.set(g);
+    return r;
+}
+
 template <typename T, typename TG, int V, int W>
-__global__ void __launch_bounds__(32 * kSlots)
+__global__ void __launch_bounds__(32 * kSlots, 2)
 conv_bwd_kernel(const T* __restrict__ x, Stride xs, const float* __restrict__ w,
                 const float* __restrict__ bias, const T* __restrict__ init,
                 const int32_t* __restrict__ lens, int silu, const TG* __restrict__ dy,
-                const T* __restrict__ dfinal, T* __restrict__ dx, T* __restrict__ dinit,
-                float* __restrict__ part, int64_t L, int64_t D, int64_t ncb, int64_t ntile) {
+                const T* __restrict__ dfinal, T* __restrict__ dx, float* __restrict__ part,
+                int64_t L, int64_t D, int64_t ncb, int64_t ntile) {
     const int lane = threadIdx.x, slot = threadIdx.y;
     const int64_t cb = blockIdx.x % ncb, tile = blockIdx.x / ncb % ntile,
                   bb = blockIdx.x / ncb / ntile;
     const int64_t c = (cb * 32 + lane) * V;
     const bool mine = c < D;
     const int64_t len = own_length(lens, bb, L);
-    float dw[W][V], db[V];
+    Vals<V> dw[W], db;
+    db.zero();
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        db[i] = 0.f;
-#pragma unroll
-        for (int k = 0; k < W; ++k) dw[k][i] = 0.f;
-    }
-    if (mine) {
+    for (int k = 0; k < W; ++k) dw[k].zero();
+    const int64_t t0 = tile * kTile + slot * kRun;
+    if (mine && t0 < L) {
+        const int64_t t1 = t0 + kRun < L ? t0 + kRun : L;
+        const int64_t s1 = t1 < len ? t1 : len;         // dx of tokens t0 .. s1-1
         x += bb * xs.batch + c;
-        dy += bb * L * D + c;
-        dx += bb * L * D + c;
+        dy += (bb * L + t0) * D + c;
+        dx += (bb * L + t0) * D + c;
         if (init) init += bb * (W - 1) * D + c;
         if (dfinal) dfinal += bb * (W - 1) * D + c;
-        if (dinit) dinit += bb * (W - 1) * D + c;
-        float wk[W][V], bv[V];
-        load_params<V, W>(w, bias, c, wk, bv);
-
-        // dL/dx of token s < len, or of the entering state's row W-1+s for s < 0
-        auto emit = [&](int64_t s, float (&v)[V]) {
-            const int64_t j = s - (len - (W - 1));      // its row in the final state
-            if (dfinal && j >= 0 && j < W - 1) {
+        int todo = s1 > t0 ? (int)(s1 - t0) : 0;        // tokens of the run with a gradient
+        const int zeros = (int)(t1 - t0) - todo;
+        if (todo > 0) {
+            Vals<V> wk[W], bv, win[W], q[W], one;
+            load_params<V, W>(w, bias, c, wk, bv);
+            {
                 float f[V];
-                raw_to_f32(raw_load<T, V>(dfinal + j * D), f);
 #pragma unroll
-                for (int i = 0; i < V; ++i) v[i] += f[i];
+                for (int i = 0; i < V; ++i) f[i] = 1.f;
+                one.set(f);
             }
-            if (s >= 0) raw_store<T, V>(dx + s * D, raw_from_f32<T, V>(v));
-            else if (dinit) raw_store<T, V>(dinit + (W - 1 + s) * D, raw_from_f32<T, V>(v));
-        };
-
-        const int64_t t0 = tile * kTile + slot * kRun;
-        const int64_t t1 = t0 + kRun < L ? t0 + kRun : L;
-        // the first run also gives the entering state's gradient: tokens -(W-1) .. -1
-        const int64_t s0 = t0 == 0 ? -(int64_t)(W - 1) : t0;
-        const int64_t s1 = t1 < len ? t1 : len;         // dx of tokens s0 .. s1-1
-        if (t0 <= t1 && s0 < s1) {
-            float win[W][V], g[W][V];
+            // win[k]: token t - W + 1 + k; q[j]: what the g so far give to the
+            // gradient of token t - (W-1) + j.  (g before t0 only reaches tokens
+            // of the run before.)
 #pragma unroll
             for (int j = 0; j < W - 1; ++j) {
-                raw_to_f32(load_row<T, V>(x, xs.token, init, D, W, t0 - (W - 1) + j), win[j + 1]);
-#pragma unroll
-                for (int i = 0; i < V; ++i) g[j + 1][i] = 0.f;
+                win[j + 1] = vals_of(load_row<T, V>(x, xs.token, init, D, W, t0 - (W - 1) + j));
+                q[j].zero();
             }
-            // g of the tokens before t0 only reaches inputs that belong to the
-            // run before (or, at t0 == 0, does not exist), so it starts at zero
-            constexpr int U = 4;
-            const int64_t te = s1 + W - 1;              // last token walked, exclusive
-            for (int64_t t = t0; t < te; t += U) {
+            x += t0 * xs.token;
+            int kept = (int)(t0 - (len - (W - 1)));     // row of the final state of the next dx
+            int lag = W - 1;                            // tokens until the first dx
+            auto step = [&](const Vals<V>& xv, const Vals<V>& dyv, bool own) {
+#pragma unroll
+                for (int k = 0; k < W - 1; ++k) win[k] = win[k + 1];
+                win[W - 1] = xv;
+                Vals<V> g = slope<V, W>(wk, bv, win, dyv, silu != 0);
+                if (own) {
+                    db = mad(g, one, db);
+#pragma unroll
+                    for (int k = 0; k < W; ++k) dw[k] = mad(g, win[k], dw[k]);
+                }
+                if (lag == 0) {
+                    float f[V];
+                    mad(wk[0], g, q[0]).get(f);
+                    if (dfinal && kept >= 0) {          // a row that the final state keeps
+                        float h[V];
+                        raw_to_f32(raw_load<T, V>(dfinal + (int64_t)kept * D), h);
+#pragma unroll
+                        for (int i = 0; i < V; ++i) f[i] += h[i];
+                    }
+                    raw_store<T, V>(dx, raw_from_f32<T, V>(f));
+                    dx += D;
+                    ++kept;
+                } else {
+                    --lag;
+                }
+#pragma unroll
+                for (int j = 0; j < W - 2; ++j) q[j] = mad(wk[j + 1], g, q[j + 1]);
+                q[W - 2].zero();
+                q[W - 2] = mad(wk[W - 1], g, q[W - 2]);
+            };
+            constexpr int U = 4;                        // rows in flight
+            int ahead = (int)(len - s1 < W - 1 ? len - s1 : W - 1);   // tokens behind with a g
+            const int rows = todo + ahead;
+            for (int i = 0; i < rows; i += U) {
                 Raw<T, V> rx[U];
                 Raw<TG, V> rg[U];
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
-                    const bool in = t + u < te && t + u < len;
-                    rx[u] = in ? raw_load<T, V>(x + (t + u) * xs.token) : raw_zero<T, V>();
-                    rg[u] = in ? raw_load<TG, V>(dy + (t + u) * D) : raw_zero<TG, V>();
-                }
-#pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    if (t + u >= te) break;
-#pragma unroll
-                    for (int k = 0; k < W - 1; ++k)
-#pragma unroll
-                        for (int i = 0; i < V; ++i) {
-                            win[k][i] = win[k + 1][i];
-                            g[k][i] = g[k + 1][i];
-                        }
-                    raw_to_f32(rx[u], win[W - 1]);
-                    raw_to_f32(rg[u], g[W - 1]);
-                    if (silu) {
-#pragma unroll
-                        for (int i = 0; i < V; ++i) {
-                            float p = bv[i];
-#pragma unroll
-                            for (int k = 0; k < W; ++k) p = fmaf(wk[k][i], win[k][i], p);
-                            const float sg = sigmoid_f32(p);
-                            g[W - 1][i] *= sg * fmaf(p, 1.f - sg, 1.f);
-                        }
-                    }
-                    if (t + u >= len) {                 // behind the sequence: no gradient
-#pragma unroll
-                        for (int i = 0; i < V; ++i) g[W - 1][i] = 0.f;
-                    }
-                    if (t + u < s1) {
-#pragma unroll
-                        for (int i = 0; i < V; ++i) {
-                            db[i] += g[W - 1][i];
-#pragma unroll
-                            for (int k = 0; k < W; ++k)
-                                dw[k][i] = fmaf(g[W - 1][i], win[k][i], dw[k][i]);
-                        }
-                    }
-                    const int64_t s = t + u - (W - 1);
-                    if (s >= s0) {
-                        float v[V];
-#pragma unroll
-                        for (int i = 0; i < V; ++i) {
-                            v[i] = 0.f;
-#pragma unroll
-                            for (int k = 0; k < W; ++k) v[i] = fmaf(wk[W - 1 - k][i], g[k][i], v[i]);
-                        }
-                        emit(s, v);
+                    rx[u] = raw_load<T, V>(x);
+                    rg[u] = raw_load<TG, V>(dy);
+                    if (i + u + 1 < rows) {             // behind the last row: that row again
+                        x += xs.token;
+                        dy += D;
                     }
                 }
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    if (i + u < rows) step(vals_of(rx[u]), vals_of(rg[u]), i + u < todo);
+            }
+            Vals<V> none;
+            none.zero();
+            for (; ahead < W - 1; ++ahead) {            // behind the sequence g is zero
+                lag = lag > 0 ? lag : 0;
+                if (lag == 0) {
+                    float f[V];
+                    q[0].get(f);
+                    if (dfinal && kept >= 0) {
+                        float h[V];
+                        raw_to_f32(raw_load<T, V>(dfinal + (int64_t)kept * D), h);
+#pragma unroll
+                        for (int i = 0; i < V; ++i) f[i] += h[i];
+                    }
+                    raw_store<T, V>(dx, raw_from_f32<T, V>(f));
+                    dx += D;
+                    ++kept;
+                } else {
+                    --lag;
+                }
+#pragma unroll
+                for (int j = 0; j < W - 2; ++j) q[j] = q[j + 1];
+                q[W - 2] = none;
             }
         }
-        for (int64_t t = s1 > t0 ? s1 : t0; t < t1; ++t)
-            raw_store<T, V>(dx + t * D, raw_zero<T, V>());
+        for (int i = 0; i < zeros; ++i, dx += D) raw_store<T, V>(dx, raw_zero<T, V>());
     }
 
     // the block's partial row: per channel W weights, then the bias
     __shared__ float red[kSlots][(W + 1) * V][32];
+    {
+        float f[V];
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
+        for (int k = 0; k <= W; ++k) {
+            if (k < W) dw[k < W ? k : 0].get(f);
+            else db.get(f);
 #pragma unroll
-        for (int k = 0; k < W; ++k) red[slot][i * (W + 1) + k][lane] = dw[k][i];
-        red[slot][i * (W + 1) + W][lane] = db[i];
+            for (int i = 0; i < V; ++i) red[slot][i * (W + 1) + k][lane] = f[i];
+        }
     }
     __syncthreads();
     for (int j = slot; j < (W + 1) * V; j += kSlots) {
@@ -272,6 +363,54 @@ conv_bwd_kernel(const T* __restrict__ x, Stride xs, const float* __restrict__ w,
 #pragma unroll
         for (int q = 0; q < kSlots; ++q) v += red[q][j][lane];
         if (mine) part[((bb * ntile + tile) * D + c) * (W + 1) + j] = v;
+    }
+}
+
+// dL/d(entering state): row j is the input W - 1 - j tokens before the first, and
+// reaches p of the tokens 0 .. j, and (where the sequence is shorter than W - 1)
+// the final state's row j - len.
+template <typename T, typename TG, int V, int W>
+__global__ void __launch_bounds__(kThreads)
+conv_dinit_kernel(const T* __restrict__ x, Stride xs, const float* __restrict__ w,
+                  const float* __restrict__ bias, const T* __restrict__ init,
+                  const int32_t* __restrict__ lens, int silu, const TG* __restrict__ dy,
+                  const T* __restrict__ dfinal, T* __restrict__ dinit, int64_t b, int64_t L,
+                  int64_t D) {
+    const int64_t nvec = D / V, item = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+    if (item >= nvec * b) return;
+    const int64_t c = item % nvec * V, bb = item / nvec;
+    const int64_t len = own_length(lens, bb, L);
+    x += bb * xs.batch + c;
+    if (init) init += bb * (W - 1) * D + c;
+    Vals<V> wk[W], bv, win[W], out[W - 1];
+    load_params<V, W>(w, bias, c, wk, bv);
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j) {
+        win[j + 1] = vals_of(load_row<T, V>(x, xs.token, init, D, W, j - (W - 1)));
+        out[j].zero();
+    }
+#pragma unroll
+    for (int t = 0; t < W - 1; ++t) {
+        if (t >= len) break;
+#pragma unroll
+        for (int k = 0; k < W - 1; ++k) win[k] = win[k + 1];
+        win[W - 1] = vals_of(raw_load<T, V>(x + t * xs.token));
+        const Vals<V> g = slope<V, W>(wk, bv, win,
+                                      vals_of(raw_load<TG, V>(dy + (bb * L + t) * D + c)), silu != 0);
+#pragma unroll
+        for (int j = t; j < W - 1; ++j) out[j] = mad(wk[j - t], g, out[j]);
+    }
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j) {
+        float f[V];
+        out[j].get(f);
+        if (dfinal && j >= len) {
+            float h[V];
+            raw_to_f32(raw_load<T, V>(dfinal + (bb * (W - 1) + j - len) * D + c), h);
+#pragma unroll
+            for (int i = 0; i < V; ++i) f[i] += h[i];
+        }
+        raw_store<T, V>(dinit + (bb * (W - 1) + j) * D + c, raw_from_f32<T, V>(f));
     }
 }
 
@@ -313,21 +452,20 @@ conv_step_kernel(T* __restrict__ state, const T* __restrict__ x, int64_t x_batch
 #pragma unroll
     for (int k = 0; k < W - 1; ++k) row[k] = *reinterpret_cast<const Raw<T, V>*>(st + k * D);
     row[W - 1] = raw_load<T, V>(x + bb * x_batch + c);
-    float wk[W][V], p[V];
+    Vals<V> wk[W], p;
     load_params<V, W>(w, bias, c, wk, p);
 #pragma unroll
     for (int k = 0; k < W; ++k) {
-        float v[V];
-        raw_to_f32(row[k], v);
-#pragma unroll
-        for (int i = 0; i < V; ++i) p[i] = fmaf(wk[k][i], v[i], p[i]);
+        p = mad(wk[k], vals_of(row[k]), p);
         if (k > 0) raw_store<T, V>(st + (k - 1) * D, row[k]);
     }
+    float f[V];
+    p.get(f);
     if (silu) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) p[i] *= sigmoid_f32(p[i]);
+        for (int i = 0; i < V; ++i) f[i] *= sigmoid_fast(f[i]);
     }
-    raw_store<T, V>(y + bb * D + c, raw_from_f32<T, V>(p));
+    raw_store<T, V>(y + bb * D + c, raw_from_f32<T, V>(f));
 }
 
 // Whether x's rows can be read V elements at a time (D % V == 0 and every
@@ -364,18 +502,24 @@ void step_v(void* state, const void* x, int64_t x_batch, const float* w, const f
         static_cast<T*>(y), d.b, d.D);
 }
 
-int64_t bwd_tiles(const ConvDims& d) { return d.L > 0 ? (d.L + kTile - 1) / kTile : 1; }
+int64_t bwd_tiles(const ConvDims& d) { return (d.L + kTile - 1) / kTile; }
 
 template <typename T, typename TG, int V, int W>
 void bwd_v(const void* x, Stride xs, const float* w, const float* bias, const void* init,
            const int32_t* lens, bool silu, const void* dy, const void* dfinal, void* dx,
            float* dw, float* dbias, void* dinit, float* ws, const ConvDims& d, cudaStream_t s) {
     const int64_t ncb = (d.D / V + 31) / 32, nt = bwd_tiles(d);
-    if (d.b > 0)
+    if (d.b > 0 && d.L > 0)
         conv_bwd_kernel<T, TG, V, W><<<(unsigned)(ncb * nt * d.b), dim3(32, kSlots), 0, s>>>(
             static_cast<const T*>(x), xs, w, bias, static_cast<const T*>(init), lens, silu,
-            static_cast<const TG*>(dy), static_cast<const T*>(dfinal), static_cast<T*>(dx),
-            static_cast<T*>(dinit), ws, d.L, d.D, ncb, nt);
+            static_cast<const TG*>(dy), static_cast<const T*>(dfinal), static_cast<T*>(dx), ws,
+            d.L, d.D, ncb, nt);
+    if (d.b > 0 && dinit)
+        conv_dinit_kernel<T, TG, V, W>
+            <<<(unsigned)((d.b * (d.D / V) + kThreads - 1) / kThreads), kThreads, 0, s>>>(
+                static_cast<const T*>(x), xs, w, bias, static_cast<const T*>(init), lens, silu,
+                static_cast<const TG*>(dy), static_cast<const T*>(dfinal),
+                static_cast<T*>(dinit), d.b, d.L, d.D);
     conv_reduce_kernel<W><<<(unsigned)((d.D * (W + 1) + 31) / 32), dim3(32, 8), 0, s>>>(
         ws, d.b * nt, d.D, dw, dbias);
 }
@@ -403,7 +547,7 @@ cudaError_t launch_conv_fwd(const void* x, Stride xs, const float* w, const floa
                             void* final_state, const ConvDims& d, Elt t, cudaStream_t s) {
     with_type(t, [&](auto ty) {
         using T = typename decltype(ty)::type;
-        constexpr int V = 16 / sizeof(T);
+        constexpr int V = 4;     // 8-byte bf16 loads: half the registers of 16, twice the threads
         with_width(d.W, [&](auto wi) {
             constexpr int W = decltype(wi)::value;
             if (rows_aligned<T>(x, xs, d.D, V))

@@ -10,48 +10,6 @@
 
 namespace ssd {
 
-constexpr float kLog2E = 1.4426950408889634f;
-
-// 2^v; results below 2^-126 are zero (a decay that small leaves nothing of a state).
-__device__ __forceinline__ float ex2(float v) {
-    float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
-    return r;
-}
-
-// Two fp32 values in one 64-bit register: add, multiply and fma work on both in
-// one instruction.
-using F2 = unsigned long long;
-__device__ __forceinline__ F2 pack2(float lo, float hi) {
-    F2 r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-    return r;
-}
-__device__ __forceinline__ float2 unpack2(F2 v) {
-    float2 r;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-    return r;
-}
-__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
-    F2 r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
-    F2 r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ F2 add2(F2 a, F2 b) {
-    F2 r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ F2 ex2_2(F2 v) {
-    const float2 f = unpack2(v);
-    return pack2(ex2(f.x), ex2(f.y));
-}
-
 // softplus(v) = max(v, 0) + log(1 + w), w = exp(-|v|) in (0, 1].  log(1 + w) =
 // w P(w), P the degree-9 polynomial that interpolates log(1 + w) / w at the
 // Chebyshev points of [0, 1]; the nearest singularity, w = -1, makes its error
@@ -71,17 +29,6 @@ __device__ __forceinline__ float softplus_f32(float v) {
 #pragma unroll
     for (int i = 8; i >= 0; --i) p = fmaf(p, w, kP[i]);
     return fmaf(w, p, fmaxf(v, 0.f));
-}
-
-// sigmoid with ex2's flush to zero: below 2^-126 it is 0.
-__device__ __forceinline__ float sigmoid_fast(float v) {
-    return __fdividef(1.f, 1.f + ex2(-v * kLog2E));
-}
-
-__device__ __forceinline__ int64_t own_length(const int32_t* lens, int64_t b, int64_t L) {
-    if (!lens) return L;
-    const int64_t n = lens[b];
-    return n < 0 ? 0 : (n > L ? L : n);
 }
 
 // Adds v[i] over LANES lanes that lie STRIDE apart, `lane` being this one's place

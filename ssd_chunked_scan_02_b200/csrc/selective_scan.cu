@@ -466,7 +466,7 @@ step_kernel(float* __restrict__ state, const SelectiveArgs a, T* __restrict__ y,
         float o = fmaf(a.D ? a.D[c] : 0.f, xv, acc);
         if (a.z) {
             const float zv = to_f32(static_cast<const T*>(a.z)[bb * a.zs.batch + c]);
-            o *= zv * sigmoid_f32(zv);
+            o *= zv * sigmoid_fast(zv);
         }
         y[bb * d.D + c] = from_f32<T>(o);
     }

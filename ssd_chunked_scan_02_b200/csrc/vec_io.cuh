@@ -78,10 +78,61 @@ __device__ __forceinline__ void copies_pending() {
     asm volatile("cp.async.wait_group %0;" :: "n"(N) : "memory");
 }
 
-// sigmoid(v) = 1 / (1 + exp(-v)); exp overflows to +inf for v < -88, whose
+constexpr float kLog2E = 1.4426950408889634f;
+
+// 2^v; results below 2^-126 are zero (a decay that small leaves nothing of a state).
+__device__ __forceinline__ float ex2(float v) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+
+// Two fp32 values in one 64-bit register: add, multiply and fma work on both in
+// one instruction.
+using F2 = unsigned long long;
+__device__ __forceinline__ F2 pack2(float lo, float hi) {
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ float2 unpack2(F2 v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+    F2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ F2 ex2_2(F2 v) {
+    const float2 f = unpack2(v);
+    return pack2(ex2(f.x), ex2(f.y));
+}
+
+// sigmoid(v) = 1 / (1 + 2^(-v log2(e))); where the power overflows to infinity the
 // reciprocal is the right 0.
-__device__ __forceinline__ float sigmoid_f32(float v) {
-    return __fdividef(1.f, 1.f + __expf(-v));
+__device__ __forceinline__ float sigmoid_fast(float v) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + ex2(-v * kLog2E)));
+    return r;
+}
+
+// The tokens of sequence b that are its own.
+__device__ __forceinline__ int64_t own_length(const int32_t* lens, int64_t b, int64_t L) {
+    if (!lens) return L;
+    const int64_t n = lens[b];
+    return n < 0 ? 0 : (n > L ? L : n);
 }
 
 }  // namespace ssd
