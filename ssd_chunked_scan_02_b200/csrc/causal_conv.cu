@@ -9,7 +9,11 @@
 // operator is a stream: x is read and y written once (2 bytes an element each
 // in bf16).  A thread owns a few neighbouring channels (one wide load a token)
 // and walks a run of tokens with the last W inputs in registers; only the W - 1
-// rows before a run are read twice, and those come from L2.
+// rows before a run are read twice, and those come from L2.  What keeps the
+// memory busy is the number of rows under way: asynchronous copies into a ring in
+// shared memory, each thread its own rows (no barrier), run 12 rows ahead
+// without a register; rows that cannot be copied 8 bytes at a time (odd widths or
+// views) are loaded as they are needed.
 #include <cuda_bf16.h>
 
 #include "common.cuh"
@@ -19,7 +23,10 @@
 namespace ssd {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
+
+template <int N> struct Int { static constexpr int value = N; };
+template <typename T> struct Type { using type = T; };
 
 // V fp32 values: pairs in 64-bit registers, one instruction for both (V even).
 template <int V>
@@ -57,6 +64,48 @@ __device__ __forceinline__ Vals<V> mad(const Vals<V>& a, const Vals<V>& b, const
     Vals<V> r;
 #pragma unroll
     for (int i = 0; i < (int)(sizeof(r.v) / sizeof(r.v[0])); ++i) r.v[i] = mad(a.v[i], b.v[i], c.v[i]);
+    return r;
+}
+__device__ __forceinline__ F2 times(F2 a, F2 b) { return mul2(a, b); }
+__device__ __forceinline__ float times(float a, float b) { return a * b; }
+__device__ __forceinline__ F2 plus(F2 a, F2 b) { return add2(a, b); }
+__device__ __forceinline__ float plus(float a, float b) { return a + b; }
+__device__ __forceinline__ void both(F2& v, float f) { v = pack2(f, f); }
+__device__ __forceinline__ void both(float& v, float f) { v = f; }
+// silu(p) = p sigmoid(p)
+template <int V>
+__device__ __forceinline__ Vals<V> silu_of(const Vals<V>& p) {
+    Vals<V> r;
+#pragma unroll
+    for (int i = 0; i < (int)(sizeof(r.v) / sizeof(r.v[0])); ++i)
+        r.v[i] = times(p.v[i], sigmoid_fast(p.v[i]));
+    return r;
+}
+// dy silu'(p) = dy s (1 + p (1 - s)), s = sigmoid(p)
+template <int V>
+__device__ __forceinline__ Vals<V> silu_slope(const Vals<V>& p, const Vals<V>& dy) {
+    Vals<V> r;
+#pragma unroll
+    for (int i = 0; i < (int)(sizeof(r.v) / sizeof(r.v[0])); ++i) {
+        auto s = sigmoid_fast(p.v[i]), one = s, minus = s;
+        both(one, 1.f);
+        both(minus, -1.f);
+        r.v[i] = times(times(dy.v[i], s), mad(p.v[i], mad(s, minus, one), one));
+    }
+    return r;
+}
+template <int V>
+__device__ __forceinline__ Vals<V> operator+(const Vals<V>& a, const Vals<V>& b) {
+    Vals<V> r;
+#pragma unroll
+    for (int i = 0; i < (int)(sizeof(r.v) / sizeof(r.v[0])); ++i) r.v[i] = plus(a.v[i], b.v[i]);
+    return r;
+}
+template <int V>
+__device__ __forceinline__ Vals<V> operator*(const Vals<V>& a, const Vals<V>& b) {
+    Vals<V> r;
+#pragma unroll
+    for (int i = 0; i < (int)(sizeof(r.v) / sizeof(r.v[0])); ++i) r.v[i] = times(a.v[i], b.v[i]);
     return r;
 }
 template <typename T, int V>
@@ -111,10 +160,46 @@ __device__ __forceinline__ Raw<T, V> load_row(const T* x, int64_t token_stride, 
     return init ? raw_load<T, V>(init + (W - 1 + t) * D) : raw_zero<T, V>();
 }
 
+// A thread's rows on their way through shared memory, in groups of kGroup: rows(g)
+// are asked for kAhead groups before they are taken.
+constexpr int kGroup = 4, kAhead = 3, kRing = kGroup * (kAhead + 1);
+
+template <typename T, int V, int THREADS>
+struct Rows {
+    static constexpr bool kAsync = sizeof(T) * V >= 8;
+    static constexpr int kBytes = kAsync ? kRing * THREADS * V * (int)sizeof(T) : 0;
+    Raw<T, V>* ring;                  // [kRing][THREADS], this thread's column
+    const T* p;                       // the next row to ask for
+    int64_t step;
+    __device__ __forceinline__ Rows(unsigned char* smem, int tid, const T* from, int64_t stride)
+        : ring(reinterpret_cast<Raw<T, V>*>(smem) + tid), p(from), step(stride) {}
+    // asks for the rows of group g that are below n
+    __device__ __forceinline__ void ask(int g, int n) {
+        if constexpr (kAsync) {
+#pragma unroll
+            for (int u = 0; u < kGroup; ++u) {
+                if (g * kGroup + u < n)
+                    copy_async(ring + (g * kGroup + u) % kRing * THREADS, p, true);
+                p += step;
+            }
+        }
+    }
+    // row r, whose group has arrived (or is loaded now)
+    __device__ __forceinline__ Raw<T, V> take(int r) {
+        if constexpr (kAsync) {
+            return ring[r % kRing * THREADS];
+        } else {
+            const Raw<T, V> v = raw_load<T, V>(p);
+            p += step;
+            return v;
+        }
+    }
+};
+
 // ------------------------------------------------------------------ forward
 // One thread: V channels, `run` tokens of one sequence.
 template <typename T, int V, int W>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 8 : 5)
 conv_fwd_kernel(const T* __restrict__ x, Stride xs, const float* __restrict__ w,
                 const float* __restrict__ bias, const T* __restrict__ init,
                 const int32_t* __restrict__ lens, int silu, T* __restrict__ y,
@@ -129,6 +214,16 @@ conv_fwd_kernel(const T* __restrict__ x, Stride xs, const float* __restrict__ w,
     if (init) init += bb * (W - 1) * D + c;
     y += bb * L * D + c;
 
+    const int64_t t0 = r * run, t1 = t0 + run < L ? t0 + run : L;
+    const int64_t te = t1 < len ? t1 : len;          // tokens of the sequence itself
+    y += t0 * D;
+    int left = (int)(t1 - t0), live = (int)(te - t0);
+    __shared__ __align__(16) unsigned char ring[Rows<T, V, kThreads>::kBytes + 16];
+    Rows<T, V, kThreads> rows(ring, threadIdx.x, x + t0 * xs.token, xs.token);
+    for (int g = 0; g < kAhead; ++g) {
+        rows.ask(g, live);
+        copies_commit();
+    }
     Vals<V> wk[W], bv;
     load_params<V, W>(w, bias, c, wk, bv);
 
@@ -140,10 +235,6 @@ conv_fwd_kernel(const T* __restrict__ x, Stride xs, const float* __restrict__ w,
                             load_row<T, V>(x, xs.token, init, D, W, len - (W - 1) + j));
     }
 
-    const int64_t t0 = r * run, t1 = t0 + run < L ? t0 + run : L;
-    const int64_t te = t1 < len ? t1 : len;          // tokens of the sequence itself
-    y += t0 * D;
-    int left = (int)(t1 - t0), live = (int)(te - t0);
     if (live > 0) {
         // p[j]: what the inputs up to here give to the output j tokens ahead
         Vals<V> p[W];
@@ -155,49 +246,40 @@ conv_fwd_kernel(const T* __restrict__ x, Stride xs, const float* __restrict__ w,
 #pragma unroll
             for (int j = 0; j <= i; ++j) p[j] = mad(wk[i - j], v, p[j]);
         }
-        x += t0 * xs.token;
-        constexpr int U = 8;                         // rows in flight
-        for (; live > 0; live -= U, left -= U) {
-            Raw<T, V> raw[U];
+        auto step = [&](const Raw<T, V>& row) {
+            const Vals<V> v = vals_of(row);
+            const Vals<V> out = mad(wk[W - 1], v, p[0]);
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                raw[u] = raw_load<T, V>(x);
-                if (u + 1 < live) x += xs.token;     // behind the last row: that row again
+            for (int j = 0; j < W - 2; ++j) p[j] = mad(wk[W - 2 - j], v, p[j + 1]);
+            p[W - 2] = mad(wk[0], v, bv);
+            raw_store<T, V>(y, raw_of<T, V>(silu ? silu_of(out) : out));
+            y += D;
+        };
+        left -= live;
+        const int groups = (live + kGroup - 1) / kGroup;
+#pragma unroll 1
+        for (int g = 0; g < groups; ++g) {
+            copies_pending<kAhead - 1>();
+            if ((g + 1) * kGroup <= live) {
+#pragma unroll
+                for (int u = 0; u < kGroup; ++u) step(rows.take(g * kGroup + u));
+            } else {
+                for (int u = g * kGroup; u < live; ++u) step(rows.take(u));
             }
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const Vals<V> v = vals_of(raw[u]);
-                const Vals<V> out = mad(wk[W - 1], v, p[0]);
-#pragma unroll
-                for (int j = 0; j < W - 2; ++j) p[j] = mad(wk[W - 2 - j], v, p[j + 1]);
-                p[W - 2] = mad(wk[0], v, bv);
-                if (u < live) {
-                    float f[V];
-                    out.get(f);
-                    if (silu) {
-#pragma unroll
-                        for (int i = 0; i < V; ++i) f[i] *= sigmoid_fast(f[i]);
-                    }
-                    raw_store<T, V>(y, raw_from_f32<T, V>(f));
-                    y += D;
-                }
-            }
-            if (live <= U) {
-                left -= live;
-                break;
-            }
+            rows.ask(g + kAhead, live);
+            copies_commit();
         }
     }
     for (; left > 0; --left, y += D) raw_store<T, V>(y, raw_zero<T, V>());
 }
 
 // ------------------------------------------------------------------ backward
-// A block of 32 x 8 threads: 32 channel vectors, 8 runs of kRun tokens.  A
+// A block of 32 x 4 threads: 32 channel vectors, 4 runs of kRun tokens.  A
 // thread walks its run and the W - 1 tokens behind it (whose g its last dx
 // need); at token t the gradient of token t - W + 1 is complete.  Each block
-// adds its eight runs' dw and dbias and writes one partial row a channel; a
+// adds its four runs' dw and dbias and writes one partial row a channel; a
 // second kernel adds the partial rows in a fixed order.
-constexpr int kRun = 32, kSlots = 8;
+constexpr int kRun = 64, kSlots = 4;
 constexpr int64_t kTile = (int64_t)kRun * kSlots;
 
 // g = dy silu'(p)
@@ -208,26 +290,17 @@ __device__ __forceinline__ Vals<V> slope(const Vals<V> (&wk)[W], const Vals<V>& 
     Vals<V> p = bv;
 #pragma unroll
     for (int k = 0; k < W; ++k) p = mad(wk[k], win[k], p);
-    float f[V], g[V];
-    p.get(f);
-    dy.get(g);
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-        const float s = sigmoid_fast(f[i]);
-        g[i] *= s * fmaf(f[i], 1.f - s, 1.f);
-    }
-    Vals<V> r;
-    r.set(g);
-    return r;
+    return silu_slope(p, dy);
 }
 
 template <typename T, typename TG, int V, int W>
-__global__ void __launch_bounds__(32 * kSlots, 2)
+__global__ void __launch_bounds__(32 * kSlots, 4)
 conv_bwd_kernel(const T* __restrict__ x, Stride xs, const float* __restrict__ w,
                 const float* __restrict__ bias, const T* __restrict__ init,
                 const int32_t* __restrict__ lens, int silu, const TG* __restrict__ dy,
                 const T* __restrict__ dfinal, T* __restrict__ dx, float* __restrict__ part,
                 int64_t L, int64_t D, int64_t ncb, int64_t ntile) {
+    extern __shared__ __align__(16) unsigned char ring[];
     const int lane = threadIdx.x, slot = threadIdx.y;
     const int64_t cb = blockIdx.x % ncb, tile = blockIdx.x / ncb % ntile,
                   bb = blockIdx.x / ncb / ntile;
@@ -250,14 +323,19 @@ conv_bwd_kernel(const T* __restrict__ x, Stride xs, const float* __restrict__ w,
         int todo = s1 > t0 ? (int)(s1 - t0) : 0;        // tokens of the run with a gradient
         const int zeros = (int)(t1 - t0) - todo;
         if (todo > 0) {
-            Vals<V> wk[W], bv, win[W], q[W], one;
+            const int ahead = (int)(len - s1 < W - 1 ? len - s1 : W - 1);   // tokens behind with a g
+            const int rows = todo + ahead;
+            constexpr int kAll = 32 * kSlots;
+            Rows<T, V, kAll> rx(ring, slot * 32 + lane, x + t0 * xs.token, xs.token);
+            Rows<TG, V, kAll> rg(ring + Rows<T, V, kAll>::kBytes, slot * 32 + lane, dy, D);
+            auto ask = [&](int g) {
+                rx.ask(g, rows);
+                rg.ask(g, rows);
+                copies_commit();
+            };
+            for (int g = 0; g < kAhead; ++g) ask(g);
+            Vals<V> wk[W], bv, win[W], q[W];
             load_params<V, W>(w, bias, c, wk, bv);
-            {
-                float f[V];
-#pragma unroll
-                for (int i = 0; i < V; ++i) f[i] = 1.f;
-                one.set(f);
-            }
             // win[k]: token t - W + 1 + k; q[j]: what the g so far give to the
             // gradient of token t - (W-1) + j.  (g before t0 only reaches tokens
             // of the run before.)
@@ -266,66 +344,49 @@ conv_bwd_kernel(const T* __restrict__ x, Stride xs, const float* __restrict__ w,
                 win[j + 1] = vals_of(load_row<T, V>(x, xs.token, init, D, W, t0 - (W - 1) + j));
                 q[j].zero();
             }
-            x += t0 * xs.token;
-            int kept = (int)(t0 - (len - (W - 1)));     // row of the final state of the next dx
-            int lag = W - 1;                            // tokens until the first dx
-            auto step = [&](const Vals<V>& xv, const Vals<V>& dyv, bool own) {
+            // token t: its g, what it gives to dw and dbias (own), and dx of token
+            // t - (W-1), which it completes
+            auto walk = [&](const Raw<T, V>& rx, const Raw<TG, V>& rg, bool own) {
 #pragma unroll
                 for (int k = 0; k < W - 1; ++k) win[k] = win[k + 1];
-                win[W - 1] = xv;
-                Vals<V> g = slope<V, W>(wk, bv, win, dyv, silu != 0);
+                win[W - 1] = vals_of(rx);
+                const Vals<V> g = slope<V, W>(wk, bv, win, vals_of(rg), silu != 0);
                 if (own) {
-                    db = mad(g, one, db);
+                    db = db + g;
 #pragma unroll
                     for (int k = 0; k < W; ++k) dw[k] = mad(g, win[k], dw[k]);
                 }
-                if (lag == 0) {
-                    float f[V];
-                    mad(wk[0], g, q[0]).get(f);
-                    if (dfinal && kept >= 0) {          // a row that the final state keeps
-                        float h[V];
-                        raw_to_f32(raw_load<T, V>(dfinal + (int64_t)kept * D), h);
-#pragma unroll
-                        for (int i = 0; i < V; ++i) f[i] += h[i];
-                    }
-                    raw_store<T, V>(dx, raw_from_f32<T, V>(f));
-                    dx += D;
-                    ++kept;
-                } else {
-                    --lag;
-                }
+                const Vals<V> done = mad(wk[0], g, q[0]);
 #pragma unroll
                 for (int j = 0; j < W - 2; ++j) q[j] = mad(wk[j + 1], g, q[j + 1]);
-                q[W - 2].zero();
-                q[W - 2] = mad(wk[W - 1], g, q[W - 2]);
+                q[W - 2] = wk[W - 1] * g;
+                return done;
             };
-            constexpr int U = 4;                        // rows in flight
-            int ahead = (int)(len - s1 < W - 1 ? len - s1 : W - 1);   // tokens behind with a g
-            const int rows = todo + ahead;
-            for (int i = 0; i < rows; i += U) {
-                Raw<T, V> rx[U];
-                Raw<TG, V> rg[U];
+            if (todo == kRun && ahead == W - 1) {
+                // a whole run, and none of its rows is in the final state
+                auto group = [&](int g, auto first, auto own, auto n) {
+                    copies_pending<kAhead - 1>();
 #pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    rx[u] = raw_load<T, V>(x);
-                    rg[u] = raw_load<TG, V>(dy);
-                    if (i + u + 1 < rows) {             // behind the last row: that row again
-                        x += xs.token;
-                        dy += D;
+                    for (int u = 0; u < decltype(n)::value; ++u) {
+                        const Vals<V> v = walk(rx.take(g * kGroup + u), rg.take(g * kGroup + u),
+                                               decltype(own)::value);
+                        if (!decltype(first)::value || u >= W - 1) {
+                            raw_store<T, V>(dx, raw_of<T, V>(v));
+                            dx += D;
+                        }
                     }
-                }
-#pragma unroll
-                for (int u = 0; u < U; ++u)
-                    if (i + u < rows) step(vals_of(rx[u]), vals_of(rg[u]), i + u < todo);
-            }
-            Vals<V> none;
-            none.zero();
-            for (; ahead < W - 1; ++ahead) {            // behind the sequence g is zero
-                lag = lag > 0 ? lag : 0;
-                if (lag == 0) {
+                    ask(g + kAhead);
+                };
+                group(0, Int<1>{}, Int<1>{}, Int<kGroup>{});
+#pragma unroll 1
+                for (int g = 1; g < kRun / kGroup; ++g) group(g, Int<0>{}, Int<1>{}, Int<kGroup>{});
+                group(kRun / kGroup, Int<0>{}, Int<0>{}, Int<W - 1>{});
+            } else {
+                int kept = (int)(t0 - (len - (W - 1)));     // row of the final state of the next dx
+                auto emit = [&](const Vals<V>& v) {
                     float f[V];
-                    q[0].get(f);
-                    if (dfinal && kept >= 0) {
+                    v.get(f);
+                    if (dfinal && kept >= 0) {              // a row that the final state keeps
                         float h[V];
                         raw_to_f32(raw_load<T, V>(dfinal + (int64_t)kept * D), h);
 #pragma unroll
@@ -334,19 +395,30 @@ conv_bwd_kernel(const T* __restrict__ x, Stride xs, const float* __restrict__ w,
                     raw_store<T, V>(dx, raw_from_f32<T, V>(f));
                     dx += D;
                     ++kept;
-                } else {
-                    --lag;
-                }
+                };
+#pragma unroll 1
+                for (int i = 0; i < todo + W - 1; ++i) {
+                    Vals<V> v = q[0];
+                    if (i < rows) {
+                        if (i % kGroup == 0) copies_pending<kAhead - 1>();
+                        v = walk(rx.take(i), rg.take(i), i < todo);
+                        if (i % kGroup == kGroup - 1) ask(i / kGroup + kAhead);
+                    } else {                                // behind the sequence g is zero
 #pragma unroll
-                for (int j = 0; j < W - 2; ++j) q[j] = q[j + 1];
-                q[W - 2] = none;
+                        for (int j = 0; j < W - 2; ++j) q[j] = q[j + 1];
+                        q[W - 2].zero();
+                    }
+                    if (i >= W - 1) emit(v);
+                }
             }
         }
         for (int i = 0; i < zeros; ++i, dx += D) raw_store<T, V>(dx, raw_zero<T, V>());
     }
 
     // the block's partial row: per channel W weights, then the bias
-    __shared__ float red[kSlots][(W + 1) * V][32];
+    float(*red)[(W + 1) * V][32] = reinterpret_cast<float(*)[(W + 1) * V][32]>(ring);
+    copies_pending<0>();
+    __syncthreads();                                    // the rows are done with
     {
         float f[V];
 #pragma unroll
@@ -459,13 +531,7 @@ conv_step_kernel(T* __restrict__ state, const T* __restrict__ x, int64_t x_batch
         p = mad(wk[k], vals_of(row[k]), p);
         if (k > 0) raw_store<T, V>(st + (k - 1) * D, row[k]);
     }
-    float f[V];
-    p.get(f);
-    if (silu) {
-#pragma unroll
-        for (int i = 0; i < V; ++i) f[i] *= sigmoid_fast(f[i]);
-    }
-    raw_store<T, V>(y + bb * D + c, raw_from_f32<T, V>(f));
+    raw_store<T, V>(y + bb * D + c, raw_of<T, V>(silu ? silu_of(p) : p));
 }
 
 // Whether x's rows can be read V elements at a time (D % V == 0 and every
@@ -505,15 +571,23 @@ void step_v(void* state, const void* x, int64_t x_batch, const float* w, const f
 int64_t bwd_tiles(const ConvDims& d) { return (d.L + kTile - 1) / kTile; }
 
 template <typename T, typename TG, int V, int W>
-void bwd_v(const void* x, Stride xs, const float* w, const float* bias, const void* init,
+cudaError_t bwd_v(const void* x, Stride xs, const float* w, const float* bias, const void* init,
            const int32_t* lens, bool silu, const void* dy, const void* dfinal, void* dx,
            float* dw, float* dbias, void* dinit, float* ws, const ConvDims& d, cudaStream_t s) {
     const int64_t ncb = (d.D / V + 31) / 32, nt = bwd_tiles(d);
-    if (d.b > 0 && d.L > 0)
-        conv_bwd_kernel<T, TG, V, W><<<(unsigned)(ncb * nt * d.b), dim3(32, kSlots), 0, s>>>(
+    if (d.b > 0 && d.L > 0) {
+        constexpr int rows = Rows<T, V, 32 * kSlots>::kBytes + Rows<TG, V, 32 * kSlots>::kBytes,
+                      sums = kSlots * (W + 1) * V * 32 * 4, smem = rows > sums ? rows : sums;
+        if (smem > 48 * 1024) {
+            const cudaError_t e = cudaFuncSetAttribute(
+                conv_bwd_kernel<T, TG, V, W>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+            if (e != cudaSuccess) return e;
+        }
+        conv_bwd_kernel<T, TG, V, W><<<(unsigned)(ncb * nt * d.b), dim3(32, kSlots), smem, s>>>(
             static_cast<const T*>(x), xs, w, bias, static_cast<const T*>(init), lens, silu,
             static_cast<const TG*>(dy), static_cast<const T*>(dfinal), static_cast<T*>(dx), ws,
             d.L, d.D, ncb, nt);
+    }
     if (d.b > 0 && dinit)
         conv_dinit_kernel<T, TG, V, W>
             <<<(unsigned)((d.b * (d.D / V) + kThreads - 1) / kThreads), kThreads, 0, s>>>(
@@ -522,12 +596,10 @@ void bwd_v(const void* x, Stride xs, const float* w, const float* bias, const vo
                 static_cast<T*>(dinit), d.b, d.L, d.D);
     conv_reduce_kernel<W><<<(unsigned)((d.D * (W + 1) + 31) / 32), dim3(32, 8), 0, s>>>(
         ws, d.b * nt, d.D, dw, dbias);
+    return cudaGetLastError();
 }
 
 // Calls f with the element type, the vector width and the taps as types.
-template <int N> struct Int { static constexpr int value = N; };
-template <typename T> struct Type { using type = T; };
-
 template <typename F>
 void with_width(int W, F f) {
     if (W == 2) f(Int<2>{});
@@ -567,6 +639,7 @@ cudaError_t launch_conv_bwd(const void* x, Stride xs, const float* w, const floa
                             const void* init, const int32_t* lens, bool silu, const void* dy,
                             bool dy_f32, const void* dfinal, void* dx, float* dw, float* dbias,
                             void* dinit, float* ws, const ConvDims& d, Elt t, cudaStream_t s) {
+    cudaError_t err = cudaSuccess;
     with_type(t, [&](auto ty) {
         using T = typename decltype(ty)::type;
         with_width(d.W, [&](auto wi) {
@@ -574,17 +647,17 @@ cudaError_t launch_conv_bwd(const void* x, Stride xs, const float* w, const floa
             auto go = [&](auto tg) {
                 using TG = typename decltype(tg)::type;
                 if (rows_aligned<T>(x, xs, d.D, 4))
-                    bwd_v<T, TG, 4, W>(x, xs, w, bias, init, lens, silu, dy, dfinal, dx, dw,
-                                       dbias, dinit, ws, d, s);
+                    err = bwd_v<T, TG, 4, W>(x, xs, w, bias, init, lens, silu, dy, dfinal, dx, dw,
+                                             dbias, dinit, ws, d, s);
                 else
-                    bwd_v<T, TG, 1, W>(x, xs, w, bias, init, lens, silu, dy, dfinal, dx, dw,
-                                       dbias, dinit, ws, d, s);
+                    err = bwd_v<T, TG, 1, W>(x, xs, w, bias, init, lens, silu, dy, dfinal, dx, dw,
+                                             dbias, dinit, ws, d, s);
             };
             if (dy_f32) go(Type<float>{});
             else go(Type<T>{});
         });
     });
-    return cudaGetLastError();
+    return err;
 }
 
 cudaError_t launch_conv_step(void* state, const void* x, int64_t x_batch, const float* w,

@@ -120,12 +120,18 @@ __device__ __forceinline__ F2 ex2_2(F2 v) {
     return pack2(ex2(f.x), ex2(f.y));
 }
 
+__device__ __forceinline__ float rcp_fast(float v) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+
 // sigmoid(v) = 1 / (1 + 2^(-v log2(e))); where the power overflows to infinity the
 // reciprocal is the right 0.
-__device__ __forceinline__ float sigmoid_fast(float v) {
-    float r;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + ex2(-v * kLog2E)));
-    return r;
+__device__ __forceinline__ float sigmoid_fast(float v) { return rcp_fast(1.f + ex2(-v * kLog2E)); }
+__device__ __forceinline__ F2 sigmoid_fast(F2 v) {
+    const float2 e = unpack2(add2(ex2_2(mul2(v, pack2(-kLog2E, -kLog2E))), pack2(1.f, 1.f)));
+    return pack2(rcp_fast(e.x), rcp_fast(e.y));
 }
 
 // The tokens of sequence b that are its own.
