@@ -583,25 +583,29 @@ def ssd_state_correction_fwd(h_in, dt, A, C, y, final_states=None, workspace=Non
 class _scope:
     """Makes the call's device, and the stream it is asked to run on, current,
     so that what the call allocates belongs to the stream that uses it.  Nothing
-    is entered where they are current already."""
+    is entered where they are current already (the raw handle is asked for
+    directly: a single-token call takes less time than a stream object)."""
+    __slots__ = ("index", "entered")
 
     def __init__(self, device, stream):
-        self.entered = []
+        self.index, self.entered = device.index, ()
         if stream is not None:
             if not isinstance(stream, torch.cuda.Stream):
                 stream = (torch.cuda.ExternalStream(int(stream), device=device) if int(stream)
                           else torch.cuda.default_stream(device))
-            self.entered.append(torch.cuda.stream(stream))
-        elif device.index != torch.cuda.current_device():
-            self.entered.append(torch.cuda.device(device))
+            if stream.device != device:
+                raise ValueError(f"stream: on {stream.device}, expected {device} (the device of x)")
+            self.entered = (torch.cuda.stream(stream),)
+        elif device.index != torch._C._cuda_getDevice():
+            self.entered = (torch.cuda.device(device),)
 
     def __enter__(self):
         for c in self.entered:
             c.__enter__()
-        return torch.cuda.current_stream().cuda_stream
+        return torch._C._cuda_getCurrentRawStream(self.index)
 
     def __exit__(self, *exc):
-        for c in reversed(self.entered):
+        for c in self.entered:
             c.__exit__(*exc)
 
 
@@ -609,7 +613,8 @@ def _dense(name, t, shape, dtype, device):
     """A dense argument (or None): checked, then its address."""
     if t is None:
         return None
-    _expect(name, t, shape, dtype, device)
+    if t.shape != shape or t.dtype != dtype or t.device != device:
+        _expect(name, t, shape, dtype, device)
     if not t.is_contiguous():
         raise ValueError(f"{name}: must be contiguous")
     return t.data_ptr()
@@ -621,12 +626,16 @@ def _view(name, t, shape, dtype, device, tokens=True):
     (or, without tokens, the batch) have to be contiguous."""
     if t is None:
         return None, ssd_stride_t(0, 0)
-    _expect(name, t, shape, dtype, device)
-    lead, strides, run = 2 if tokens else 1, t.stride(), 1
-    for i in range(len(shape) - 1, lead - 1, -1):
-        if shape[i] != 1 and strides[i] != run:
-            raise ValueError(f"{name}: its last {len(shape) - lead} dimension(s) must be contiguous")
-        run *= shape[i]
+    if t.shape != shape or t.dtype != dtype or t.device != device:
+        _expect(name, t, shape, dtype, device)
+    lead, strides = 2 if tokens else 1, t.stride()
+    if not t.is_contiguous():
+        run = 1
+        for i in range(len(shape) - 1, lead - 1, -1):
+            if shape[i] != 1 and strides[i] != run:
+                raise ValueError(f"{name}: its last {len(shape) - lead} dimension(s) must be "
+                                 "contiguous")
+            run *= shape[i]
     return t.data_ptr(), ssd_stride_t(strides[0], strides[1] if tokens else 0)
 
 
@@ -665,10 +674,10 @@ def ssd_causal_conv_fwd(x, weight, bias=None, init_state=None, seq_lens=None, si
     pf = _dense("final_state", final_state, (b, W - 1, D), T, dev)
     with _scope(_device_of(x), stream) as st:
         if y is None:
-            y = torch.empty((b, L, D), device=dev, dtype=T)
+            y = x.new_empty((b, L, D))
             py = y.data_ptr()
         if return_final_state and final_state is None:
-            final_state = torch.empty((b, W - 1, D), device=dev, dtype=T)
+            final_state = x.new_empty((b, W - 1, D))
             pf = final_state.data_ptr()
         _check(load().ssd_causal_conv_fwd(px, sx, pw, pb, pi, pl, int(silu), py, pf, dims, code, st),
                "ssd_causal_conv_fwd")
@@ -727,7 +736,7 @@ def ssd_causal_conv_step(state, x, weight, bias=None, silu: bool = True, y=None,
     py = _dense("y", y, (b, D), T, dev)
     with _scope(_device_of(x), stream) as st:
         if y is None:
-            y = torch.empty((b, D), device=dev, dtype=T)
+            y = x.new_empty((b, D))
             py = y.data_ptr()
         _check(load().ssd_causal_conv_step(ps, px, sx, pw, pb, int(silu), py,
                                            ssd_conv_dims_t(b, 1, D, W), code, st),
@@ -784,7 +793,7 @@ def ssd_selective_scan_fwd(x, dt, A, B, C, D=None, z=None, dt_bias=None, softplu
     pf = _dense("final_states", final_states, (b, ch, N), f32, dev)
     with _scope(_device_of(x), stream) as st:
         if y is None:
-            y = torch.empty((b, L, ch), device=dev, dtype=T)
+            y = x.new_empty((b, L, ch))
             py = y.data_ptr()
         if return_final_states and final_states is None:
             final_states = torch.empty((b, ch, N), device=dev, dtype=f32)
@@ -848,7 +857,7 @@ def ssd_selective_step(state, x, dt, A, B, C, D=None, z=None, dt_bias=None, soft
     py = _dense("y", y, (b, ch), x.dtype, dev)
     with _scope(_device_of(x), stream) as st:
         if y is None:
-            y = torch.empty((b, ch), device=dev, dtype=x.dtype)
+            y = x.new_empty((b, ch))
             py = y.data_ptr()
         _check(load().ssd_selective_step(ps, *args, py, strides, dims, code, st),
                "ssd_selective_step")
@@ -887,10 +896,10 @@ def ssd_bc_norm_rotate_fwd(B, C, B_weight, C_weight, positions, freq, eps: float
     oC = _dense("C_out", C_out, tuple(B.shape), B.dtype, dev)
     with _scope(_device_of(B), stream) as st:
         if B_out is None:
-            B_out = torch.empty(B.shape, device=dev, dtype=B.dtype)
+            B_out = B.new_empty(B.shape)
             oB = B_out.data_ptr()
         if C_out is None:
-            C_out = torch.empty(B.shape, device=dev, dtype=B.dtype)
+            C_out = B.new_empty(B.shape)
             oC = C_out.data_ptr()
         _check(load().ssd_bc_norm_rotate_fwd(*args, oB, oC, dims, code, st),
                "ssd_bc_norm_rotate_fwd")
