@@ -43,11 +43,11 @@ struct Args {
     int interleaved;
     void *oB, *oC;                    // out, or dL/dB and dL/dC
     float* part;                      // (blocks, 2 G, N): partial sums of dweight
-    int64_t tokens, L;                // tokens = b * L
+    int64_t L;
     int G, N, R;
     int lanes;                        // lanes of a unit: a power of two
-    int tile;                         // tokens of a block's tile
-    int64_t ntile;
+    int tile;                         // tokens of a block's tile, all of one sequence
+    int64_t tiles, ntile;             // of a sequence, and of all
 };
 
 // The fraction of a turn that position `pos` makes at `step` = freq / (2 pi),
@@ -86,21 +86,31 @@ __device__ __forceinline__ float unit_sum(float v, int lanes) {
     return v;
 }
 
-// Vec: the runs of four are whole, aligned loads.  Otherwise each of the eight
-// elements is loaded on its own where it exists.
+// A row's eight elements of a lane as loaded.  Vec: the runs of four are whole,
+// aligned loads; otherwise each element is loaded on its own where it exists.
 template <typename T, bool Vec>
-__device__ __forceinline__ void load8(const T* row, const int (&at)[8], int N, float (&v)[8]) {
-    if constexpr (Vec) {
-        float a[4], b[4];
-        raw_to_f32(raw_load<T, 4>(row + at[0]), a);
-        raw_to_f32(raw_load<T, 4>(row + at[4]), b);
+struct Row8 {
+    Raw<T, 4> lo, hi;
+    __device__ __forceinline__ void load(const T* row, const int (&at)[8], int N) {
+        if constexpr (Vec) {
+            lo = raw_load<T, 4>(row + at[0]);
+            hi = raw_load<T, 4>(row + at[4]);
+        } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) { v[i] = a[i]; v[4 + i] = b[i]; }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = at[i] < N ? to_f32(row[at[i]]) : 0.f;
+            for (int i = 0; i < 4; ++i) {
+                lo.v[i] = at[i] < N ? row[at[i]] : from_f32<T>(0.f);
+                hi.v[i] = at[4 + i] < N ? row[at[4 + i]] : from_f32<T>(0.f);
+            }
+        }
     }
-}
+    __device__ __forceinline__ void get(float (&v)[8]) const {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[i] = to_f32(lo.v[i]);
+            v[4 + i] = to_f32(hi.v[i]);
+        }
+    }
+};
 template <typename T, bool Vec>
 __device__ __forceinline__ void store8(T* row, const int (&at)[8], int N, const float (&v)[8]) {
     if constexpr (Vec) {
@@ -199,26 +209,38 @@ norm_rotate_kernel(const Args a) {
             }
         }
         for (int64_t tl = blockIdx.x; tl < a.ntile; tl += gridDim.x) {
-            const int64_t t0 = tl * a.tile;
-            const int nt = (int)(a.tokens - t0 < a.tile ? a.tokens - t0 : a.tile);
+            const int64_t bb = tl / a.tiles, t0 = (tl - bb * a.tiles) * a.tile;
+            const int nt = (int)(a.L - t0 < a.tile ? a.L - t0 : a.tile);
             __syncthreads();                        // the last tile's readers are done
             for (int i = threadIdx.x; i < nt * half; i += kThreads) {
                 const int t = i / half;
-                table[i] = cos_sin(a.pos[t0 + t], steps[i - t * half]);
+                table[i] = cos_sin(a.pos[bb * a.L + t0 + t], steps[i - t * half]);
+            }
+            // this unit's rows of the tile, the next one loaded a step ahead
+            const Stride st = isB ? a.bs : a.cs;
+            const T* src = static_cast<const T*>(isB ? a.B : a.C) + bb * st.batch +
+                           (t0 + slot) * st.token + (int64_t)g * a.N;
+            const int64_t dense = ((bb * a.L + t0 + slot) * a.G + g) * a.N, step = (int64_t)slots * a.G * a.N;
+            T* dst = static_cast<T*>(isB ? a.oB : a.oC) + dense;
+            const TG* grd = Bwd ? static_cast<const TG*>(isB ? a.gB : a.gC) + dense : nullptr;
+            Row8<T, Vec> nv{};
+            Row8<TG, Vec> nd{};
+            if (mine && on && slot < nt) {
+                nv.load(src, at, a.N);
+                if (Bwd) nd.load(grd, at, a.N);
             }
             __syncthreads();
             for (int t = slot; t - slot < nt; t += slots) {      // uniform in a warp's units
-                const bool live = mine && t < nt;
-                const int64_t tok = t0 + (live ? t : 0);
-                const int64_t bb = tok / a.L, tt = tok - bb * a.L;
-                const Stride st = isB ? a.bs : a.cs;
-                const T* src = static_cast<const T*>(isB ? a.B : a.C) + bb * st.batch +
-                               tt * st.token + (int64_t)g * a.N;
-                const int64_t dense = (tok * a.G + g) * a.N;
-                float v[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) v[i] = 0.f;
-                if (live && on) load8<T, Vec>(src, at, a.N, v);
+                const bool live = mine && on && t < nt;
+                float v[8], d[8];
+                nv.get(v);
+                if (Bwd) nd.get(d);
+                src += slots * st.token;
+                if (Bwd) grd += step;
+                if (mine && on && t + slots < nt) {
+                    nv.load(src, at, a.N);
+                    if (Bwd) nd.load(grd, at, a.N);
+                }
                 float2 cs[4];
 #pragma unroll
                 for (int q = 0; q < 4; ++q)
@@ -228,34 +250,29 @@ norm_rotate_kernel(const Args a) {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) sq = fmaf(v[i], v[i], sq);
                 const float r = rsqrtf(unit_sum(sq, a.lanes) * inv_n + a.eps);
-                T* dst = static_cast<T*>(isB ? a.oB : a.oC) + dense;
                 if constexpr (!Bwd) {
                     float u[8];
 #pragma unroll
                     for (int i = 0; i < 8; ++i) u[i] = v[i] * r * w[i];
                     if (halves) turn_pairs<true>(u, cs, 1.f);
                     else turn_pairs<false>(u, cs, 1.f);
-                    if (live && on) store8<T, Vec>(dst, at, a.N, u);
+                    if (live) store8<T, Vec>(dst, at, a.N, u);
                 } else {
-                    float d[8];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) d[i] = 0.f;
-                    if (live && on)
-                        load8<TG, Vec>(static_cast<const TG*>(isB ? a.gB : a.gC) + dense, at, a.N, d);
                     if (halves) turn_pairs<true>(d, cs, -1.f);
                     else turn_pairs<false>(d, cs, -1.f);
                     float dot = 0.f;
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
-                        dw[i] = fmaf(d[i], v[i] * r, dw[i]);
+                        if (live) dw[i] = fmaf(d[i], v[i] * r, dw[i]);
                         d[i] *= w[i];
                         dot = fmaf(d[i], v[i], dot);
                     }
                     const float m = unit_sum(dot, a.lanes) * inv_n * r * r;
 #pragma unroll
                     for (int i = 0; i < 8; ++i) d[i] = r * (d[i] - v[i] * m);
-                    if (live && on) store8<T, Vec>(dst, at, a.N, d);
+                    if (live) store8<T, Vec>(dst, at, a.N, d);
                 }
+                dst += step;
             }
         }
         if constexpr (Bwd) {
@@ -279,9 +296,9 @@ norm_rotate_kernel(const Args a) {
 }
 
 // dweight: the blocks' partial rows (and, for weights that all groups share,
-// the groups') added in a fixed order.  32 columns x 8 row groups a block;
+// the groups') added in a fixed order.  32 columns x 32 row groups a block;
 // blockIdx.y: B or C.
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(1024)
 norm_reduce_kernel(const float* __restrict__ part, int64_t blocks, int G, int N, int per_group,
                    float* __restrict__ dwB, float* __restrict__ dwC) {
     const int which = blockIdx.y;
@@ -290,17 +307,17 @@ norm_reduce_kernel(const float* __restrict__ part, int64_t blocks, int G, int N,
     const int64_t rows = per_group ? blocks : blocks * G;
     float v = 0.f;
     if (j < cols)
-        for (int64_t r = threadIdx.y; r < rows; r += 8) {
+        for (int64_t r = threadIdx.y; r < rows; r += 32) {
             const int64_t block = per_group ? r : r / G;
             const int64_t off = per_group ? j : (r % G) * N + j;
             v += part[(block * 2 + which) * G * N + off];
         }
-    __shared__ float red[8][32];
+    __shared__ float red[32][33];
     red[threadIdx.y][threadIdx.x] = v;
     __syncthreads();
     if (threadIdx.y || j >= cols) return;
-#pragma unroll
-    for (int q = 1; q < 8; ++q) v += red[q][threadIdx.x];
+#pragma unroll 8
+    for (int q = 1; q < 32; ++q) v += red[q][threadIdx.x];
     (which ? dwC : dwB)[j] = v;
 }
 
@@ -310,11 +327,31 @@ int lanes_of(int N) {
     return lanes;
 }
 
-int64_t tile_of(int64_t tokens) { return tokens < 32 * 592 ? (tokens < 4 * 592 ? 1 : 8) : 32; }
+// Tiles of 32 tokens, shorter where those are too few to give every SM four blocks.
+int tile_of(const RotateDims& d) {
+    int tile = 32;
+    while (tile > 1 && d.b * ((d.L + tile - 1) / tile) < 592) tile /= 2;
+    return tile;
+}
 
-int64_t blocks_of(int64_t tokens) {
-    const int64_t n = (tokens + tile_of(tokens) - 1) / tile_of(tokens);
+int64_t blocks_of(const RotateDims& d) {
+    const int64_t n = d.b * ((d.L + tile_of(d) - 1) / tile_of(d));
     return n < 592 ? n : 592;            // four blocks for each of 148 SMs
+}
+
+// Sequences that lie behind one another as their tokens do are one long sequence,
+// of which tiles then hold whole (single tokens of many sequences above all).
+RotateDims joined(RotateArgs& r, const RotateDims& d) {
+    if (d.L == 1) {
+        r.bs.token = r.bs.batch;
+        r.cs.token = r.cs.batch;
+    } else if (r.bs.batch != d.L * r.bs.token || r.cs.batch != d.L * r.cs.token) {
+        return d;
+    }
+    RotateDims j = d;
+    j.b = 1;
+    j.L = d.b * d.L;
+    return j;
 }
 
 template <typename T>
@@ -328,22 +365,23 @@ Args args_of(const RotateArgs& r, const RotateDims& d) {
     a.B = r.B; a.C = r.C; a.bs = r.bs; a.cs = r.cs; a.wB = r.wB; a.wC = r.wC;
     a.per_group = r.per_group; a.pos = r.pos; a.freq = r.freq; a.eps = r.eps;
     a.interleaved = r.interleaved;
-    a.tokens = d.b * d.L; a.L = d.L; a.G = (int)d.G; a.N = (int)d.N; a.R = (int)d.R;
+    a.L = d.L; a.G = (int)d.G; a.N = (int)d.N; a.R = (int)d.R;
     a.lanes = lanes_of(a.N);
-    a.tile = (int)tile_of(a.tokens);
-    a.ntile = (a.tokens + a.tile - 1) / a.tile;
+    a.tile = tile_of(d);
+    a.tiles = (d.L + a.tile - 1) / a.tile;
+    a.ntile = d.b * a.tiles;
     return a;
 }
 
 template <typename T, typename TG, bool Bwd>
-cudaError_t run(const Args& a, cudaStream_t s) {
+cudaError_t run(const Args& a, int64_t nblocks, cudaStream_t s) {
     const int units = kThreads / a.lanes, rows = 2 * a.G, wide = rows < units ? rows : units;
     size_t smem = (size_t)a.tile * (a.R / 2) * sizeof(float2);
     if (Bwd) {
         const size_t acc = (size_t)(units / wide) * wide * a.N * 4;
         smem = smem > acc ? smem : acc;
     }
-    const unsigned blocks = (unsigned)blocks_of(a.tokens);
+    const unsigned blocks = (unsigned)nblocks;
     const bool vec = a.N % 8 == 0 && a.R / 2 % 4 == 0 && vec_rows<T>(a.B, a.bs) &&
                      vec_rows<T>(a.C, a.cs);
     if (vec) norm_rotate_kernel<T, TG, true, Bwd><<<blocks, kThreads, smem, s>>>(a);
@@ -353,32 +391,41 @@ cudaError_t run(const Args& a, cudaStream_t s) {
 
 }  // namespace
 
-cudaError_t launch_norm_rotate_fwd(const RotateArgs& r, void* oB, void* oC, const RotateDims& d,
-                                   Elt t, cudaStream_t s) {
+cudaError_t launch_norm_rotate_fwd(const RotateArgs& args, void* oB, void* oC,
+                                   const RotateDims& dims, Elt t, cudaStream_t s) {
+    RotateArgs r = args;
+    const RotateDims d = joined(r, dims);
     Args a = args_of(r, d);
     a.oB = oB; a.oC = oC;
-    return t == Elt::F32 ? run<float, float, false>(a, s)
-                         : run<__nv_bfloat16, __nv_bfloat16, false>(a, s);
+    return t == Elt::F32 ? run<float, float, false>(a, blocks_of(d), s)
+                         : run<__nv_bfloat16, __nv_bfloat16, false>(a, blocks_of(d), s);
 }
 
+// Partial rows for the sequences by themselves or joined, whichever are more (the
+// workspace does not depend on the strides).
 size_t norm_rotate_bwd_workspace_bytes(const RotateDims& d) {
-    return (size_t)(blocks_of(d.b * d.L) * 2 * d.G * d.N) * 4;
+    const RotateDims j{1, d.b * d.L, d.G, d.N, d.R};
+    const int64_t n = blocks_of(d) > blocks_of(j) ? blocks_of(d) : blocks_of(j);
+    return (size_t)(n * 2 * d.G * d.N) * 4;
 }
 
-cudaError_t launch_norm_rotate_bwd(const RotateArgs& r, const void* gB, const void* gC,
+cudaError_t launch_norm_rotate_bwd(const RotateArgs& args, const void* gB, const void* gC,
                                    bool grad_f32, void* dB, void* dC, float* dwB, float* dwC,
-                                   float* ws, const RotateDims& d, Elt t, cudaStream_t s) {
+                                   float* ws, const RotateDims& dims, Elt t, cudaStream_t s) {
+    RotateArgs r = args;
+    const RotateDims d = joined(r, dims);
     Args a = args_of(r, d);
     a.gB = gB; a.gC = gC; a.oB = dB; a.oC = dC; a.part = ws;
-    if (a.tokens > 0) {
-        cudaError_t e = t == Elt::F32 ? run<float, float, true>(a, s)
-                        : grad_f32    ? run<__nv_bfloat16, float, true>(a, s)
-                                      : run<__nv_bfloat16, __nv_bfloat16, true>(a, s);
+    const int64_t n = blocks_of(d);
+    if (n > 0) {
+        cudaError_t e = t == Elt::F32 ? run<float, float, true>(a, n, s)
+                        : grad_f32    ? run<__nv_bfloat16, float, true>(a, n, s)
+                                      : run<__nv_bfloat16, __nv_bfloat16, true>(a, n, s);
         if (e != cudaSuccess) return e;
     }
     const int cols = a.per_group ? a.G * a.N : a.N;
-    norm_reduce_kernel<<<dim3((unsigned)((cols + 31) / 32), 2), dim3(32, 8), 0, s>>>(
-        ws, blocks_of(a.tokens), a.G, a.N, a.per_group, dwB, dwC);
+    norm_reduce_kernel<<<dim3((unsigned)((cols + 31) / 32), 2), dim3(32, 32), 0, s>>>(
+        ws, n, a.G, a.N, a.per_group, dwB, dwC);
     return cudaGetLastError();
 }
 
