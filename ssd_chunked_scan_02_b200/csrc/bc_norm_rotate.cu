@@ -47,6 +47,7 @@ struct Args {
     int G, N, R;
     int lanes;                        // lanes of a unit: a power of two
     int tile;                         // tokens of a block's tile, all of one sequence
+    int table_bytes;                  // of the tile's cosines and sines
     int64_t tiles, ntile;             // of a sequence, and of all
 };
 
@@ -58,13 +59,26 @@ __device__ __forceinline__ int64_t turn_step(float freq) {
     return __double2ll_rn(frac * 18446744073709551616.0);    // half a turn saturates: 2^-64 off
 }
 
+// Cosine and sine of pos * freq: the turn modulo 2^64, its upper 32 bits to the
+// nearest quarter and a rest of at most an eighth of a turn (exact), and there the
+// Taylor series, to x^9 and x^10 (below 2e-9 at pi / 4).
 __device__ __forceinline__ float2 cos_sin(int64_t pos, int64_t step) {
-    const int64_t turn = (int64_t)((uint64_t)pos * (uint64_t)step);
-    // upper 32 bits, in half turns in [-1, 1)
-    const float half = (float)(int32_t)(turn >> 32) * 4.656612873077393e-10f;
-    float2 q;
-    sincospif(half, &q.y, &q.x);
-    return q;
+    const uint32_t turn = (uint32_t)(((uint64_t)pos * (uint64_t)step) >> 32);
+    const uint32_t quarter = (turn + 0x20000000u) >> 30;
+    const float x = (float)(int32_t)(turn - (quarter << 30)) * 1.4629180792671596e-9f;   // 2 pi / 2^32
+    const float x2 = x * x;
+    float s = 2.7557319e-6f, c = -2.7557319e-7f;        // 1 / 9!, -1 / 10!
+    s = fmaf(s, x2, -1.9841270e-4f);
+    s = fmaf(s, x2, 8.3333333e-3f);
+    s = fmaf(s, x2, -1.6666667e-1f);
+    s = fmaf(s * x2, x, x);
+    c = fmaf(c, x2, 2.4801587e-5f);
+    c = fmaf(c, x2, -1.3888889e-3f);
+    c = fmaf(c, x2, 4.1666667e-2f);
+    c = fmaf(c, x2, -0.5f);
+    c = fmaf(c, x2, 1.f);
+    const float a = quarter & 1 ? s : c, b = quarter & 1 ? c : s;
+    return make_float2((quarter + 1) & 2 ? -a : a, quarter & 2 ? -b : b);
 }
 
 // Element e (0..7) of the lane's four pairs: pairs p0 .. p0+3 sit at runs of
@@ -81,33 +95,59 @@ __device__ __forceinline__ void turn_pairs(float (&v)[8], const float2 (&cs)[4],
     }
 }
 
+// Over a unit's lanes (LANES, or `lanes` where that is 0).
+template <int LANES>
 __device__ __forceinline__ float unit_sum(float v, int lanes) {
-    for (int o = lanes / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    if constexpr (LANES > 0) {
+#pragma unroll
+        for (int o = LANES / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    } else {
+        for (int o = lanes / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    }
     return v;
 }
 
-// A row's eight elements of a lane as loaded.  Vec: the runs of four are whole,
-// aligned loads; otherwise each element is loaded on its own where it exists.
+// A lane's part of the rows to come.  Vec: the runs of four are whole, aligned
+// copies of 8 or 16 bytes, kAhead rows ahead through a ring in shared memory (a
+// lane copies and reads its own elements: no barrier); otherwise each element is
+// loaded on its own, where it exists, as its row is taken.
+constexpr int kRing = 4, kAhead = kRing - 1;
+
 template <typename T, bool Vec>
-struct Row8 {
-    Raw<T, 4> lo, hi;
-    __device__ __forceinline__ void load(const T* row, const int (&at)[8], int N) {
+struct Rows {
+    static constexpr int kBytes = Vec ? kRing * kThreads * 8 * (int)sizeof(T) : 0;
+    Raw<T, 4>* ring;                  // [kRing][2][threads], this thread's column
+    const T* ask_at;
+    const T* take_at;
+    int64_t step;
+    __device__ __forceinline__ Rows(unsigned char* smem)
+        : ring(reinterpret_cast<Raw<T, 4>*>(smem) + threadIdx.x), ask_at(nullptr), take_at(nullptr),
+          step(0) {}
+    __device__ __forceinline__ void start(const T* p, int64_t stride) {
+        ask_at = take_at = p;
+        step = stride;
+    }
+    __device__ __forceinline__ void ask(int i, bool exists, const int (&at)[8]) {
         if constexpr (Vec) {
-            lo = raw_load<T, 4>(row + at[0]);
-            hi = raw_load<T, 4>(row + at[4]);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                lo.v[i] = at[i] < N ? row[at[i]] : from_f32<T>(0.f);
-                hi.v[i] = at[4 + i] < N ? row[at[4 + i]] : from_f32<T>(0.f);
+            if (exists) {
+                copy_async(ring + (i % kRing * 2) * kThreads, ask_at + at[0], true);
+                copy_async(ring + (i % kRing * 2 + 1) * kThreads, ask_at + at[4], true);
             }
+            ask_at += step;
         }
     }
-    __device__ __forceinline__ void get(float (&v)[8]) const {
+    __device__ __forceinline__ void take(int i, bool exists, const int (&at)[8], int N, float (&v)[8]) {
+        if constexpr (Vec) {
+            const Raw<T, 4> lo = ring[(i % kRing * 2) * kThreads], hi = ring[(i % kRing * 2 + 1) * kThreads];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            v[i] = to_f32(lo.v[i]);
-            v[4 + i] = to_f32(hi.v[i]);
+            for (int k = 0; k < 4; ++k) {
+                v[k] = exists ? to_f32(lo.v[k]) : 0.f;
+                v[4 + k] = exists ? to_f32(hi.v[k]) : 0.f;
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[k] = exists && at[k] < N ? to_f32(take_at[at[k]]) : 0.f;
+            take_at += step;
         }
     }
 };
@@ -173,103 +213,142 @@ __device__ __forceinline__ void lane_pairs(int lane, int N, int R, bool interlea
     }
 }
 
-template <typename T, typename TG, bool Vec, bool Bwd>
+// Halves: pairs (p, p + R / 2).  LANES: lanes of a unit where that is known (16
+// and 8: dstate 128 and 64), so that the sums over them are straight code.
+template <typename T, typename TG, bool Vec, bool Halves, int LANES, bool Bwd>
 __global__ void __launch_bounds__(kThreads)
 norm_rotate_kernel(const Args a) {
-    extern __shared__ float2 table[];               // (tile, R / 2): cosine, sine
-    __shared__ int64_t steps[128];
-    const int half = a.R / 2, rows = 2 * a.G;
-    for (int k = threadIdx.x; k < half; k += kThreads) steps[k] = turn_step(a.freq[k]);
-    const int units = kThreads / a.lanes;
-    const int unit = threadIdx.x / a.lanes, lane = threadIdx.x % a.lanes;
+    extern __shared__ __align__(16) unsigned char smem[];
+    float* table = reinterpret_cast<float*>(smem);     // (tile, 2, R / 2): cosines, sines
+    Rows<T, Vec> xr(smem + a.table_bytes);
+    Rows<TG, Vec> gr(smem + a.table_bytes + Rows<T, Vec>::kBytes);
+    const int half = a.R / 2, rows = 2 * a.G, lanes = LANES > 0 ? LANES : a.lanes;
+    const int units = kThreads / lanes;
+    const int unit = threadIdx.x / lanes, lane = threadIdx.x % lanes;
     // rows of a token a block walks at once, and the tokens side by side
     const int wide = rows < units ? rows : units, slots = units / wide;
     const int slot = unit / wide;
     const float inv_n = 1.f / (float)a.N;
+    // the pair whose angles this thread computes, and the tokens it does so for
+    int pairs = 1;
+    while (pairs < half) pairs *= 2;
+    const int pair = threadIdx.x % pairs, pair_from = threadIdx.x / pairs, pair_step = kThreads / pairs;
+    const int64_t turn = pair < half ? turn_step(a.freq[pair]) : 0;
 
-    // Vec: halves in lanes whose pairs are all turned, neighbours elsewhere
+    // (elements that no pair turns follow the same order: lane_elements)
     int at[8];
-    const bool halves = Vec ? (!a.interleaved && lane * 4 < half) : true;
-    if constexpr (Vec) lane_elements(lane, a.N, a.R, a.interleaved, at);
-    else lane_pairs(lane, a.N, a.R, a.interleaved, at);
+    if constexpr (Vec) lane_elements(lane, a.N, a.R, !Halves, at);
+    else lane_pairs(lane, a.N, a.R, !Halves, at);
     const bool on = Vec ? lane * 8 < a.N : true;    // spare lanes of a row hold zeros
+    const bool turned = lane * 4 < half;            // Vec: all of the lane's pairs or none
+    constexpr bool kHalves = Vec ? Halves : true;   // lane_pairs puts pair q at (q, 4 + q)
 
     for (int first = 0; first < rows; first += wide) {
         const int row = first + unit % wide;
         const bool mine = slot < slots && row < rows;
         const bool isB = row < a.G;
         const int g = isB ? row : row - a.G;
-        float w[8], dw[8];
+        F2 w2[4], dw2[4];
         {
+            float w[8];
             const float* wp = (isB ? a.wB : a.wC) + (a.per_group ? (int64_t)g * a.N : 0);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 w[i] = mine && on && at[i] < a.N ? wp[at[i]] : 0.f;
-                dw[i] = 0.f;
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                w2[i] = pack2(w[2 * i], w[2 * i + 1]);
+                dw2[i] = 0;
             }
         }
         for (int64_t tl = blockIdx.x; tl < a.ntile; tl += gridDim.x) {
             const int64_t bb = tl / a.tiles, t0 = (tl - bb * a.tiles) * a.tile;
             const int nt = (int)(a.L - t0 < a.tile ? a.L - t0 : a.tile);
-            __syncthreads();                        // the last tile's readers are done
-            for (int i = threadIdx.x; i < nt * half; i += kThreads) {
-                const int t = i / half;
-                table[i] = cos_sin(a.pos[bb * a.L + t0 + t], steps[i - t * half]);
-            }
-            // this unit's rows of the tile, the next one loaded a step ahead
+            // this unit's rows of the tile, kAhead of them on their way
             const Stride st = isB ? a.bs : a.cs;
-            const T* src = static_cast<const T*>(isB ? a.B : a.C) + bb * st.batch +
-                           (t0 + slot) * st.token + (int64_t)g * a.N;
             const int64_t dense = ((bb * a.L + t0 + slot) * a.G + g) * a.N, step = (int64_t)slots * a.G * a.N;
             T* dst = static_cast<T*>(isB ? a.oB : a.oC) + dense;
-            const TG* grd = Bwd ? static_cast<const TG*>(isB ? a.gB : a.gC) + dense : nullptr;
-            Row8<T, Vec> nv{};
-            Row8<TG, Vec> nd{};
-            if (mine && on && slot < nt) {
-                nv.load(src, at, a.N);
-                if (Bwd) nd.load(grd, at, a.N);
-            }
+            xr.start(static_cast<const T*>(isB ? a.B : a.C) + bb * st.batch + (t0 + slot) * st.token +
+                     (int64_t)g * a.N, slots * st.token);
+            if (Bwd) gr.start(static_cast<const TG*>(isB ? a.gB : a.gC) + dense, step);
+            auto ask = [&](int i) {
+                const bool exists = mine && on && slot + i * slots < nt;
+                xr.ask(i, exists, at);
+                if (Bwd) gr.ask(i, exists, at);
+                copies_commit();
+            };
+            for (int i = 0; i < kAhead; ++i) ask(i);
+            __syncthreads();                        // the last tile's readers are done
+            for (int t = pair_from; t < nt; t += pair_step)
+                if (pair < half) {
+                    const float2 q = cos_sin(a.pos[bb * a.L + t0 + t], turn);
+                    table[2 * t * half + pair] = q.x;
+                    table[(2 * t + 1) * half + pair] = q.y;
+                }
             __syncthreads();
-            for (int t = slot; t - slot < nt; t += slots) {      // uniform in a warp's units
+            for (int i = 0; i * slots < nt; ++i) {               // uniform in a block
+                const int t = slot + i * slots;
                 const bool live = mine && on && t < nt;
                 float v[8], d[8];
-                nv.get(v);
-                if (Bwd) nd.get(d);
-                src += slots * st.token;
-                if (Bwd) grd += step;
-                if (mine && on && t + slots < nt) {
-                    nv.load(src, at, a.N);
-                    if (Bwd) nd.load(grd, at, a.N);
+                copies_pending<kAhead - 1>();
+                xr.take(i, live, at, a.N, v);
+                if (Bwd) gr.take(i, live, at, a.N, d);
+                ask(i + kAhead);
+                F2 v2[4], sq2 = 0;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    v2[k] = pack2(v[2 * k], v[2 * k + 1]);
+                    sq2 = fma2(v2[k], v2[k], sq2);
                 }
-                float2 cs[4];
+                const float2 sq = unpack2(sq2);
+                const float r = rsqrtf(unit_sum<LANES>(sq.x + sq.y, lanes) * inv_n + a.eps);
+                const F2 rr = pack2(r, r);
+                auto turn_by = [&](float (&u)[8], float sign) {
+                    if (!turned || !live) return;
+                    float2 cs[4];
+                    const float* tc = table + 2 * t * half + lane * 4;
+                    if constexpr (Vec) {
+                        const float4 c4 = *reinterpret_cast<const float4*>(tc);
+                        const float4 s4 = *reinterpret_cast<const float4*>(tc + half);
+                        cs[0] = make_float2(c4.x, s4.x); cs[1] = make_float2(c4.y, s4.y);
+                        cs[2] = make_float2(c4.z, s4.z); cs[3] = make_float2(c4.w, s4.w);
+                    } else {
 #pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    cs[q] = live && lane * 4 + q < half ? table[t * half + lane * 4 + q]
+                        for (int q = 0; q < 4; ++q)
+                            cs[q] = lane * 4 + q < half ? make_float2(tc[q], tc[q + half])
                                                         : make_float2(1.f, 0.f);
-                float sq = 0.f;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) sq = fmaf(v[i], v[i], sq);
-                const float r = rsqrtf(unit_sum(sq, a.lanes) * inv_n + a.eps);
-                if constexpr (!Bwd) {
-                    float u[8];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) u[i] = v[i] * r * w[i];
-                    if (halves) turn_pairs<true>(u, cs, 1.f);
-                    else turn_pairs<false>(u, cs, 1.f);
-                    if (live) store8<T, Vec>(dst, at, a.N, u);
-                } else {
-                    if (halves) turn_pairs<true>(d, cs, -1.f);
-                    else turn_pairs<false>(d, cs, -1.f);
-                    float dot = 0.f;
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        if (live) dw[i] = fmaf(d[i], v[i] * r, dw[i]);
-                        d[i] *= w[i];
-                        dot = fmaf(d[i], v[i], dot);
                     }
-                    const float m = unit_sum(dot, a.lanes) * inv_n * r * r;
+                    turn_pairs<kHalves>(u, cs, sign);
+                };
+                if constexpr (!Bwd) {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) d[i] = r * (d[i] - v[i] * m);
+                    for (int k = 0; k < 4; ++k) {
+                        const float2 u = unpack2(mul2(mul2(v2[k], rr), w2[k]));
+                        v[2 * k] = u.x;
+                        v[2 * k + 1] = u.y;
+                    }
+                    turn_by(v, 1.f);
+                    if (live) store8<T, Vec>(dst, at, a.N, v);
+                } else {
+                    turn_by(d, -1.f);
+                    F2 dot2 = 0, d2[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        d2[k] = pack2(d[2 * k], d[2 * k + 1]);
+                        dw2[k] = fma2(d2[k], mul2(v2[k], rr), dw2[k]);
+                        d2[k] = mul2(d2[k], w2[k]);
+                        dot2 = fma2(d2[k], v2[k], dot2);
+                    }
+                    const float2 dot = unpack2(dot2);
+                    const float m = -unit_sum<LANES>(dot.x + dot.y, lanes) * inv_n * r * r;
+                    const F2 mm = pack2(m, m);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const float2 o = unpack2(mul2(rr, fma2(v2[k], mm, d2[k])));
+                        d[2 * k] = o.x;
+                        d[2 * k + 1] = o.y;
+                    }
                     if (live) store8<T, Vec>(dst, at, a.N, d);
                 }
                 dst += step;
@@ -277,12 +356,15 @@ norm_rotate_kernel(const Args a) {
         }
         if constexpr (Bwd) {
             // the block's partial sums: its slots' in order
-            float* acc = reinterpret_cast<float*>(table);        // (slots, wide, N)
+            float* acc = reinterpret_cast<float*>(smem);         // (slots, wide, N)
+            copies_pending<0>();
             __syncthreads();
             if (mine && on) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    if (at[i] < a.N) acc[(slot * wide + unit % wide) * a.N + at[i]] = dw[i];
+                for (int i = 0; i < 8; ++i) {
+                    const float2 q = unpack2(dw2[i / 2]);
+                    if (at[i] < a.N) acc[(slot * wide + unit % wide) * a.N + at[i]] = i % 2 ? q.y : q.x;
+                }
             }
             __syncthreads();
             for (int j = threadIdx.x; j < wide * a.N; j += kThreads) {
@@ -291,6 +373,7 @@ norm_rotate_kernel(const Args a) {
                 for (int q = 0; q < slots; ++q) v += acc[q * wide * a.N + j];
                 a.part[((int64_t)blockIdx.x * rows + first) * a.N + j] = v;
             }
+            __syncthreads();                        // before the next rows' copies land there
         }
     }
 }
@@ -304,14 +387,20 @@ norm_reduce_kernel(const float* __restrict__ part, int64_t blocks, int G, int N,
     const int which = blockIdx.y;
     const int cols = per_group ? G * N : N;
     const int j = blockIdx.x * 32 + threadIdx.x;
+    // eight rows in flight; the groups of one block's partial rows lie N apart
     const int64_t rows = per_group ? blocks : blocks * G;
     float v = 0.f;
-    if (j < cols)
-        for (int64_t r = threadIdx.y; r < rows; r += 32) {
-            const int64_t block = per_group ? r : r / G;
-            const int64_t off = per_group ? j : (r % G) * N + j;
-            v += part[(block * 2 + which) * G * N + off];
+    if (j < cols) {
+        const float* p = part + (int64_t)which * G * N + j;
+        if (per_group) {
+#pragma unroll 8
+            for (int b = threadIdx.y; b < (int)rows; b += 32) v += __ldg(p + (int64_t)b * 2 * G * N);
+        } else {
+#pragma unroll 8
+            for (int r = threadIdx.y; r < (int)rows; r += 32)
+                v += __ldg(p + (int64_t)(r / G) * 2 * G * N + (r % G) * N);
         }
+    }
     __shared__ float red[32][33];
     red[threadIdx.y][threadIdx.x] = v;
     __syncthreads();
@@ -327,16 +416,18 @@ int lanes_of(int N) {
     return lanes;
 }
 
-// Tiles of 32 tokens, shorter where those are too few to give every SM four blocks.
+// Four blocks for each of 148 SMs, each with the same number of tiles of at most
+// 32 tokens.
 int tile_of(const RotateDims& d) {
-    int tile = 32;
-    while (tile > 1 && d.b * ((d.L + tile - 1) / tile) < 592) tile /= 2;
-    return tile;
+    const int64_t per = (d.b * d.L + 591) / 592;         // tokens of a block
+    const int64_t tiles = (per + 31) / 32;
+    const int64_t tile = tiles > 0 ? (per + tiles - 1) / tiles : 1;
+    return (int)(tile < d.L ? tile : (d.L > 0 ? d.L : 1));
 }
 
 int64_t blocks_of(const RotateDims& d) {
     const int64_t n = d.b * ((d.L + tile_of(d) - 1) / tile_of(d));
-    return n < 592 ? n : 592;            // four blocks for each of 148 SMs
+    return n < 592 ? n : 592;
 }
 
 // Sequences that lie behind one another as their tokens do are one long sequence,
@@ -373,20 +464,37 @@ Args args_of(const RotateArgs& r, const RotateDims& d) {
     return a;
 }
 
-template <typename T, typename TG, bool Bwd>
-cudaError_t run(const Args& a, int64_t nblocks, cudaStream_t s) {
+template <typename T, typename TG, bool Bwd, bool Vec>
+cudaError_t launch(Args& a, int64_t blocks, cudaStream_t s) {
     const int units = kThreads / a.lanes, rows = 2 * a.G, wide = rows < units ? rows : units;
-    size_t smem = (size_t)a.tile * (a.R / 2) * sizeof(float2);
-    if (Bwd) {
-        const size_t acc = (size_t)(units / wide) * wide * a.N * 4;
-        smem = smem > acc ? smem : acc;
-    }
-    const unsigned blocks = (unsigned)nblocks;
+    a.table_bytes = (a.tile * (a.R / 2) * (int)sizeof(float2) + 15) / 16 * 16;
+    int smem = a.table_bytes + Rows<T, Vec>::kBytes + (Bwd ? Rows<TG, Vec>::kBytes : 0);
+    const int acc = units / wide * wide * a.N * 4;
+    if (Bwd && smem < acc) smem = acc;
+    auto go = [&](auto kernel) {
+        if (smem > 48 * 1024) {
+            const cudaError_t e = cudaFuncSetAttribute(
+                kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+            if (e != cudaSuccess) return e;
+        }
+        kernel<<<(unsigned)blocks, kThreads, smem, s>>>(a);
+        return cudaGetLastError();
+    };
+    if (Vec && a.lanes == 16)
+        return a.interleaved ? go(norm_rotate_kernel<T, TG, Vec, false, Vec ? 16 : 0, Bwd>)
+                             : go(norm_rotate_kernel<T, TG, Vec, true, Vec ? 16 : 0, Bwd>);
+    if (Vec && a.lanes == 8)
+        return a.interleaved ? go(norm_rotate_kernel<T, TG, Vec, false, Vec ? 8 : 0, Bwd>)
+                             : go(norm_rotate_kernel<T, TG, Vec, true, Vec ? 8 : 0, Bwd>);
+    return a.interleaved ? go(norm_rotate_kernel<T, TG, Vec, false, 0, Bwd>)
+                         : go(norm_rotate_kernel<T, TG, Vec, true, 0, Bwd>);
+}
+
+template <typename T, typename TG, bool Bwd>
+cudaError_t run(Args& a, int64_t blocks, cudaStream_t s) {
     const bool vec = a.N % 8 == 0 && a.R / 2 % 4 == 0 && vec_rows<T>(a.B, a.bs) &&
                      vec_rows<T>(a.C, a.cs);
-    if (vec) norm_rotate_kernel<T, TG, true, Bwd><<<blocks, kThreads, smem, s>>>(a);
-    else norm_rotate_kernel<T, TG, false, Bwd><<<blocks, kThreads, smem, s>>>(a);
-    return cudaGetLastError();
+    return vec ? launch<T, TG, Bwd, true>(a, blocks, s) : launch<T, TG, Bwd, false>(a, blocks, s);
 }
 
 }  // namespace
