@@ -402,74 +402,136 @@ scan_fwd_kernel(const SelectiveArgs a, T* __restrict__ y, float* __restrict__ fi
 
 // ------------------------------------------------------------------ one token
 // Each state element is read and written once (8 bytes against one
-// exponential): a stream.  Lanes of a channel as in decode: four neighbouring
-// states each.
-template <typename T, bool Vec>
+// exponential): a stream.  Four neighbouring states a lane, as in decode.  A
+// thread takes its channel of kStepBatch sequences, whose states are all under
+// way before the first is used, and reads A once for them; what a channel and
+// sequence needs once (softplus, gate) is shared out over the channel's lanes.
+constexpr int kStepBatch = 4;
+
+template <typename T, int LANES, bool Vec>
 __global__ void __launch_bounds__(256)
 step_kernel(float* __restrict__ state, const SelectiveArgs a, T* __restrict__ y,
-            const SelectiveDims d, int lanes) {
-    const int per = 256 / lanes;
-    const int lane = threadIdx.x % lanes;
-    const int64_t item = (int64_t)blockIdx.x * per + threadIdx.x / lanes;
-    const bool on = item < d.b * d.D;
-    const int64_t bb = on ? item / d.D : 0, c = on ? item - bb * d.D : 0;
-    const int64_t g = c / (d.D / d.G);
-    float v = 0.f, xv = 0.f;
-    if (on) {
-        xv = to_f32(static_cast<const T*>(a.x)[bb * a.xs.batch + c]);
-        v = to_f32(static_cast<const T*>(a.dt)[bb * a.dts.batch + c]) +
-            (a.dt_bias ? a.dt_bias[c] : 0.f);
-        if (a.softplus) v = softplus_f32(v);
-    }
-    const float u = v * xv;
-    const T* Bp = static_cast<const T*>(a.B) + bb * a.Bs.batch + g * d.N;
-    const T* Cp = static_cast<const T*>(a.C) + bb * a.Cs.batch + g * d.N;
-    float* st = state + (bb * d.D + c) * d.N;
-    const float* Ar = a.A + c * d.N;
-    float acc = 0.f;
-    if (on) {
-        for (int64_t n = lane * 4; n < d.N; n += lanes * 4) {
-            float hs[4], As[4], Bs[4], Cs[4];
+            const SelectiveDims d) {
+    constexpr int KB = kStepBatch, PER = 256 / LANES;
+    constexpr int OWN = LANES >= KB ? 1 : KB / LANES;      // sequences a lane is in charge of
+    constexpr int SPAN = LANES >= KB ? LANES / KB : 1;     // lanes in charge of one
+    const int lane = threadIdx.x % LANES, N = (int)d.N, D = (int)d.D;
+    const unsigned across = (unsigned)((D + PER - 1) / PER);             // blocks of a sequence
+    const int64_t at = (int64_t)(blockIdx.x % across) * PER + threadIdx.x / LANES;
+    const bool on = at < D;
+    const int c = on ? (int)at : 0, g = c / (int)(d.D / d.G);
+    const int64_t b0 = (int64_t)(blockIdx.x / across) * KB;
+    const int nb = d.b - b0 < KB ? (int)(d.b - b0) : KB;
+    const float* Ar = a.A + (int64_t)c * N;
+    float* st = state + (b0 * D + c) * N;
+    const int64_t next = (int64_t)D * N;                   // the same channel of the next sequence
+    const T* Bp = static_cast<const T*>(a.B) + b0 * a.Bs.batch + g * N;
+    const T* Cp = static_cast<const T*>(a.C) + b0 * a.Cs.batch + g * N;
+
+    // one round for up to 4 LANES states, two for 129 to 256
+    float hs[KB][4], Bs[KB][4], Cs[KB][4], As[4], acc[KB];
+    auto load = [&](int n) {
+#pragma unroll
+        for (int k = 0; k < KB; ++k) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) hs[k][i] = Bs[k][i] = Cs[k][i] = 0.f;
+            if (k >= nb || !on || n >= N) continue;
             if constexpr (Vec) {
-                const float4 q = __ldcs(reinterpret_cast<const float4*>(st + n));
-                const float4 r = __ldg(reinterpret_cast<const float4*>(Ar + n));
-                hs[0] = q.x; hs[1] = q.y; hs[2] = q.z; hs[3] = q.w;
-                As[0] = r.x; As[1] = r.y; As[2] = r.z; As[3] = r.w;
-                raw_to_f32(raw_load<T, 4>(Bp + n), Bs);
-                raw_to_f32(raw_load<T, 4>(Cp + n), Cs);
+                const float4 q = __ldcs(reinterpret_cast<const float4*>(st + k * next + n));
+                hs[k][0] = q.x; hs[k][1] = q.y; hs[k][2] = q.z; hs[k][3] = q.w;
+                raw_to_f32(raw_load<T, 4>(Bp + k * a.Bs.batch + n), Bs[k]);
+                raw_to_f32(raw_load<T, 4>(Cp + k * a.Cs.batch + n), Cs[k]);
             } else {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const bool in = n + i < d.N;
-                    hs[i] = in ? st[n + i] : 0.f;
-                    As[i] = in ? Ar[n + i] : 0.f;
-                    Bs[i] = in ? to_f32(Bp[n + i]) : 0.f;
-                    Cs[i] = in ? to_f32(Cp[n + i]) : 0.f;
+                    if (n + i >= N) continue;
+                    hs[k][i] = st[k * next + n + i];
+                    Bs[k][i] = to_f32(Bp[k * a.Bs.batch + n + i]);
+                    Cs[k][i] = to_f32(Cp[k * a.Cs.batch + n + i]);
                 }
             }
+        }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                hs[i] = fmaf(ex2(v * kLog2E * As[i]), hs[i], u * Bs[i]);
-                acc = fmaf(Cs[i], hs[i], acc);
-            }
+        for (int i = 0; i < 4; ++i) As[i] = 0.f;
+        if (n < N) {
             if constexpr (Vec) {
-                __stcs(reinterpret_cast<float4*>(st + n), make_float4(hs[0], hs[1], hs[2], hs[3]));
+                const float4 r = __ldg(reinterpret_cast<const float4*>(Ar + n));
+                As[0] = r.x; As[1] = r.y; As[2] = r.z; As[3] = r.w;
             } else {
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (n + i < d.N) st[n + i] = hs[i];
+                for (int i = 0; i < 4; ++i) As[i] = n + i < N ? Ar[n + i] : 0.f;
+            }
+        }
+    };
+    load(lane * 4);
+
+    float v[OWN], u[OWN], skip[OWN], gate[OWN];
+#pragma unroll
+    for (int j = 0; j < OWN; ++j) {
+        const int k = lane / SPAN * OWN + j;
+        v[j] = u[j] = skip[j] = 0.f;
+        gate[j] = 1.f;
+        if (k >= nb) continue;
+        const float xv = to_f32(static_cast<const T*>(a.x)[(b0 + k) * a.xs.batch + c]);
+        v[j] = to_f32(static_cast<const T*>(a.dt)[(b0 + k) * a.dts.batch + c]) +
+               (a.dt_bias ? __ldg(a.dt_bias + c) : 0.f);
+        if (a.softplus) v[j] = softplus_f32(v[j]);
+        u[j] = v[j] * xv;
+        v[j] *= kLog2E;
+        if (a.D) skip[j] = __ldg(a.D + c) * xv;
+        if (a.z) {
+            const float zv = to_f32(static_cast<const T*>(a.z)[(b0 + k) * a.zs.batch + c]);
+            gate[j] = zv * sigmoid_fast(zv);
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < KB; ++k) acc[k] = 0.f;
+    for (int n0 = 0; n0 < N; n0 += 4 * LANES) {
+        const int n = n0 + lane * 4;
+        if (n0 > 0) load(n);
+#pragma unroll
+        for (int k = 0; k < KB; ++k) {
+            const float vk = __shfl_sync(0xffffffffu, v[k % OWN], k / OWN * SPAN, LANES);
+            const float uk = __shfl_sync(0xffffffffu, u[k % OWN], k / OWN * SPAN, LANES);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                hs[k][i] = fmaf(ex2(vk * As[i]), hs[k][i], uk * Bs[k][i]);
+                acc[k] = fmaf(Cs[k][i], hs[k][i], acc[k]);
+            }
+            if (k < nb && on && n < N) {
+                if constexpr (Vec) {
+                    __stcs(reinterpret_cast<float4*>(st + k * next + n),
+                           make_float4(hs[k][0], hs[k][1], hs[k][2], hs[k][3]));
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (n + i < N) st[k * next + n + i] = hs[k][i];
+                }
             }
         }
     }
-    for (int o = lanes / 2; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
-    if (on && lane == 0) {
-        float o = fmaf(a.D ? a.D[c] : 0.f, xv, acc);
-        if (a.z) {
-            const float zv = to_f32(static_cast<const T*>(a.z)[bb * a.zs.batch + c]);
-            o *= zv * sigmoid_fast(zv);
-        }
-        y[bb * d.D + c] = from_f32<T>(o);
+    fold<KB, LANES>(acc, lane);
+#pragma unroll
+    for (int j = 0; j < OWN; ++j) {
+        const int k = lane / SPAN * OWN + j;
+        if (on && k < nb && lane % SPAN == 0)
+            y[(b0 + k) * D + c] = from_f32<T>((acc[j] + skip[j]) * gate[j]);
     }
+}
+
+template <typename T, bool Vec>
+void step_lanes(float* state, const SelectiveArgs& a, void* y, const SelectiveDims& d, cudaStream_t s) {
+    auto go = [&](auto kernel, int lanes) {
+        const int64_t per = 256 / lanes;
+        const int64_t blocks = (d.D + per - 1) / per * ((d.b + kStepBatch - 1) / kStepBatch);
+        kernel<<<(unsigned)blocks, 256, 0, s>>>(state, a, static_cast<T*>(y), d);
+    };
+    if (d.N <= 4) go(step_kernel<T, 1, Vec>, 1);
+    else if (d.N <= 8) go(step_kernel<T, 2, Vec>, 2);
+    else if (d.N <= 16) go(step_kernel<T, 4, Vec>, 4);
+    else if (d.N <= 32) go(step_kernel<T, 8, Vec>, 8);
+    else if (d.N <= 64) go(step_kernel<T, 16, Vec>, 16);
+    else go(step_kernel<T, 32, Vec>, 32);
 }
 
 }  // namespace
@@ -556,15 +618,12 @@ cudaError_t launch_selective_checkpoints(const SelectiveArgs& a, float* ckpt, fl
 
 cudaError_t launch_selective_step(float* state, const SelectiveArgs& a, void* y,
                                   const SelectiveDims& d, Elt t, cudaStream_t s) {
-    int lanes = 1;
-    while (lanes < 32 && lanes * 4 < d.N) lanes *= 2;
-    const int64_t per = 256 / lanes, blocks = (d.b * d.D + per - 1) / per;
     with_elt(t, [&](auto ty) {
         using T = typename decltype(ty)::type;
         const bool vec = d.N % 4 == 0 && rows_fit<T>(a.B, Stride{a.Bs.batch, 0}, 4) &&
                          rows_fit<T>(a.C, Stride{a.Cs.batch, 0}, 4);
-        if (vec) step_kernel<T, true><<<(unsigned)blocks, 256, 0, s>>>(state, a, static_cast<T*>(y), d, lanes);
-        else step_kernel<T, false><<<(unsigned)blocks, 256, 0, s>>>(state, a, static_cast<T*>(y), d, lanes);
+        if (vec) step_lanes<T, true>(state, a, y, d, s);
+        else step_lanes<T, false>(state, a, y, d, s);
     });
     return cudaGetLastError();
 }
