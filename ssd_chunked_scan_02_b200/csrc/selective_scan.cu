@@ -409,19 +409,19 @@ scan_fwd_kernel(const SelectiveArgs a, T* __restrict__ y, float* __restrict__ fi
 constexpr int kStepBatch = 4;
 
 template <typename T, int LANES, bool Vec>
-__global__ void __launch_bounds__(256)
-step_kernel(float* __restrict__ state, const SelectiveArgs a, T* __restrict__ y,
-            const SelectiveDims d) {
+__global__ void __launch_bounds__(256, 3)
+step_kernel(float* __restrict__ state, const SelectiveArgs a, T* __restrict__ y, int64_t b, int D,
+            int N, int per_group, unsigned across) {
     constexpr int KB = kStepBatch, PER = 256 / LANES;
     constexpr int OWN = LANES >= KB ? 1 : KB / LANES;      // sequences a lane is in charge of
     constexpr int SPAN = LANES >= KB ? LANES / KB : 1;     // lanes in charge of one
-    const int lane = threadIdx.x % LANES, N = (int)d.N, D = (int)d.D;
-    const unsigned across = (unsigned)((D + PER - 1) / PER);             // blocks of a sequence
-    const int64_t at = (int64_t)(blockIdx.x % across) * PER + threadIdx.x / LANES;
-    const bool on = at < D;
-    const int c = on ? (int)at : 0, g = c / (int)(d.D / d.G);
-    const int64_t b0 = (int64_t)(blockIdx.x / across) * KB;
-    const int nb = d.b - b0 < KB ? (int)(d.b - b0) : KB;
+    const int lane = threadIdx.x % LANES;
+    const unsigned group = blockIdx.x / across;            // `across` blocks hold a sequence's channels
+    const unsigned at = (blockIdx.x - group * across) * PER + threadIdx.x / LANES;
+    const bool on = at < (unsigned)D;
+    const int c = on ? (int)at : 0, g = c / per_group;
+    const int64_t b0 = (int64_t)group * KB;
+    const int nb = b - b0 < KB ? (int)(b - b0) : KB;
     const float* Ar = a.A + (int64_t)c * N;
     float* st = state + (b0 * D + c) * N;
     const int64_t next = (int64_t)D * N;                   // the same channel of the next sequence
@@ -429,38 +429,33 @@ step_kernel(float* __restrict__ state, const SelectiveArgs a, T* __restrict__ y,
     const T* Cp = static_cast<const T*>(a.C) + b0 * a.Cs.batch + g * N;
 
     // one round for up to 4 LANES states, two for 129 to 256
-    float hs[KB][4], Bs[KB][4], Cs[KB][4], As[4], acc[KB];
+    float hs[KB][4], As[4], acc[KB];
+    Raw<T, 4> rB[KB], rC[KB];
     auto load = [&](int n) {
 #pragma unroll
         for (int k = 0; k < KB; ++k) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) hs[k][i] = Bs[k][i] = Cs[k][i] = 0.f;
-            if (k >= nb || !on || n >= N) continue;
+            const int kk = k < nb ? k : 0, m = n < N ? n : 0;      // what does not exist reads what does
             if constexpr (Vec) {
-                const float4 q = __ldcs(reinterpret_cast<const float4*>(st + k * next + n));
+                const float4 q = __ldcs(reinterpret_cast<const float4*>(st + kk * next + m));
                 hs[k][0] = q.x; hs[k][1] = q.y; hs[k][2] = q.z; hs[k][3] = q.w;
-                raw_to_f32(raw_load<T, 4>(Bp + k * a.Bs.batch + n), Bs[k]);
-                raw_to_f32(raw_load<T, 4>(Cp + k * a.Cs.batch + n), Cs[k]);
+                rB[k] = raw_load<T, 4>(Bp + kk * a.Bs.batch + m);
+                rC[k] = raw_load<T, 4>(Cp + kk * a.Cs.batch + m);
             } else {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    if (n + i >= N) continue;
-                    hs[k][i] = st[k * next + n + i];
-                    Bs[k][i] = to_f32(Bp[k * a.Bs.batch + n + i]);
-                    Cs[k][i] = to_f32(Cp[k * a.Cs.batch + n + i]);
+                    const bool in = n + i < N;
+                    hs[k][i] = in ? st[kk * next + n + i] : 0.f;
+                    rB[k].v[i] = in ? Bp[kk * a.Bs.batch + n + i] : from_f32<T>(0.f);
+                    rC[k].v[i] = in ? Cp[kk * a.Cs.batch + n + i] : from_f32<T>(0.f);
                 }
             }
         }
+        if constexpr (Vec) {
+            const float4 r = __ldg(reinterpret_cast<const float4*>(Ar + (n < N ? n : 0)));
+            As[0] = r.x; As[1] = r.y; As[2] = r.z; As[3] = r.w;
+        } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) As[i] = 0.f;
-        if (n < N) {
-            if constexpr (Vec) {
-                const float4 r = __ldg(reinterpret_cast<const float4*>(Ar + n));
-                As[0] = r.x; As[1] = r.y; As[2] = r.z; As[3] = r.w;
-            } else {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) As[i] = n + i < N ? Ar[n + i] : 0.f;
-            }
+            for (int i = 0; i < 4; ++i) As[i] = n + i < N ? Ar[n + i] : 0.f;
         }
     };
     load(lane * 4);
@@ -495,8 +490,8 @@ step_kernel(float* __restrict__ state, const SelectiveArgs a, T* __restrict__ y,
             const float uk = __shfl_sync(0xffffffffu, u[k % OWN], k / OWN * SPAN, LANES);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                hs[k][i] = fmaf(ex2(vk * As[i]), hs[k][i], uk * Bs[k][i]);
-                acc[k] = fmaf(Cs[k][i], hs[k][i], acc[k]);
+                hs[k][i] = fmaf(ex2(vk * As[i]), hs[k][i], uk * to_f32(rB[k].v[i]));
+                if (n < N) acc[k] = fmaf(to_f32(rC[k].v[i]), hs[k][i], acc[k]);
             }
             if (k < nb && on && n < N) {
                 if constexpr (Vec) {
@@ -522,9 +517,10 @@ step_kernel(float* __restrict__ state, const SelectiveArgs a, T* __restrict__ y,
 template <typename T, bool Vec>
 void step_lanes(float* state, const SelectiveArgs& a, void* y, const SelectiveDims& d, cudaStream_t s) {
     auto go = [&](auto kernel, int lanes) {
-        const int64_t per = 256 / lanes;
-        const int64_t blocks = (d.D + per - 1) / per * ((d.b + kStepBatch - 1) / kStepBatch);
-        kernel<<<(unsigned)blocks, 256, 0, s>>>(state, a, static_cast<T*>(y), d);
+        const int64_t across = (d.D + 256 / lanes - 1) / (256 / lanes);
+        const int64_t blocks = across * ((d.b + kStepBatch - 1) / kStepBatch);
+        kernel<<<(unsigned)blocks, 256, 0, s>>>(state, a, static_cast<T*>(y), d.b, (int)d.D, (int)d.N,
+                                                (int)(d.D / d.G), (unsigned)across);
     };
     if (d.N <= 4) go(step_kernel<T, 1, Vec>, 1);
     else if (d.N <= 8) go(step_kernel<T, 2, Vec>, 2);
