@@ -31,6 +31,19 @@ __device__ __forceinline__ float softplus_f32(float v) {
     return fmaf(w, p, fmaxf(v, 0.f));
 }
 
+// a = exp(dt A) = 2^(dl A), dl = dt log2(e).  ex2 comes out low: by 2e-8 of its value on
+// average over the exponents of slowly decaying states, (-0.3, 0) (measured over
+// 4 million of them; 3e-8 rms about that).  A state takes the product of as many
+// factors as it remembers tokens, so that the shift would build up where the rest
+// averages out; 2e-8 log2(e) added to the exponent takes it away, in the same
+// instruction (the gradient of A over 2048 tokens: 1.9e-6 off without, 1.0e-6 with).  2^(the shift)
+// alone is 1: a step of length zero leaves the state as it is.
+constexpr float kDecayShift = 2.9e-8f;
+__device__ __forceinline__ float decay(float dl, float A) { return ex2(fmaf(dl, A, kDecayShift)); }
+__device__ __forceinline__ F2 decay2(F2 dl, F2 A) {
+    return ex2_2(fma2(dl, A, pack2(kDecayShift, kDecayShift)));
+}
+
 // Adds v[i] over LANES lanes that lie STRIDE apart, `lane` being this one's place
 // among them, for all NV values at once: each step gives half of the values away and keeps the sums of the
 // other half, so NV values cost NV - NV / LANES shuffles instead of

@@ -174,7 +174,7 @@ scan_fwd_kernel(const SelectiveArgs a, T* __restrict__ y, float* __restrict__ fi
 #pragma unroll
                     for (int i = 0; i < SPL; i += 4) {
                         const float4 bv = *reinterpret_cast<const float4*>(Bt + (tt + k) * NP + i);
-                        const F2 e0 = ex2_2(mul2(dd, A[i / 2])), e1 = ex2_2(mul2(dd, A[i / 2 + 1]));
+                        const F2 e0 = decay2(dd, A[i / 2]), e1 = decay2(dd, A[i / 2 + 1]);
                         h[i / 2] = fma2(e0, h[i / 2], mul2(uu, pack2(bv.x, bv.y)));
                         h[i / 2 + 1] = fma2(e1, h[i / 2 + 1], mul2(uu, pack2(bv.z, bv.w)));
                         if (Output) {
@@ -490,7 +490,7 @@ step_kernel(float* __restrict__ state, const SelectiveArgs a, T* __restrict__ y,
             const float uk = __shfl_sync(0xffffffffu, u[k % OWN], k / OWN * SPAN, LANES);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                hs[k][i] = fmaf(ex2(vk * As[i]), hs[k][i], uk * to_f32(rB[k].v[i]));
+                hs[k][i] = fmaf(decay(vk, As[i]), hs[k][i], uk * to_f32(rB[k].v[i]));
                 if (n < N) acc[k] = fmaf(to_f32(rC[k].v[i]), hs[k][i], acc[k]);
             }
             if (k < nb && on && n < N) {

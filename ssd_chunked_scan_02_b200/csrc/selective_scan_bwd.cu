@@ -263,8 +263,8 @@ scan_bwd_kernel(const SelectiveArgs a, const SelectiveGrads gr, const float* __r
 #pragma unroll
                 for (int i = 0; i < SPL / 2; i += 2) {
                     const float4 bv = *reinterpret_cast<const float4*>(Bt + 2 * i);
-                    e[k][i] = ex2_2(mul2(dd, A[i]));
-                    e[k][i + 1] = ex2_2(mul2(dd, A[i + 1]));
+                    e[k][i] = decay2(dd, A[i]);
+                    e[k][i + 1] = decay2(dd, A[i + 1]);
                     h[k + 1][i] = fma2(e[k][i], h[k][i], mul2(uu, pack2(bv.x, bv.y)));
                     h[k + 1][i + 1] = fma2(e[k][i + 1], h[k][i + 1], mul2(uu, pack2(bv.z, bv.w)));
                 }
