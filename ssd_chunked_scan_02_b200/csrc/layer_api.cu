@@ -248,7 +248,7 @@ ssd_status_t ssd_selective_scan_fwd_workspace_size(const ssd_selective_dims_t* d
     ssd::SelectiveDims d{}; ssd::Elt t = ssd::Elt::BF16;
     ssd_status_t st = selective_dims(dims, dtype, &d, &t);
     if (st != SSD_OK) return st;
-    *bytes = ssd::selective_fwd_workspace_bytes(d);
+    *bytes = ssd::selective_fwd_workspace_bytes(d, t);
     return SSD_OK;
 }
 
@@ -276,7 +276,7 @@ ssd_status_t ssd_selective_scan_fwd(const void* x, const void* dt, const float* 
         if (z) REQUIRE_VIEW(z);
         REQUIRE_PTR(y);
     }
-    const size_t need = ssd::selective_fwd_workspace_bytes(d);
+    const size_t need = ssd::selective_fwd_workspace_bytes(d, t);
     if (workspace_bytes < need)
         return fail(SSD_ERR_INVALID_ARG, "workspace too small: %zu bytes given, %zu needed",
                     workspace_bytes, need);
@@ -295,7 +295,7 @@ ssd_status_t ssd_selective_scan_bwd_workspace_size(const ssd_selective_dims_t* d
     ssd::SelectiveDims d{}; ssd::Elt t = ssd::Elt::BF16;
     ssd_status_t st = selective_dims(dims, dtype, &d, &t);
     if (st != SSD_OK) return st;
-    *bytes = ssd::selective_bwd_workspace_bytes(d);
+    *bytes = ssd::selective_bwd_workspace_bytes(d, t);
     return SSD_OK;
 }
 
@@ -327,7 +327,7 @@ ssd_status_t ssd_selective_scan_bwd(const void* x, const void* dt, const float* 
         REQUIRE_PTR(dy); REQUIRE_PTR(dx); REQUIRE_PTR(ddt); REQUIRE_PTR(dB); REQUIRE_PTR(dC);
         if (z) { REQUIRE_VIEW(z); REQUIRE_PTR(dz); }
     }
-    const size_t need = ssd::selective_bwd_workspace_bytes(d);
+    const size_t need = ssd::selective_bwd_workspace_bytes(d, t);
     if (workspace_bytes < need)
         return fail(SSD_ERR_INVALID_ARG, "workspace too small: %zu bytes given, %zu needed",
                     workspace_bytes, need);

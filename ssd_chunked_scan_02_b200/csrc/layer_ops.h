@@ -40,7 +40,7 @@ struct SelectiveArgs {
     const int32_t* lens;
     bool softplus;
 };
-size_t selective_fwd_workspace_bytes(const SelectiveDims& d);
+size_t selective_fwd_workspace_bytes(const SelectiveDims& d, Elt t);
 cudaError_t launch_selective_fwd(const SelectiveArgs& a, void* y, float* final_states, float* ws,
                                  const SelectiveDims& d, Elt t, cudaStream_t s);
 // The states before every TS-th token, ckpt (b, ceil(L / TS), D, padded N) (ws: as
@@ -53,7 +53,7 @@ struct SelectiveGrads {
     void *dx, *ddt, *dB, *dC, *dz;
     float *dA, *dD, *ddt_bias, *dinit;
 };
-size_t selective_bwd_workspace_bytes(const SelectiveDims& d);
+size_t selective_bwd_workspace_bytes(const SelectiveDims& d, Elt t);
 cudaError_t launch_selective_bwd(const SelectiveArgs& a, const SelectiveGrads& g, float* ws,
                                  const SelectiveDims& d, Elt t, cudaStream_t s);
 cudaError_t launch_selective_step(float* state, const SelectiveArgs& a, void* y,

@@ -132,6 +132,16 @@ int64_t channel_blocks(const SelectiveDims& d) {
     return d.G * ((d.D / d.G + CH - 1) / CH);
 }
 
+// Where batch and channels are too few blocks, a sequence is cut into spans that
+// run side by side; what each does to a state that enters it is in the workspace:
+// state (b, spans - 1, D, NP), then sums of dt log2(e) (b, spans - 1, D).
+struct Spans {
+    int count;            // spans of a sequence
+    int64_t tokens;       // tokens of a span, a multiple of the tile
+    float *state, *sum;
+};
+Spans selective_spans(const SelectiveDims& d, Elt t, float* ws);
+
 // VW neighbouring channels of one token: `n` of them exist; vec: one aligned
 // load where all do.
 template <typename T, int VW>

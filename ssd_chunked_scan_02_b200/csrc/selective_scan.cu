@@ -31,14 +31,6 @@ namespace {
 
 constexpr int kWalkers = 128;      // threads of the walking warps
 
-// A span's result: state (b, spans - 1, D, NP), then sums of dt log2(e)
-// (b, spans - 1, D).
-struct Spans {
-    int count;            // spans of a sequence
-    int64_t tokens;       // tokens of a span, a multiple of the tile
-    float *state, *sum;
-};
-
 enum class What { SpanState, Output, Checkpoints };
 
 template <typename T, typename Lay>
@@ -542,18 +534,20 @@ bool selective_vec(const SelectiveArgs& a, const SelectiveDims& d, int w) {
 template bool selective_vec<float>(const SelectiveArgs&, const SelectiveDims&, int);
 template bool selective_vec<__nv_bfloat16>(const SelectiveArgs&, const SelectiveDims&, int);
 
-// Spans of a sequence: one where the blocks of (batch, channels) fill half of
-// what 148 SMs hold (four blocks each); else as many as fill it, of at least 8
-// tiles.
-Spans spans_of(const SelectiveDims& d, float* ws) {
+// Spans of a sequence: one where the blocks of (batch, channels) are two for each
+// of 148 SMs or more; else as many as give every SM what it holds (three blocks in
+// bf16, two in fp32), of at least two tiles.  Below three spans the second walk
+// over the tokens costs what the first gains.  (1 x 32768 x 1536, 9 spans: 628 us;
+// 6 spans 672, 12 spans 662, one 2300.)
+Spans selective_spans(const SelectiveDims& d, Elt t, float* ws) {
     Spans sp{1, d.L, nullptr, nullptr};
     with_layout(d.N, [&](auto lay) {
         using Lay = decltype(lay);
         const int64_t blocks = d.b * channel_blocks<Lay::CH>(d), tiles = (d.L + Lay::TT - 1) / Lay::TT;
         if (blocks == 0 || blocks >= 148 * 2) return;
-        int64_t want = 148 * 4 / blocks;
-        if (want > tiles / 8) want = tiles / 8;
-        if (want < 3) return;                       // two spans cost what they gain
+        int64_t want = 148 * (t == Elt::F32 ? 2 : 3) / blocks;
+        if (want > tiles / 2) want = tiles / 2;
+        if (want < 3) return;
         const int64_t per = (tiles + want - 1) / want;
         sp.tokens = per * Lay::TT;
         sp.count = (int)((tiles + per - 1) / per);
@@ -563,8 +557,8 @@ Spans spans_of(const SelectiveDims& d, float* ws) {
     return sp;
 }
 
-size_t selective_fwd_workspace_bytes(const SelectiveDims& d) {
-    const Spans sp = spans_of(d, nullptr);
+size_t selective_fwd_workspace_bytes(const SelectiveDims& d, Elt t) {
+    const Spans sp = selective_spans(d, t, nullptr);
     return (size_t)(d.b * (sp.count - 1) * d.D * (padded_states(d.N) + 1)) * 4;
 }
 
@@ -572,7 +566,7 @@ size_t selective_fwd_workspace_bytes(const SelectiveDims& d) {
 template <What W>
 cudaError_t run_fwd(const SelectiveArgs& a, void* y, float* out, float* ws, const SelectiveDims& d,
                     Elt t, cudaStream_t s) {
-    const Spans sp = spans_of(d, ws);
+    const Spans sp = selective_spans(d, t, ws);
     cudaError_t err = cudaSuccess;
     with_elt(t, [&](auto ty) {
         using T = typename decltype(ty)::type;

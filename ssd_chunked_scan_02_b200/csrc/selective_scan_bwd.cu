@@ -57,12 +57,15 @@ struct Bwd {
 };
 
 // ------------------------------------------------------------------ the reverse walk
-// ckpt (b, ceil(L / TS), D, NP): the state before token TS * j.
-template <typename T, typename Lay, bool Vec>
+// ckpt (b, ceil(L / TS), D, NP): the state before token TS * j.  blockIdx.y: the span
+// of the sequence.  Carry: only what a span's tokens send to the token before its
+// first, from nothing behind its last, and its sum of dt; the walk for the
+// gradients then finds the g that enters a span from those of the spans behind.
+template <typename T, typename Lay, bool Vec, bool Carry>
 __global__ void __launch_bounds__(kThreads, (Bwd<T, Lay>::BLOCKS))
 scan_bwd_kernel(const SelectiveArgs a, const SelectiveGrads gr, const float* __restrict__ ckpt,
                 float* __restrict__ part_bc, float* __restrict__ part_a,
-                float* __restrict__ part_d, const SelectiveDims d) {
+                float* __restrict__ part_d, const Spans sp, const SelectiveDims d) {
     using S = Bwd<T, Lay>;
     constexpr int SPL = Lay::SPL, LPC = Lay::LPC, NP = Lay::NP, CH = Lay::CH, TS = kTS;
     constexpr int TT = S::TT, VW = S::VW, PER = S::PER, IT = S::IT, VB = S::VB, NB = S::NB;
@@ -94,7 +97,9 @@ scan_bwd_kernel(const SelectiveArgs a, const SelectiveGrads gr, const float* __r
     const Place pl = place_of<CH>(blockIdx.x, d);
     const int tid = threadIdx.x, lane = tid % LPC, ch = tid / LPC, warp = tid / 32;
     const int64_t len = own_length(a.lens, pl.b, d.L), nck = (d.L + TS - 1) / TS;
-    const int L = (int)d.L, own = (int)len;
+    const int span = Carry ? blockIdx.y + 1 : blockIdx.y;
+    const int first = (int)(span * sp.tokens), own = (int)len;
+    const int L = span + 1 == sp.count ? (int)d.L : first + (int)sp.tokens;     // the span's end
     const T* x = static_cast<const T*>(a.x) + pl.b * a.xs.batch + pl.c0;
     const T* dt = static_cast<const T*>(a.dt) + pl.b * a.dts.batch + pl.c0;
     const T* z = a.z ? static_cast<const T*>(a.z) + pl.b * a.zs.batch + pl.c0 : nullptr;
@@ -123,7 +128,16 @@ scan_bwd_kernel(const SelectiveArgs a, const SelectiveGrads gr, const float* __r
             const int n = lane * SPL + i;
             const bool on = ch < pl.count && n < d.N;
             av[i] = on ? a.A[(pl.c0 + ch) * d.N + n] : 0.f;
-            gv[i] = on && gr.dfinal ? gr.dfinal[row * d.N + n] : 0.f;
+            gv[i] = on && !Carry && gr.dfinal ? gr.dfinal[row * d.N + n] : 0.f;
+        }
+        if (!Carry && ch < pl.count) {
+            for (int k = sp.count - 1; k > span; --k) {         // the spans behind this one
+                const int64_t at = (pl.b * (sp.count - 1) + k - 1) * d.D + pl.c0 + ch;
+                const float sum = sp.sum[at];
+                const float* G = sp.state + at * NP + lane * SPL;
+#pragma unroll
+                for (int i = 0; i < SPL; ++i) gv[i] = fmaf(ex2(sum * av[i]), gv[i], G[i]);
+            }
         }
 #pragma unroll
         for (int i = 0; i < SPL / 2; ++i) {
@@ -193,6 +207,7 @@ scan_bwd_kernel(const SelectiveArgs a, const SelectiveGrads gr, const float* __r
                 u[j] = v * to_f32(rx.v[j]);
                 if (j >= n) v = u[j] = gy[j] = 0.f;
                 dl[j] = v * kLog2E;
+                if (Carry) s_sum[j * kThreads + tid] += dl[j];
             }
 #pragma unroll
             for (int j = 0; j < VW; j += 4) {
@@ -234,192 +249,225 @@ scan_bwd_kernel(const SelectiveArgs a, const SelectiveGrads gr, const float* __r
         for (int i = 0; i < SPL / 4; ++i) hn[i] = raw_load<float, 4>(ck + j * d.D * NP + 4 * i);
     };
 
-    const int ntile = (L + TT - 1) / TT;
-    if (ntile > 0) {
+    const int tile0 = first / TT, ntile = (L + TT - 1) / TT;
+    if (ntile > tile0) {
         load((ntile - 1) * TT, (ntile - 1) & 1);
-        fetch(ntile * TT - TS);
+        if (!Carry) fetch(ntile * TT - TS);
         __syncthreads();                                        // s_B's zeros, s_bias
     }
-    for (int tile = ntile - 1; tile >= 0; --tile) {
+    for (int tile = ntile - 1; tile >= tile0; --tile) {
         const int t0 = tile * TT, w = tile & 1;
         stage(t0, w);
         __syncthreads();
-        if (tile > 0) load(t0 - TT, w ^ 1);
+        if (tile > tile0) load(t0 - TT, w ^ 1);
+        if constexpr (Carry) {
+#pragma unroll 1
+            for (int tt = TT - TS; tt >= 0; tt -= TS) {
+#pragma unroll
+                for (int k = TS - 1; k >= 0; --k) {
+                    const float dl = s_du[(tt + k) * CH + ch].x, gy = s_g[(tt + k) * CH + ch];
+                    const F2 dd = pack2(dl, dl), gg = pack2(gy, gy);
+                    const float* Ct = s_C + (tt + k) * NP + lane * SPL;
+#pragma unroll
+                    for (int i = 0; i < SPL / 2; ++i) {
+                        const float2 c2 = *reinterpret_cast<const float2*>(Ct + 2 * i);
+                        g[i] = mul2(fma2(gg, pack2(c2.x, c2.y), g[i]), decay2(dd, A[i]));
+                    }
+                }
+            }
+        } else {
 
 #pragma unroll 1
-        for (int tt = TT - TS; tt >= 0; tt -= TS) {
-            // a_t and h_t of TS tokens; h[0] is the state before them.  (Behind the
-            // last token dt = 0 keeps whatever state is loaded, and u, dyg, B and C
-            // are zero: nothing of it is used.)
-            F2 e[TS][SPL / 2], h[TS + 1][SPL / 2];
+            for (int tt = TT - TS; tt >= 0; tt -= TS) {
+                // a_t and h_t of TS tokens; h[0] is the state before them.  (Behind the
+                // last token dt = 0 keeps whatever state is loaded, and u, dyg, B and C
+                // are zero: nothing of it is used.)
+                F2 e[TS][SPL / 2], h[TS + 1][SPL / 2];
 #pragma unroll
-            for (int i = 0; i < SPL / 2; ++i) h[0][i] = pack2(hn[i / 2].v[i % 2 * 2], hn[i / 2].v[i % 2 * 2 + 1]);
-            fetch(t0 + tt - TS);
+                for (int i = 0; i < SPL / 2; ++i) h[0][i] = pack2(hn[i / 2].v[i % 2 * 2], hn[i / 2].v[i % 2 * 2 + 1]);
+                fetch(t0 + tt - TS);
 #pragma unroll
-            for (int k = 0; k < TS; ++k) {
-                const float2 q = s_du[(tt + k) * CH + ch];
-                const F2 dd = pack2(q.x, q.x), uu = pack2(q.y, q.y);
-                const float* Bt = s_B + (tt + k) * NP + lane * SPL;
+                for (int k = 0; k < TS; ++k) {
+                    const float2 q = s_du[(tt + k) * CH + ch];
+                    const F2 dd = pack2(q.x, q.x), uu = pack2(q.y, q.y);
+                    const float* Bt = s_B + (tt + k) * NP + lane * SPL;
 #pragma unroll
-                for (int i = 0; i < SPL / 2; i += 2) {
-                    const float4 bv = *reinterpret_cast<const float4*>(Bt + 2 * i);
-                    e[k][i] = decay2(dd, A[i]);
-                    e[k][i + 1] = decay2(dd, A[i + 1]);
-                    h[k + 1][i] = fma2(e[k][i], h[k][i], mul2(uu, pack2(bv.x, bv.y)));
-                    h[k + 1][i + 1] = fma2(e[k][i + 1], h[k][i + 1], mul2(uu, pack2(bv.z, bv.w)));
-                }
-            }
-            F2 at[SPL / 2];
-#pragma unroll
-            for (int i = 0; i < SPL / 2; ++i) at[i] = 0;
-            float py[NG], pu[NG], pq[NG], pB[FG * SPL], pC[FG * SPL];
-#pragma unroll
-            for (int k = TS - 1; k >= 0; --k) {
-                const float2 q = s_du[(tt + k) * CH + ch];
-                const float gy = s_g[(tt + k) * CH + ch];
-                const F2 dd = pack2(q.x, q.x), uu = pack2(q.y, q.y), gg = pack2(gy, gy);
-                const float* Bt = s_B + (tt + k) * NP + lane * SPL;
-                const float* Ct = s_C + (tt + k) * NP + lane * SPL;
-                F2 sy = 0, su = 0, sq = 0;
-#pragma unroll
-                for (int i4 = 0; i4 < SPL; i4 += 4) {
-                    const float4 b4 = *reinterpret_cast<const float4*>(Bt + i4);
-                    const float4 c4 = *reinterpret_cast<const float4*>(Ct + i4);
-                    const F2 Bv[2] = {pack2(b4.x, b4.y), pack2(b4.z, b4.w)};
-                    const F2 Cv[2] = {pack2(c4.x, c4.y), pack2(c4.z, c4.w)};
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const int i = i4 / 2 + j;
-                        g[i] = fma2(gg, Cv[j], g[i]);
-                        sy = i == 0 ? mul2(Cv[j], h[k + 1][i]) : fma2(Cv[j], h[k + 1][i], sy);
-                        su = i == 0 ? mul2(Bv[j], g[i]) : fma2(Bv[j], g[i], su);
-                        const float2 dc = unpack2(mul2(gg, h[k + 1][i])), db = unpack2(mul2(uu, g[i]));
-                        pC[k % FG * SPL + 2 * i] = dc.x;
-                        pC[k % FG * SPL + 2 * i + 1] = dc.y;
-                        pB[k % FG * SPL + 2 * i] = db.x;
-                        pB[k % FG * SPL + 2 * i + 1] = db.y;
-                        g[i] = mul2(g[i], e[k][i]);
-                        const F2 qv = mul2(g[i], h[k][i]);
-                        sq = i == 0 ? mul2(A[i], qv) : fma2(A[i], qv, sq);
-                        at[i] = fma2(dd, qv, at[i]);
+                    for (int i = 0; i < SPL / 2; i += 2) {
+                        const float4 bv = *reinterpret_cast<const float4*>(Bt + 2 * i);
+                        e[k][i] = decay2(dd, A[i]);
+                        e[k][i + 1] = decay2(dd, A[i + 1]);
+                        h[k + 1][i] = fma2(e[k][i], h[k][i], mul2(uu, pack2(bv.x, bv.y)));
+                        h[k + 1][i + 1] = fma2(e[k][i + 1], h[k][i + 1], mul2(uu, pack2(bv.z, bv.w)));
                     }
                 }
-                const float2 fy = unpack2(sy), fu = unpack2(su), fq = unpack2(sq);
-                py[k % NG] = fy.x + fy.y;
-                pu[k % NG] = fu.x + fu.y;
-                pq[k % NG] = fq.x + fq.y;
-                if (k % FG == 0) {
-                    // over a warp's channels: the lanes of one place in the channel lie LPC apart
-                    const int place = tid % 32 / LPC;
-                    constexpr int ALL = FG * SPL, NV = ALL >= CPW ? ALL / CPW : 1;
-                    constexpr int SH = ALL >= CPW ? 1 : CPW / ALL;
-                    fold<ALL, CPW, LPC>(pB, place);
-                    fold<ALL, CPW, LPC>(pC, place);
-                    if (place % SH == 0) {
+                F2 at[SPL / 2];
 #pragma unroll
-                        for (int i = 0; i < NV; ++i) {
-                            const int v = place / SH * NV + i, t = tt + k + v / SPL, n = lane * SPL + v % SPL;
-                            float* q = s_red + (warp * TT + t) * 2 * NP + n;
-                            q[(t & 1) * NP] = pB[i];            // odd tokens: dC first, so that
-                            q[(t & 1 ^ 1) * NP] = pC[i];        // two tokens meet no bank twice
+                for (int i = 0; i < SPL / 2; ++i) at[i] = 0;
+                float py[NG], pu[NG], pq[NG], pB[FG * SPL], pC[FG * SPL];
+#pragma unroll
+                for (int k = TS - 1; k >= 0; --k) {
+                    const float2 q = s_du[(tt + k) * CH + ch];
+                    const float gy = s_g[(tt + k) * CH + ch];
+                    const F2 dd = pack2(q.x, q.x), uu = pack2(q.y, q.y), gg = pack2(gy, gy);
+                    const float* Bt = s_B + (tt + k) * NP + lane * SPL;
+                    const float* Ct = s_C + (tt + k) * NP + lane * SPL;
+                    F2 sy = 0, su = 0, sq = 0;
+#pragma unroll
+                    for (int i4 = 0; i4 < SPL; i4 += 4) {
+                        const float4 b4 = *reinterpret_cast<const float4*>(Bt + i4);
+                        const float4 c4 = *reinterpret_cast<const float4*>(Ct + i4);
+                        const F2 Bv[2] = {pack2(b4.x, b4.y), pack2(b4.z, b4.w)};
+                        const F2 Cv[2] = {pack2(c4.x, c4.y), pack2(c4.z, c4.w)};
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            const int i = i4 / 2 + j;
+                            g[i] = fma2(gg, Cv[j], g[i]);
+                            sy = i == 0 ? mul2(Cv[j], h[k + 1][i]) : fma2(Cv[j], h[k + 1][i], sy);
+                            su = i == 0 ? mul2(Bv[j], g[i]) : fma2(Bv[j], g[i], su);
+                            const float2 dc = unpack2(mul2(gg, h[k + 1][i])), db = unpack2(mul2(uu, g[i]));
+                            pC[k % FG * SPL + 2 * i] = dc.x;
+                            pC[k % FG * SPL + 2 * i + 1] = dc.y;
+                            pB[k % FG * SPL + 2 * i] = db.x;
+                            pB[k % FG * SPL + 2 * i + 1] = db.y;
+                            g[i] = mul2(g[i], e[k][i]);
+                            const F2 qv = mul2(g[i], h[k][i]);
+                            sq = i == 0 ? mul2(A[i], qv) : fma2(A[i], qv, sq);
+                            at[i] = fma2(dd, qv, at[i]);
+                        }
+                    }
+                    const float2 fy = unpack2(sy), fu = unpack2(su), fq = unpack2(sq);
+                    py[k % NG] = fy.x + fy.y;
+                    pu[k % NG] = fu.x + fu.y;
+                    pq[k % NG] = fq.x + fq.y;
+                    if (k % FG == 0) {
+                        // over a warp's channels: the lanes of one place in the channel lie LPC apart
+                        const int place = tid % 32 / LPC;
+                        constexpr int ALL = FG * SPL, NV = ALL >= CPW ? ALL / CPW : 1;
+                        constexpr int SH = ALL >= CPW ? 1 : CPW / ALL;
+                        fold<ALL, CPW, LPC>(pB, place);
+                        fold<ALL, CPW, LPC>(pC, place);
+                        if (place % SH == 0) {
+#pragma unroll
+                            for (int i = 0; i < NV; ++i) {
+                                const int v = place / SH * NV + i, t = tt + k + v / SPL, n = lane * SPL + v % SPL;
+                                float* q = s_red + (warp * TT + t) * 2 * NP + n;
+                                q[(t & 1) * NP] = pB[i];            // odd tokens: dC first, so that
+                                q[(t & 1 ^ 1) * NP] = pC[i];        // two tokens meet no bank twice
+                            }
+                        }
+                    }
+                    if (k % NG == 0) {
+                        // over a channel's lanes
+                        fold<NG, LPC>(py, lane);
+                        fold<NG, LPC>(pu, lane);
+                        fold<NG, LPC>(pq, lane);
+                        constexpr int NT = NG >= LPC ? NG / LPC : 1, SH = NG >= LPC ? 1 : LPC / NG;
+                        if (lane % SH == 0) {
+#pragma unroll
+                            for (int i = 0; i < NT; ++i) {
+                                const int o = (tt + k + lane / SH * NT + i) * PY + ch;
+                                s_y[o] = py[i];
+                                s_dtg[o] = pu[i];
+                                s_q[o] = pq[i];
+                            }
                         }
                     }
                 }
-                if (k % NG == 0) {
-                    // over a channel's lanes
-                    fold<NG, LPC>(py, lane);
-                    fold<NG, LPC>(pu, lane);
-                    fold<NG, LPC>(pq, lane);
-                    constexpr int NT = NG >= LPC ? NG / LPC : 1, SH = NG >= LPC ? 1 : LPC / NG;
-                    if (lane % SH == 0) {
 #pragma unroll
-                        for (int i = 0; i < NT; ++i) {
-                            const int o = (tt + k + lane / SH * NT + i) * PY + ch;
-                            s_y[o] = py[i];
-                            s_dtg[o] = pu[i];
-                            s_q[o] = pq[i];
-                        }
-                    }
-                }
+                for (int i = 0; i < SPL / 2; ++i) dA[i] = add2(dA[i], at[i]);
             }
-#pragma unroll
-            for (int i = 0; i < SPL / 2; ++i) dA[i] = add2(dA[i], at[i]);
-        }
-        __syncthreads();
+            __syncthreads();
 
-        for (int i = tid * 4; i < TT * 2 * NP; i += 4 * kThreads) {
-            const int t = t0 + i / (2 * NP), col = i % (2 * NP);
-            if (t < L) {
-                float4 v = *reinterpret_cast<const float4*>(s_red + i);
+            for (int i = tid * 4; i < TT * 2 * NP; i += 4 * kThreads) {
+                const int t = t0 + i / (2 * NP), col = i % (2 * NP);
+                if (t < L) {
+                    float4 v = *reinterpret_cast<const float4*>(s_red + i);
 #pragma unroll
-                for (int k = 1; k < kWarps; ++k) {
-                    const float4 o = *reinterpret_cast<const float4*>(s_red + k * TT * 2 * NP + i);
-                    v.x += o.x; v.y += o.y; v.z += o.z; v.w += o.w;
-                }
-                *reinterpret_cast<float4*>(part_bc + ((cb * d.b + pl.b) * d.L + t) * 2 * NP +
-                                           (col ^ (t & 1) * NP)) = v;
-            }
-        }
-#pragma unroll
-        for (int k = 0; k < IT; ++k) {
-            const int i = k * kThreads + tid, tl = i / PER, t = t0 + tl, c = i % PER * VW;
-            if (tl >= TT || t >= L) continue;
-            const int n = t < own ? pl.count - c : 0, o = (w * IT + k) * kThreads + tid;
-            const RV rx = r_x[o], rdt = r_dt[o], rdy = r_dy[o];
-            RV rz;
-            if (z) rz = r_z[o];
-            float ox[VW], ot[VW], oz[VW];
-#pragma unroll
-            for (int j4 = 0; j4 < VW; j4 += 4) {
-                const float4 du4 = *reinterpret_cast<const float4*>(s_dtg + tl * PY + c + j4);
-                const float4 q4 = *reinterpret_cast<const float4*>(s_q + tl * PY + c + j4);
-                const float4 y4 = *reinterpret_cast<const float4*>(s_y + tl * PY + c + j4);
-                const float4 g4 = *reinterpret_cast<const float4*>(s_g + tl * CH + c + j4);
-                const float4 d0 = reinterpret_cast<const float4*>(s_du + tl * CH + c + j4)[0];
-                const float4 d1 = reinterpret_cast<const float4*>(s_du + tl * CH + c + j4)[1];
-                const float du[4] = {du4.x, du4.y, du4.z, du4.w}, q[4] = {q4.x, q4.y, q4.z, q4.w};
-                const float gy[4] = {g4.x, g4.y, g4.z, g4.w}, yv[4] = {y4.x, y4.y, y4.z, y4.w};
-                const float dl[4] = {d0.x, d0.z, d1.x, d1.z};
-#pragma unroll
-                for (int jj = 0; jj < 4; ++jj) {
-                    const int j = j4 + jj;
-                    const float xv = to_f32(rx.v[j]), Dv = s_skip[c + j];
-                    ox[j] = fmaf(dl[jj] * kLn2, du[jj], Dv * gy[jj]);
-                    ot[j] = fmaf(du[jj], xv, q[jj]);
-                    if (a.softplus) ot[j] *= sigmoid_fast(to_f32(rdt.v[j]) + s_bias[c + j]);
-                    oz[j] = 0.f;
-                    if (z) {
-                        const float zv = to_f32(rz.v[j]), sg = sigmoid_fast(zv);
-                        oz[j] = to_f32(rdy.v[j]) * fmaf(Dv, xv, yv[jj]) * sg * fmaf(zv, 1.f - sg, 1.f);
+                    for (int k = 1; k < kWarps; ++k) {
+                        const float4 o = *reinterpret_cast<const float4*>(s_red + k * TT * 2 * NP + i);
+                        v.x += o.x; v.y += o.y; v.z += o.z; v.w += o.w;
                     }
-                    float gx = gy[jj] * xv;
-                    if (j >= n) ox[j] = ot[j] = oz[j] = gx = 0.f;
-                    s_sum[j * kThreads + tid] += gx;
-                    s_sum[(VW + j) * kThreads + tid] += ot[j];
+                    *reinterpret_cast<float4*>(part_bc + ((cb * d.b + pl.b) * d.L + t) * 2 * NP +
+                                               (col ^ (t & 1) * NP)) = v;
                 }
             }
-            const int left = pl.count - c;
-            const int64_t at = (int64_t)t * Dt + c;
-            store_channels<T, VW>(dx + at, raw_from_f32<T, VW>(ox), left, Vec);
-            store_channels<T, VW>(ddt + at, raw_from_f32<T, VW>(ot), left, Vec);
-            if (z) store_channels<T, VW>(dz + at, raw_from_f32<T, VW>(oz), left, Vec);
+#pragma unroll
+            for (int k = 0; k < IT; ++k) {
+                const int i = k * kThreads + tid, tl = i / PER, t = t0 + tl, c = i % PER * VW;
+                if (tl >= TT || t >= L) continue;
+                const int n = t < own ? pl.count - c : 0, o = (w * IT + k) * kThreads + tid;
+                const RV rx = r_x[o], rdt = r_dt[o], rdy = r_dy[o];
+                RV rz;
+                if (z) rz = r_z[o];
+                float ox[VW], ot[VW], oz[VW];
+#pragma unroll
+                for (int j4 = 0; j4 < VW; j4 += 4) {
+                    const float4 du4 = *reinterpret_cast<const float4*>(s_dtg + tl * PY + c + j4);
+                    const float4 q4 = *reinterpret_cast<const float4*>(s_q + tl * PY + c + j4);
+                    const float4 y4 = *reinterpret_cast<const float4*>(s_y + tl * PY + c + j4);
+                    const float4 g4 = *reinterpret_cast<const float4*>(s_g + tl * CH + c + j4);
+                    const float4 d0 = reinterpret_cast<const float4*>(s_du + tl * CH + c + j4)[0];
+                    const float4 d1 = reinterpret_cast<const float4*>(s_du + tl * CH + c + j4)[1];
+                    const float du[4] = {du4.x, du4.y, du4.z, du4.w}, q[4] = {q4.x, q4.y, q4.z, q4.w};
+                    const float gy[4] = {g4.x, g4.y, g4.z, g4.w}, yv[4] = {y4.x, y4.y, y4.z, y4.w};
+                    const float dl[4] = {d0.x, d0.z, d1.x, d1.z};
+#pragma unroll
+                    for (int jj = 0; jj < 4; ++jj) {
+                        const int j = j4 + jj;
+                        const float xv = to_f32(rx.v[j]), Dv = s_skip[c + j];
+                        ox[j] = fmaf(dl[jj] * kLn2, du[jj], Dv * gy[jj]);
+                        ot[j] = fmaf(du[jj], xv, q[jj]);
+                        if (a.softplus) ot[j] *= sigmoid_fast(to_f32(rdt.v[j]) + s_bias[c + j]);
+                        oz[j] = 0.f;
+                        if (z) {
+                            const float zv = to_f32(rz.v[j]), sg = sigmoid_fast(zv);
+                            oz[j] = to_f32(rdy.v[j]) * fmaf(Dv, xv, yv[jj]) * sg * fmaf(zv, 1.f - sg, 1.f);
+                        }
+                        float gx = gy[jj] * xv;
+                        if (j >= n) ox[j] = ot[j] = oz[j] = gx = 0.f;
+                        s_sum[j * kThreads + tid] += gx;
+                        s_sum[(VW + j) * kThreads + tid] += ot[j];
+                    }
+                }
+                const int left = pl.count - c;
+                const int64_t at = (int64_t)t * Dt + c;
+                store_channels<T, VW>(dx + at, raw_from_f32<T, VW>(ox), left, Vec);
+                store_channels<T, VW>(ddt + at, raw_from_f32<T, VW>(ot), left, Vec);
+                if (z) store_channels<T, VW>(dz + at, raw_from_f32<T, VW>(oz), left, Vec);
+            }
         }
         __syncthreads();
     }
 
-    // sums over the tokens: dA by lane; dD and ddt_bias over the threads of a channel
+    if constexpr (Carry) {
+        const int64_t at = (pl.b * (sp.count - 1) + span - 1) * d.D + pl.c0;
+        if (ch < pl.count) {
+#pragma unroll
+            for (int i = 0; i < SPL / 2; ++i) {
+                const float2 gv = unpack2(g[i]);
+                *reinterpret_cast<float2*>(sp.state + (at + ch) * NP + lane * SPL + 2 * i) = gv;
+            }
+        }
+        __syncthreads();
+        for (int c = tid; c < pl.count; c += kThreads) {
+            float v = 0.f;
+            for (int q = c / VW; q < kThreads; q += PER) v += s_sum[c % VW * kThreads + q];
+            sp.sum[at + c] = v;
+        }
+        return;
+    }
+    // sums over the span's tokens: dA by lane; dD and ddt_bias over the threads of a channel
+    const int64_t part = span * d.b + pl.b;
     if (ch < pl.count) {
 #pragma unroll
         for (int i = 0; i < SPL / 2; ++i) {
             const float2 da = unpack2(dA[i]), gv = unpack2(g[i]);
-            const int n = lane * SPL + 2 * i;
-            if (n < d.N) {
-                part_a[row * d.N + n] = da.x * kLn2;
-                if (gr.dinit) gr.dinit[row * d.N + n] = gv.x;
-            }
-            if (n + 1 < d.N) {
-                part_a[row * d.N + n + 1] = da.y * kLn2;
-                if (gr.dinit) gr.dinit[row * d.N + n + 1] = gv.y;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int n = lane * SPL + 2 * i + j;
+                if (n >= d.N) continue;
+                part_a[(part * d.D + pl.c0 + ch) * d.N + n] = (j ? da.y : da.x) * kLn2;
+                if (gr.dinit && span == 0) gr.dinit[row * d.N + n] = j ? gv.y : gv.x;
             }
         }
     }
@@ -429,7 +477,7 @@ scan_bwd_kernel(const SelectiveArgs a, const SelectiveGrads gr, const float* __r
         if (c >= pl.count) continue;
         float v = 0.f;
         for (int q = c / VW; q < kThreads; q += PER) v += s_sum[(which * VW + c % VW) * kThreads + q];
-        part_d[((int64_t)which * d.b + pl.b) * d.D + pl.c0 + c] = v;
+        part_d[((int64_t)which * sp.count * d.b + part) * d.D + pl.c0 + c] = v;
     }
 }
 
@@ -459,7 +507,7 @@ reduce_bc_kernel(const float* __restrict__ part, T* __restrict__ dB, T* __restri
     }
 }
 
-// out[i] = sum over the batch of part[b][i]
+// out[i] = sum over the rows (spans and batch) of part[b][i]
 __global__ void __launch_bounds__(256)
 reduce_batch_kernel(const float* __restrict__ part, float* __restrict__ out, int64_t b, int64_t n) {
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
@@ -470,9 +518,9 @@ reduce_batch_kernel(const float* __restrict__ part, float* __restrict__ out, int
 }
 
 struct Work {
-    size_t ckpt, bc, a, d, fwd, total;       // floats; fwd: the checkpoint walk's own
+    size_t ckpt, bc, a, d, fwd, total;       // floats; fwd: the spans, of either walk
 };
-Work work_of(const SelectiveDims& d) {
+Work work_of(const SelectiveDims& d, Elt t) {
     Work w{};
     with_layout(d.N, [&](auto lay) {
         using Lay = decltype(lay);
@@ -480,20 +528,22 @@ Work work_of(const SelectiveDims& d) {
         w.ckpt = 0;
         w.bc = w.ckpt + (size_t)(d.b * ((d.L + TS - 1) / TS) * d.D * Lay::NP);
         w.a = w.bc + (size_t)(channel_blocks<Lay::CH>(d) * d.b * d.L * 2 * Lay::NP);
-        w.d = w.a + (size_t)(d.b * d.D * d.N);
-        w.fwd = (w.d + (size_t)(2 * d.b * d.D) + 3) / 4 * 4;
-        w.total = w.fwd + selective_fwd_workspace_bytes(d) / 4;
+        const int64_t rows = d.b * selective_spans(d, t, nullptr).count;
+        w.d = w.a + (size_t)(rows * d.D * d.N);
+        w.fwd = (w.d + (size_t)(2 * rows * d.D) + 3) / 4 * 4;
+        w.total = w.fwd + selective_fwd_workspace_bytes(d, t) / 4;
     });
     return w;
 }
 
 }  // namespace
 
-size_t selective_bwd_workspace_bytes(const SelectiveDims& d) { return work_of(d).total * 4; }
+size_t selective_bwd_workspace_bytes(const SelectiveDims& d, Elt t) { return work_of(d, t).total * 4; }
 
 cudaError_t launch_selective_bwd(const SelectiveArgs& a, const SelectiveGrads& g, float* ws,
                                  const SelectiveDims& d, Elt t, cudaStream_t s) {
-    const Work w = work_of(d);
+    const Work w = work_of(d, t);
+    const Spans sp = selective_spans(d, t, ws + w.fwd);
     cudaError_t err = cudaSuccess;
     if (d.b > 0 && d.L > 0) err = launch_selective_checkpoints(a, ws + w.ckpt, ws + w.fwd, d, t, s);
     if (err != cudaSuccess) return err;
@@ -504,17 +554,23 @@ cudaError_t launch_selective_bwd(const SelectiveArgs& a, const SelectiveGrads& g
             using S = Bwd<T, Lay>;
             const int64_t nb = channel_blocks<Lay::CH>(d), blocks = d.b * nb;
             if (blocks == 0) return;
-            auto go = [&](auto kernel) {
-                err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
+            auto go = [&](auto kernel, unsigned spans) {
                 if (err == cudaSuccess)
-                    kernel<<<(unsigned)blocks, kThreads, S::SMEM, s>>>(
-                        a, g, ws + w.ckpt, ws + w.bc, ws + w.a, ws + w.d, d);
+                    err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               S::SMEM);
+                if (err == cudaSuccess)
+                    kernel<<<dim3((unsigned)blocks, spans), kThreads, S::SMEM, s>>>(
+                        a, g, ws + w.ckpt, ws + w.bc, ws + w.a, ws + w.d, sp, d);
+            };
+            auto both = [&](auto carry, auto whole) {
+                if (sp.count > 1) go(carry, (unsigned)sp.count - 1);
+                go(whole, (unsigned)sp.count);
             };
             if (selective_vec<T>(a, d, S::VW) && d.N % S::VB == 0 && rows_fit<T>(a.B, a.Bs, S::VB) &&
                 rows_fit<T>(a.C, a.Cs, S::VB))
-                go(scan_bwd_kernel<T, Lay, true>);
+                both(scan_bwd_kernel<T, Lay, true, true>, scan_bwd_kernel<T, Lay, true, false>);
             else
-                go(scan_bwd_kernel<T, Lay, false>);
+                both(scan_bwd_kernel<T, Lay, false, true>, scan_bwd_kernel<T, Lay, false, false>);
             if (err == cudaSuccess && d.L > 0) {
                 const int64_t total = d.b * d.L * d.G * 2 * Lay::NP / 4, nblk = (total + 255) / 256;
                 reduce_bc_kernel<T><<<(unsigned)(nblk < 148 * 16 ? nblk : 148 * 16), 256, 0, s>>>(
@@ -524,13 +580,14 @@ cudaError_t launch_selective_bwd(const SelectiveArgs& a, const SelectiveGrads& g
         });
     });
     if (err != cudaSuccess) return err;
-    auto over_batch = [&](size_t from, float* out, int64_t n) {
+    const int64_t rows = d.b * sp.count;
+    auto add_rows = [&](size_t from, float* out, int64_t n) {
         if (out)
-            reduce_batch_kernel<<<(unsigned)((n + 255) / 256), 256, 0, s>>>(ws + from, out, d.b, n);
+            reduce_batch_kernel<<<(unsigned)((n + 255) / 256), 256, 0, s>>>(ws + from, out, rows, n);
     };
-    over_batch(w.a, g.dA, d.D * d.N);
-    over_batch(w.d, g.dD, d.D);
-    over_batch(w.d + (size_t)(d.b * d.D), g.ddt_bias, d.D);
+    add_rows(w.a, g.dA, d.D * d.N);
+    add_rows(w.d, g.dD, d.D);
+    add_rows(w.d + (size_t)(rows * d.D), g.ddt_bias, d.D);
     return cudaGetLastError();
 }
 

@@ -304,3 +304,42 @@ def test_streams_graphs_and_repeats(lib):
     want = call()
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(kept, want)) and not torch.equal(one[0], kept[0])
+
+
+SPANS = [  # long and narrow: the sequence is cut into spans, of both walks
+    Case(1, 700, 40, 16, lens=[650]),
+    Case(2, 333, 24, 16, G=2, dt="f32", lens=[333, 64]),
+    Case(1, 520, 33, 24, view=3, init=False),
+    Case(1, 300, 12, 100, dt="f32"),
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("c", SPANS, ids=repr)
+def test_spans(lib, c):
+    """Few channels and many tokens.  The sums of dt over a span add up to L
+    roundings of their size, and a span's decay that many of its exponent: the
+    running bounds' 10 |dt A| a token cover it.  (Lengths that end inside a span,
+    at its border, and before the last one.)"""
+    d, m = make(c, 31)
+    dims = ssd.ssd_selective_dims_t(c.b, c.L, c.ch, c.N, c.G)
+    assert ssd.ssd_selective_scan_fwd_workspace_size(dims, DT[c.dt]) > 0
+    y, f = ssd.ssd_selective_scan_fwd(**d, init_states=m["init"], seq_lens=m["lens_t"],
+                                      return_final_states=True)
+    dy = torch.randn(c.b, c.L, c.ch, generator=m["gen"]).to(DT[c.dt]).cuda()
+    df = torch.randn(c.b, c.ch, c.N, generator=m["gen"]).cuda() if c.init else None
+    g = ssd.ssd_selective_scan_bwd(**d, dy=dy, init_states=m["init"], dfinal_states=df,
+                                   seq_lens=m["lens_t"], want_dinit=c.init)
+    ra = ref_args(d, m)
+    leaf = {k: v.requires_grad_() for k, v in ra.items() if torch.is_tensor(v)}
+    ry, rf = R.scan(**ra)
+    loss = (ry * R.f64(dy)).sum() + ((rf * R.f64(df)).sum() if df is not None else 0)
+    ref = dict(zip(leaf, torch.autograd.grad(loss, list(leaf.values()), allow_unused=True)))
+    plain = {k: (v.detach() if torch.is_tensor(v) else v) for k, v in ra.items()}
+    bound = R.scan_bounds(**plain, dy=R.f64(dy), dfinal=R.f64(df))
+    R.within("y", y, ry, bound["y"])
+    R.within("final", f, rf, bound["final"])
+    for k, of in NAMES.items():
+        if of in leaf:
+            want = ref[of] if ref[of] is not None else torch.zeros_like(leaf[of])
+            R.within(k, g[k], want, bound[k])
