@@ -176,11 +176,4 @@ constexpr int load_width() {
     return CH < (int)(16 / sizeof(T)) ? CH : (int)(16 / sizeof(T));
 }
 
-// The same where a thread has `mine` of a tile, so that every thread is busy: at
-// least 4.
-template <typename T, int CH>
-constexpr int spread_width(int mine) {
-    return mine >= load_width<T, CH>() ? load_width<T, CH>() : mine < 4 ? 4 : mine;
-}
-
 }  // namespace ssd

@@ -33,23 +33,19 @@ constexpr int kWalkers = 128;      // threads of the walking warps
 
 enum class What { SpanState, Output, Checkpoints };
 
-// Split: carriers and walkers are different warps.  Otherwise every warp does both in
-// turn, on shorter tiles and half the threads a block, so that an SM holds five
-// blocks instead of three: more channels at once, each more slowly.
-template <typename T, typename Lay, bool Split>
+template <typename T, typename Lay>
 struct Fwd {
-    static constexpr int TT = Split || Lay::TT < 16 ? Lay::TT : 16, CH = Lay::CH, NP = Lay::NP;
+    static constexpr int TT = Lay::TT, CH = Lay::CH, NP = Lay::NP;
     static constexpr int PY = CH + 8;                               // s_y's row: no bank twice
     static constexpr int KC = 128;                                  // threads of the carriers
-    static constexpr int THREADS = Split ? kWalkers + KC : kWalkers;
-    static constexpr int BUF = Split ? 2 : 1, RING = Split ? 4 : 2; // tiles ready, and as they come
-    static constexpr int VW = Split ? load_width<T, CH>() : spread_width<T, CH>(TT * CH / KC);
-    static constexpr int NI = (TT * CH / VW + KC - 1) / KC;         // loads a thread and tile
+    static constexpr int THREADS = kWalkers + KC;
+    static constexpr int VW = load_width<T, CH>();
+    static constexpr int NI = (TT * CH / VW + KC - 1) / KC;               // loads a thread and tile
     static constexpr int VB = 16 / sizeof(T);
     static constexpr int NB = (TT * NP * 2 / VB + KC - 1) / KC;
     static constexpr int RAW = KC * (3 * NI * VW + NB * VB) * (int)sizeof(T);   // a tile as it comes
-    static constexpr int SMEM = RING * RAW + BUF * (TT * CH * 8 + TT * PY * 4 + TT * NP * 8) + 2 * CH * 4;
-    static constexpr int BLOCKS = !Split && Lay::SPL == 4 ? 5 : SMEM <= 75 * 1024 ? 3 : 2;   // of an SM
+    static constexpr int SMEM = 4 * RAW + 2 * (TT * CH * 8 + TT * PY * 4 + TT * NP * 8) + 2 * CH * 4;
+    static constexpr int BLOCKS = SMEM <= 75 * 1024 ? 3 : 2;   // of an SM
 };
 
 // What: the state a span reaches from zero; y and the final states; or the
@@ -58,15 +54,14 @@ struct Fwd {
 // branches (rows and channels that do not exist read ones that do, and are
 // replaced by zeros when the tile is staged), because the join behind a branch
 // would wait for them.
-template <typename T, typename Lay, What W, bool Vec, bool Split>
-__global__ void __launch_bounds__((Fwd<T, Lay, Split>::THREADS), (Fwd<T, Lay, Split>::BLOCKS))
+template <typename T, typename Lay, What W, bool Vec>
+__global__ void __launch_bounds__((Fwd<T, Lay>::THREADS), (Fwd<T, Lay>::BLOCKS))
 scan_fwd_kernel(const SelectiveArgs a, T* __restrict__ y, float* __restrict__ final_states,
                 const Spans sp, const SelectiveDims d) {
-    using F = Fwd<T, Lay, Split>;
+    using F = Fwd<T, Lay>;
     constexpr bool Output = W == What::Output, Sum = W == What::SpanState;
-    constexpr int SPL = Lay::SPL, LPC = Lay::LPC, NP = Lay::NP, CH = Lay::CH, TT = F::TT;
+    constexpr int SPL = Lay::SPL, LPC = Lay::LPC, NP = Lay::NP, CH = Lay::CH, TT = Lay::TT;
     constexpr int VW = F::VW, NI = F::NI, VB = F::VB, NB = F::NB, PY = F::PY, KC = F::KC;
-    constexpr int BUF = F::BUF, RING = F::RING;
     constexpr int TG = LPC < 8 ? LPC : 8;                           // tokens summed at once
     // s_du's columns are permuted by the number of the load that brings them, so
     // that neither the eight lanes that store side by side nor those that read
@@ -76,20 +71,20 @@ scan_fwd_kernel(const SelectiveArgs a, T* __restrict__ y, float* __restrict__ fi
     extern __shared__ __align__(16) unsigned char smem[];
     using RV = Raw<T, VW>;
     using RB = Raw<T, VB>;
-    // RING tiles as they come: every carrier copies and reads its own elements
-    RB* r_bc = reinterpret_cast<RB*>(smem);                         // [RING][NB][KC]
-    RV* r_x = reinterpret_cast<RV*>(r_bc + RING * NB * KC);         // [RING][NI][KC] each
-    RV* r_dt = r_x + RING * NI * KC;
-    RV* r_z = r_dt + RING * NI * KC;
-    float2* s_du = reinterpret_cast<float2*>(r_z + RING * NI * KC); // [BUF][TT][CH]: dt log2(e), u
-    float* s_B = reinterpret_cast<float*>(s_du + BUF * TT * CH);    // [BUF][TT][NP]
-    float* s_C = s_B + BUF * TT * NP;
-    float* s_y = s_C + BUF * TT * NP;                               // [BUF][TT][PY]
-    float* s_bias = s_y + BUF * TT * PY;                            // [CH] each
+    // four tiles as they come: every carrier copies and reads its own elements
+    RB* r_bc = reinterpret_cast<RB*>(smem);                         // [4][NB][KC]
+    RV* r_x = reinterpret_cast<RV*>(r_bc + 4 * NB * KC);            // [4][NI][KC] each
+    RV* r_dt = r_x + 4 * NI * KC;
+    RV* r_z = r_dt + 4 * NI * KC;
+    float2* s_du = reinterpret_cast<float2*>(r_z + 4 * NI * KC);    // [2][TT][CH]: dt, u
+    float* s_B = reinterpret_cast<float*>(s_du + 2 * TT * CH);      // [2][TT][NP]
+    float* s_C = s_B + 2 * TT * NP;
+    float* s_y = s_C + 2 * TT * NP;                                 // [2][TT][PY]
+    float* s_bias = s_y + 2 * TT * PY;                              // [CH] each
     float* s_skip = s_bias + CH;
 
     const Place pl = place_of<CH>(blockIdx.x, d);
-    const bool walker = threadIdx.x < kWalkers, carrier = !Split || !walker;
+    const bool walker = threadIdx.x < kWalkers;
     const int tid = walker ? threadIdx.x : threadIdx.x - kWalkers;
     const int64_t own = own_length(a.lens, pl.b, d.L);
     const int span = blockIdx.y;
@@ -104,238 +99,93 @@ scan_fwd_kernel(const SelectiveArgs a, T* __restrict__ y, float* __restrict__ fi
     const T* Cp = static_cast<const T*>(a.C) + pl.b * a.Cs.batch + pl.g * d.N;
     if (Output) y += pl.b * d.L * d.D + pl.c0;
 
-    for (int i = threadIdx.x; i < 2 * BUF * TT * NP; i += F::THREADS) s_B[i] = 0.f;   // states beyond N
+    for (int i = threadIdx.x; i < 4 * TT * NP; i += F::THREADS) s_B[i] = 0.f;   // states beyond N
     for (int c = threadIdx.x; c < CH; c += F::THREADS) {
         s_bias[c] = a.dt_bias && c < pl.count ? a.dt_bias[pl.c0 + c] : 0.f;
         s_skip[c] = Output && a.D && c < pl.count ? a.D[pl.c0 + c] : 0.f;
     }
     __syncthreads();
 
-    const int lane = tid % LPC, ch = tid / LPC;
-    F2 A[SPL / 2], h[SPL / 2];
-    const int64_t row = pl.b * d.D + pl.c0 + ch;
     if (walker) {
-        float av[SPL], hv[SPL];
+        const int lane = tid % LPC, ch = tid / LPC;
+        F2 A[SPL / 2], h[SPL / 2];
+        const int64_t row = pl.b * d.D + pl.c0 + ch;
+        {
+            float av[SPL], hv[SPL];
 #pragma unroll
-        for (int i = 0; i < SPL; ++i) {
-            const int n = lane * SPL + i;
-            const bool on = ch < pl.count && n < d.N;
-            av[i] = on ? a.A[(pl.c0 + ch) * d.N + n] : 0.f;
-            hv[i] = on && !Sum && a.init ? a.init[row * d.N + n] : 0.f;
-        }
-        if (!Sum && ch < pl.count) {
-            for (int k = 0; k < span; ++k) {                        // the spans before this one
-                const int64_t at = (pl.b * (sp.count - 1) + k) * d.D + pl.c0 + ch;
-                const float sum = sp.sum[at];
-                const float* S = sp.state + at * NP + lane * SPL;
+            for (int i = 0; i < SPL; ++i) {
+                const int n = lane * SPL + i;
+                const bool on = ch < pl.count && n < d.N;
+                av[i] = on ? a.A[(pl.c0 + ch) * d.N + n] : 0.f;
+                hv[i] = on && !Sum && a.init ? a.init[row * d.N + n] : 0.f;
+            }
+            if (!Sum && ch < pl.count) {
+                for (int k = 0; k < span; ++k) {                        // the spans before this one
+                    const int64_t at = (pl.b * (sp.count - 1) + k) * d.D + pl.c0 + ch;
+                    const float sum = sp.sum[at];
+                    const float* S = sp.state + at * NP + lane * SPL;
 #pragma unroll
-                for (int i = 0; i < SPL; ++i) hv[i] = fmaf(ex2(sum * av[i]), hv[i], S[i]);
+                    for (int i = 0; i < SPL; ++i) hv[i] = fmaf(ex2(sum * av[i]), hv[i], S[i]);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < SPL / 2; ++i) {
+                A[i] = pack2(av[2 * i], av[2 * i + 1]);
+                h[i] = pack2(hv[2 * i], hv[2 * i + 1]);
             }
         }
-#pragma unroll
-        for (int i = 0; i < SPL / 2; ++i) {
-            A[i] = pack2(av[2 * i], av[2 * i + 1]);
-            h[i] = pack2(hv[2 * i], hv[2 * i + 1]);
-        }
-    }
-    constexpr int TS = kTS;
-    const int64_t nck = (d.L + TS - 1) / TS;
-    float* ck = W == What::Checkpoints
-                    ? final_states + ((pl.b * nck + first / TS) * d.D + pl.c0 + ch) * NP + lane * SPL
-                    : nullptr;
-    int ck_left = (rows + TS - 1) / TS;
-    auto walk = [&](int w) {
-        const float2* du = s_du + w * TT * CH;
-        const float* Bt = s_B + w * TT * NP + lane * SPL;
-        const float* Ct = s_C + w * TT * NP + lane * SPL;
+        constexpr int TS = kTS;
+        const int64_t nck = (d.L + TS - 1) / TS;
+        float* ck = W == What::Checkpoints
+                        ? final_states + ((pl.b * nck + first / TS) * d.D + pl.c0 + ch) * NP + lane * SPL
+                        : nullptr;
+        int ck_left = (rows + TS - 1) / TS;
+        auto walk = [&](int w) {
+            const float2* du = s_du + w * TT * CH;
+            const float* Bt = s_B + w * TT * NP + lane * SPL;
+            const float* Ct = s_C + w * TT * NP + lane * SPL;
 #pragma unroll 1
-        for (int tt = 0; tt < TT; tt += 8) {
-            float ys[TG];
+            for (int tt = 0; tt < TT; tt += 8) {
+                float ys[TG];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                if (W == What::Checkpoints && k % TS == 0) {
-                    if (ch < pl.count && ck_left > 0) {
+                for (int k = 0; k < 8; ++k) {
+                    if (W == What::Checkpoints && k % TS == 0) {
+                        if (ch < pl.count && ck_left > 0) {
 #pragma unroll
-                        for (int i = 0; i < SPL; i += 4) {
-                            const float2 lo = unpack2(h[i / 2]), hi = unpack2(h[i / 2 + 1]);
-                            *reinterpret_cast<float4*>(ck + i) = make_float4(lo.x, lo.y, hi.x, hi.y);
+                            for (int i = 0; i < SPL; i += 4) {
+                                const float2 lo = unpack2(h[i / 2]), hi = unpack2(h[i / 2 + 1]);
+                                *reinterpret_cast<float4*>(ck + i) = make_float4(lo.x, lo.y, hi.x, hi.y);
+                            }
+                        }
+                        ck += d.D * NP;
+                        --ck_left;
+                    }
+                    const float2 q = du[(tt + k) * CH + (ch ^ ((k * PER + ch / VW) & SWZ))];
+                    const F2 dd = pack2(q.x, q.x), uu = pack2(q.y, q.y);
+                    F2 yy = 0;
+#pragma unroll
+                    for (int i = 0; i < SPL; i += 4) {
+                        const float4 bv = *reinterpret_cast<const float4*>(Bt + (tt + k) * NP + i);
+                        const F2 e0 = decay2(dd, A[i / 2]), e1 = decay2(dd, A[i / 2 + 1]);
+                        h[i / 2] = fma2(e0, h[i / 2], mul2(uu, pack2(bv.x, bv.y)));
+                        h[i / 2 + 1] = fma2(e1, h[i / 2 + 1], mul2(uu, pack2(bv.z, bv.w)));
+                        if (Output) {
+                            const float4 cv = *reinterpret_cast<const float4*>(Ct + (tt + k) * NP + i);
+                            yy = i == 0 ? mul2(pack2(cv.x, cv.y), h[0])
+                                        : fma2(pack2(cv.x, cv.y), h[i / 2], yy);
+                            yy = fma2(pack2(cv.z, cv.w), h[i / 2 + 1], yy);
                         }
                     }
-                    ck += d.D * NP;
-                    --ck_left;
-                }
-                const float2 q = du[(tt + k) * CH + (ch ^ ((k * PER + ch / VW) & SWZ))];
-                const F2 dd = pack2(q.x, q.x), uu = pack2(q.y, q.y);
-                F2 yy = 0;
-#pragma unroll
-                for (int i = 0; i < SPL; i += 4) {
-                    const float4 bv = *reinterpret_cast<const float4*>(Bt + (tt + k) * NP + i);
-                    const F2 e0 = decay2(dd, A[i / 2]), e1 = decay2(dd, A[i / 2 + 1]);
-                    h[i / 2] = fma2(e0, h[i / 2], mul2(uu, pack2(bv.x, bv.y)));
-                    h[i / 2 + 1] = fma2(e1, h[i / 2 + 1], mul2(uu, pack2(bv.z, bv.w)));
-                    if (Output) {
-                        const float4 cv = *reinterpret_cast<const float4*>(Ct + (tt + k) * NP + i);
-                        yy = i == 0 ? mul2(pack2(cv.x, cv.y), h[0])
-                                    : fma2(pack2(cv.x, cv.y), h[i / 2], yy);
-                        yy = fma2(pack2(cv.z, cv.w), h[i / 2 + 1], yy);
+                    const float2 f = unpack2(yy);
+                    ys[k % TG] = f.x + f.y;
+                    if (Output && k % TG == TG - 1) {
+                        fold<TG, LPC>(ys, lane);
+                        if (lane % (LPC / TG) == 0)
+                            s_y[(w * TT + tt + k + 1 - TG + lane / (LPC / TG)) * PY + ch] = ys[0];
                     }
                 }
-                const float2 f = unpack2(yy);
-                ys[k % TG] = f.x + f.y;
-                if (Output && k % TG == TG - 1) {
-                    fold<TG, LPC>(ys, lane);
-                    if (lane % (LPC / TG) == 0)
-                        s_y[(w * TT + tt + k + 1 - TG + lane / (LPC / TG)) * PY + ch] = ys[0];
-                }
             }
-        }
-    };
-    // where this thread's loads of a tile come from and go to; positions `at`
-    // of a tile are tokens from the span's first on
-    const int own_rows = (int)(len - first > 0 ? len - first : 0);
-    const T *px[NI], *pdt[NI], *pz[NI], *pbc[NB];
-    int bc_token[NB], bc_to[NB];
-    bool is_b[NB];
-#pragma unroll
-    for (int k = 0; k < NI; ++k) {
-        const int i = k * KC + tid, t = i / PER, c = i % PER * VW < pl.count ? i % PER * VW : 0;
-        px[k] = x + (first + t) * a.xs.token + c;
-        pdt[k] = dt + (first + t) * a.dts.token + c;
-        pz[k] = z ? z + (first + t) * a.zs.token + c : px[k];
-    }
-    const int nvb = Vec ? (int)d.N / VB : 1;
-#pragma unroll
-    for (int k = 0; k < NB; ++k) {
-        const int i = k * KC + tid, t = i / (2 * nvb), v = i % (2 * nvb);
-        is_b[k] = v < nvb;
-        bc_token[k] = t;
-        bc_to[k] = (is_b[k] ? v * VB : BUF * TT * NP + (v - nvb) * VB) + t * NP;
-        pbc[k] = is_b[k] ? Bp + (first + t) * a.Bs.token + v * VB
-                         : Cp + (first + t) * a.Cs.token + (v - nvb) * VB;
-    }
-    const int64_t x_step = TT * a.xs.token, dt_step = TT * a.dts.token,
-                  z_step = TT * (z ? a.zs.token : a.xs.token);
-    auto load = [&](int at) {                                   // into ring place at / TT % RING
-        const int ring = at / TT % RING;
-        if (at < own_rows) {
-#pragma unroll
-            for (int k = 0; k < NI; ++k) {
-                const int i = k * KC + tid, t = i / PER, c = i % PER * VW, o = (ring * NI + k) * KC + tid;
-                if constexpr (Vec) {
-                    const bool in = t < TT && at + t < own_rows && c < pl.count;
-                    copy_async(r_x + o, px[k], in);
-                    copy_async(r_dt + o, pdt[k], in);
-                    if (z) copy_async(r_z + o, pz[k], in);
-                } else {
-                    const int n = t < TT && at + t < own_rows ? pl.count - c : 0;
-                    r_x[o] = load_channels<T, VW>(px[k], n, false);
-                    r_dt[o] = load_channels<T, VW>(pdt[k], n, false);
-                    if (z) r_z[o] = load_channels<T, VW>(pz[k], n, false);
-                }
-                px[k] += x_step;
-                pdt[k] += dt_step;
-                pz[k] += z_step;
-            }
-            if constexpr (Vec) {
-#pragma unroll
-                for (int k = 0; k < NB; ++k) {
-                    copy_async(r_bc + (ring * NB + k) * KC + tid, pbc[k],
-                               bc_token[k] < TT && at + bc_token[k] < own_rows);
-                    pbc[k] += TT * (is_b[k] ? a.Bs.token : a.Cs.token);
-                }
-            }
-        }
-        if constexpr (Vec) copies_commit();
-    };
-    float sum_dt[NI][VW];
-#pragma unroll
-    for (int k = 0; k < NI; ++k)
-#pragma unroll
-        for (int j = 0; j < VW; ++j) sum_dt[k][j] = 0.f;
-    // the loaded tile into buffer w; rows behind the sequence: dt = 0, no input
-    auto stage = [&](int at, int w) {
-        float2* du = s_du + w * TT * CH;
-        const int ring = at / TT % RING;
-        if constexpr (Vec) copies_pending<1>();                 // the tile behind may be under way
-#pragma unroll
-        for (int k = 0; k < NI; ++k) {
-            const int i = k * KC + tid, t = i / PER, c = i % PER * VW, o = (ring * NI + k) * KC + tid;
-            if (t < TT) {
-                const int n = at + t < own_rows ? pl.count - c : 0;
-                const RV rx = r_x[o], rdt = r_dt[o];
-#pragma unroll
-                for (int j = 0; j < VW; ++j) {
-                    float v = to_f32(rdt.v[j]) + s_bias[c + j];
-                    if (a.softplus) v = softplus_f32(v);
-                    float u = v * to_f32(rx.v[j]);
-                    if (j >= n) v = u = 0.f;
-                    v *= kLog2E;                      // the decays are powers of two
-                    if (Sum) sum_dt[k][j] += v;
-                    du[t * CH + ((c + j) ^ (i & SWZ))] = make_float2(v, u);
-                }
-            }
-        }
-        if constexpr (Vec) {
-#pragma unroll
-            for (int k = 0; k < NB; ++k) {
-                if (bc_token[k] < TT) {
-                    float f[VB];
-                    raw_to_f32(at + bc_token[k] < own_rows ? r_bc[(ring * NB + k) * KC + tid]
-                                                           : raw_zero<T, VB>(), f);
-                    float* q = s_B + w * TT * NP + bc_to[k];
-#pragma unroll
-                    for (int j = 0; j < VB; j += 4)
-                        *reinterpret_cast<float4*>(q + j) = make_float4(f[j], f[j + 1], f[j + 2], f[j + 3]);
-                }
-            }
-        } else {
-            for (int i = tid; i < TT * NP; i += KC) {
-                const int t = i / NP, n = i % NP;
-                const bool on = n < d.N && at + t < own_rows;
-                s_B[w * TT * NP + i] = on ? to_f32(Bp[(first + at + t) * a.Bs.token + n]) : 0.f;
-                if (Output)
-                    s_C[w * TT * NP + i] = on ? to_f32(Cp[(first + at + t) * a.Cs.token + n]) : 0.f;
-            }
-        }
-    };
-    T* py = y + first * d.D;
-    auto finish = [&](int at, int w) {
-#pragma unroll
-        for (int k = 0; k < NI; ++k) {
-            const int i = k * KC + tid, t = i / PER, c = i % PER * VW;
-            if (t < TT && at + t < rows) {
-                const int n = at + t < own_rows ? pl.count - c : 0;
-                const int q = ((at / TT % RING) * NI + k) * KC + tid;
-                const RV kx = r_x[q];
-                RV kz;
-                if (z) kz = r_z[q];
-                float o[VW];
-#pragma unroll
-                for (int j = 0; j < VW; ++j) {
-                    o[j] = fmaf(s_skip[c + j], to_f32(kx.v[j]), s_y[(w * TT + t) * PY + c + j]);
-                    if (z) {
-                        const float zv = to_f32(kz.v[j]);
-                        o[j] *= zv * sigmoid_fast(zv);
-                    }
-                    if (j >= n) o[j] = 0.f;
-                }
-                store_channels<T, VW>(py + (int64_t)(at + t) * d.D + c, raw_from_f32<T, VW>(o),
-                                      pl.count - c, Vec);
-            }
-        }
-    };
-
-    if constexpr (!Split) {
-        load(0);
-        for (int at = 0; at < rows; at += TT) {
-            load(at + TT);
-            stage(at, 0);
-            __syncthreads();
-            walk(0);
-            __syncthreads();
-            if (Output) finish(at, 0);
-        }
-    } else if (walker) {
+        };
         __syncthreads();                                             // the first tile is down
         for (int at = 0; at < rows; at += 2 * TT) {
             walk(0);
@@ -345,27 +195,6 @@ scan_fwd_kernel(const SelectiveArgs a, T* __restrict__ y, float* __restrict__ fi
                 __syncthreads();
             }
         }
-    } else {
-        load(0);
-        load(TT);
-        if (rows > 0) stage(0, 0);
-        load(2 * TT);
-        __syncthreads();                                             // the first tile is down
-        auto tile = [&](int at, int w) {
-            if (Output && at > 0) finish(at - TT, w ^ 1);
-            if (at + TT < rows) {
-                stage(at + TT, w ^ 1);
-                load(at + 3 * TT);
-            }
-            __syncthreads();
-            if (Output && at + TT >= rows) finish(at, w);
-        };
-        for (int at = 0; at < rows; at += 2 * TT) {
-            tile(at, 0);
-            if (at + TT < rows) tile(at + TT, 1);
-        }
-    }
-    if (walker) {
         float hv[SPL];
 #pragma unroll
         for (int i = 0; i < SPL / 2; ++i) {
@@ -386,14 +215,168 @@ scan_fwd_kernel(const SelectiveArgs a, T* __restrict__ y, float* __restrict__ fi
                 for (int i = 0; i < SPL; ++i) sp.state[(at + ch) * NP + lane * SPL + i] = hv[i];
             }
         }
-    }
-    if (Sum && carrier) {
+    } else {
+        // where this thread's loads of a tile come from and go to; positions `at`
+        // of a tile are tokens from the span's first on
+        const int own_rows = (int)(len - first > 0 ? len - first : 0);
+        const T *px[NI], *pdt[NI], *pz[NI], *pbc[NB];
+        int bc_token[NB], bc_to[NB];
+        bool is_b[NB];
 #pragma unroll
         for (int k = 0; k < NI; ++k) {
-            const int i = k * KC + tid, t = i / PER, c = i % PER * VW;
-            if (t < TT) {
+            const int i = k * KC + tid, t = i / PER, c = i % PER * VW < pl.count ? i % PER * VW : 0;
+            px[k] = x + (first + t) * a.xs.token + c;
+            pdt[k] = dt + (first + t) * a.dts.token + c;
+            pz[k] = z ? z + (first + t) * a.zs.token + c : px[k];
+        }
+        const int nvb = Vec ? (int)d.N / VB : 1;
 #pragma unroll
-                for (int j = 0; j < VW; ++j) s_y[t * PY + c + j] = sum_dt[k][j];
+        for (int k = 0; k < NB; ++k) {
+            const int i = k * KC + tid, t = i / (2 * nvb), v = i % (2 * nvb);
+            is_b[k] = v < nvb;
+            bc_token[k] = t;
+            bc_to[k] = (is_b[k] ? v * VB : 2 * TT * NP + (v - nvb) * VB) + t * NP;
+            pbc[k] = is_b[k] ? Bp + (first + t) * a.Bs.token + v * VB
+                             : Cp + (first + t) * a.Cs.token + (v - nvb) * VB;
+        }
+        const int64_t x_step = TT * a.xs.token, dt_step = TT * a.dts.token,
+                      z_step = TT * (z ? a.zs.token : a.xs.token);
+        auto load = [&](int at) {                                   // into ring place at / TT % 4
+            const int ring = at / TT & 3;
+            if (at < own_rows) {
+#pragma unroll
+                for (int k = 0; k < NI; ++k) {
+                    const int i = k * KC + tid, t = i / PER, c = i % PER * VW, o = (ring * NI + k) * KC + tid;
+                    if constexpr (Vec) {
+                        const bool in = t < TT && at + t < own_rows && c < pl.count;
+                        copy_async(r_x + o, px[k], in);
+                        copy_async(r_dt + o, pdt[k], in);
+                        if (z) copy_async(r_z + o, pz[k], in);
+                    } else {
+                        const int n = t < TT && at + t < own_rows ? pl.count - c : 0;
+                        r_x[o] = load_channels<T, VW>(px[k], n, false);
+                        r_dt[o] = load_channels<T, VW>(pdt[k], n, false);
+                        if (z) r_z[o] = load_channels<T, VW>(pz[k], n, false);
+                    }
+                    px[k] += x_step;
+                    pdt[k] += dt_step;
+                    pz[k] += z_step;
+                }
+                if constexpr (Vec) {
+#pragma unroll
+                    for (int k = 0; k < NB; ++k) {
+                        copy_async(r_bc + (ring * NB + k) * KC + tid, pbc[k],
+                                   bc_token[k] < TT && at + bc_token[k] < own_rows);
+                        pbc[k] += TT * (is_b[k] ? a.Bs.token : a.Cs.token);
+                    }
+                }
+            }
+            if constexpr (Vec) copies_commit();
+        };
+        float sum_dt[NI][VW];
+#pragma unroll
+        for (int k = 0; k < NI; ++k)
+#pragma unroll
+            for (int j = 0; j < VW; ++j) sum_dt[k][j] = 0.f;
+        // the loaded tile into buffer w; rows behind the sequence: dt = 0, no input
+        auto stage = [&](int at, int w) {
+            float2* du = s_du + w * TT * CH;
+            const int ring = at / TT & 3;
+            if constexpr (Vec) copies_pending<1>();                 // the tile behind may be under way
+#pragma unroll
+            for (int k = 0; k < NI; ++k) {
+                const int i = k * KC + tid, t = i / PER, c = i % PER * VW, o = (ring * NI + k) * KC + tid;
+                if (t < TT) {
+                    const int n = at + t < own_rows ? pl.count - c : 0;
+                    const RV rx = r_x[o], rdt = r_dt[o];
+#pragma unroll
+                    for (int j = 0; j < VW; ++j) {
+                        float v = to_f32(rdt.v[j]) + s_bias[c + j];
+                        if (a.softplus) v = softplus_f32(v);
+                        float u = v * to_f32(rx.v[j]);
+                        if (j >= n) v = u = 0.f;
+                        v *= kLog2E;                      // the decays are powers of two
+                        if (Sum) sum_dt[k][j] += v;
+                        du[t * CH + ((c + j) ^ (i & SWZ))] = make_float2(v, u);
+                    }
+                }
+            }
+            if constexpr (Vec) {
+#pragma unroll
+                for (int k = 0; k < NB; ++k) {
+                    if (bc_token[k] < TT) {
+                        float f[VB];
+                        raw_to_f32(at + bc_token[k] < own_rows ? r_bc[(ring * NB + k) * KC + tid]
+                                                               : raw_zero<T, VB>(), f);
+                        float* q = s_B + w * TT * NP + bc_to[k];
+#pragma unroll
+                        for (int j = 0; j < VB; j += 4)
+                            *reinterpret_cast<float4*>(q + j) = make_float4(f[j], f[j + 1], f[j + 2], f[j + 3]);
+                    }
+                }
+            } else {
+                for (int i = tid; i < TT * NP; i += KC) {
+                    const int t = i / NP, n = i % NP;
+                    const bool on = n < d.N && at + t < own_rows;
+                    s_B[w * TT * NP + i] = on ? to_f32(Bp[(first + at + t) * a.Bs.token + n]) : 0.f;
+                    if (Output)
+                        s_C[w * TT * NP + i] = on ? to_f32(Cp[(first + at + t) * a.Cs.token + n]) : 0.f;
+                }
+            }
+        };
+        T* py = y + first * d.D;
+        auto finish = [&](int at, int w) {
+#pragma unroll
+            for (int k = 0; k < NI; ++k) {
+                const int i = k * KC + tid, t = i / PER, c = i % PER * VW;
+                if (t < TT && at + t < rows) {
+                    const int n = at + t < own_rows ? pl.count - c : 0;
+                    const int q = ((at / TT & 3) * NI + k) * KC + tid;
+                    const RV kx = r_x[q];
+                    RV kz;
+                    if (z) kz = r_z[q];
+                    float o[VW];
+#pragma unroll
+                    for (int j = 0; j < VW; ++j) {
+                        o[j] = fmaf(s_skip[c + j], to_f32(kx.v[j]), s_y[(w * TT + t) * PY + c + j]);
+                        if (z) {
+                            const float zv = to_f32(kz.v[j]);
+                            o[j] *= zv * sigmoid_fast(zv);
+                        }
+                        if (j >= n) o[j] = 0.f;
+                    }
+                    store_channels<T, VW>(py + (int64_t)(at + t) * d.D + c, raw_from_f32<T, VW>(o),
+                                          pl.count - c, Vec);
+                }
+            }
+        };
+
+        load(0);
+        load(TT);
+        if (rows > 0) stage(0, 0);
+        load(2 * TT);
+        __syncthreads();                                             // the first tile is down
+        auto tile = [&](int at, int w) {
+            if (Output && at > 0) finish(at - TT, w ^ 1);
+            if (at + TT < rows) {
+                stage(at + TT, w ^ 1);
+                load(at + 3 * TT);
+            }
+            __syncthreads();
+            if (Output && at + TT >= rows) finish(at, w);
+        };
+        for (int at = 0; at < rows; at += 2 * TT) {
+            tile(at, 0);
+            if (at + TT < rows) tile(at + TT, 1);
+        }
+        if (Sum) {
+#pragma unroll
+            for (int k = 0; k < NI; ++k) {
+                const int i = k * KC + tid, t = i / PER, c = i % PER * VW;
+                if (t < TT) {
+#pragma unroll
+                    for (int j = 0; j < VW; ++j) s_y[t * PY + c + j] = sum_dt[k][j];
+                }
             }
         }
     }
@@ -579,7 +562,6 @@ size_t selective_fwd_workspace_bytes(const SelectiveDims& d, Elt t) {
     return (size_t)(d.b * (sp.count - 1) * d.D * (padded_states(d.N) + 1)) * 4;
 }
 
-constexpr bool kSplitAlways = false;
 // The span states where there are several spans, then the walk for `W`.
 template <What W>
 cudaError_t run_fwd(const SelectiveArgs& a, void* y, float* out, float* ws, const SelectiveDims& d,
@@ -590,34 +572,25 @@ cudaError_t run_fwd(const SelectiveArgs& a, void* y, float* out, float* ws, cons
         using T = typename decltype(ty)::type;
         with_layout(d.N, [&](auto lay) {
             using Lay = decltype(lay);
-            const int64_t blocks = d.b * channel_blocks<Lay::CH>(d);
-            auto go = [&](auto kernel, auto f, int spans) {
-                using F = decltype(f);
+            using F = Fwd<T, Lay>;
+            const unsigned blocks = (unsigned)(d.b * channel_blocks<Lay::CH>(d));
+            const bool vec = selective_vec<T>(a, d, F::VW) && d.N % F::VB == 0 &&
+                             rows_fit<T>(a.B, a.Bs, F::VB) && rows_fit<T>(a.C, a.Cs, F::VB);
+            auto go = [&](auto kernel, unsigned spans) {
+                err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                           F::SMEM);
                 if (err == cudaSuccess)
-                    err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               F::SMEM);
-                if (err == cudaSuccess)
-                    kernel<<<dim3((unsigned)blocks, (unsigned)spans), F::THREADS, F::SMEM, s>>>(
+                    kernel<<<dim3(blocks, spans), F::THREADS, F::SMEM, s>>>(
                         a, static_cast<T*>(y), out, sp, d);
             };
-            using S = Fwd<T, Lay, true>;
-            using U = Fwd<T, Lay, false>;
-            auto fits = [&](int vw, int vb) {
-                return selective_vec<T>(a, d, vw) && d.N % vb == 0 && rows_fit<T>(a.B, a.Bs, vb) &&
-                       rows_fit<T>(a.C, a.Cs, vb);
+            auto both = [&](auto state_only, auto whole) {
+                if (sp.count > 1) go(state_only, (unsigned)sp.count - 1);
+                if (err == cudaSuccess) go(whole, (unsigned)sp.count);
             };
-            if (!kSplitAlways && blocks > 148 * S::BLOCKS) {
-                if (fits(U::VW, U::VB)) go(scan_fwd_kernel<T, Lay, W, true, false>, U{}, 1);
-                else go(scan_fwd_kernel<T, Lay, W, false, false>, U{}, 1);
-                return;
-            }
-            const bool vec = fits(S::VW, S::VB);
-            if (sp.count > 1) {
-                if (vec) go(scan_fwd_kernel<T, Lay, What::SpanState, true, true>, S{}, sp.count - 1);
-                else go(scan_fwd_kernel<T, Lay, What::SpanState, false, true>, S{}, sp.count - 1);
-            }
-            if (vec) go(scan_fwd_kernel<T, Lay, W, true, true>, S{}, sp.count);
-            else go(scan_fwd_kernel<T, Lay, W, false, true>, S{}, sp.count);
+            if (vec)
+                both(scan_fwd_kernel<T, Lay, What::SpanState, true>, scan_fwd_kernel<T, Lay, W, true>);
+            else
+                both(scan_fwd_kernel<T, Lay, What::SpanState, false>, scan_fwd_kernel<T, Lay, W, false>);
         });
     });
     return err != cudaSuccess ? err : cudaGetLastError();

@@ -38,7 +38,10 @@ template <typename T, typename Lay>
 struct Bwd {
     static constexpr int NP = Lay::NP, CH = Lay::CH;
     static constexpr int TT = NP <= 64 ? 16 : 8;                     // tokens of a tile
-    static constexpr int VW = spread_width<T, CH>(TT * CH / kThreads);   // channels of a load
+    // channels of a load: as many as keep every thread busy
+    static constexpr int VW = TT * CH / kThreads < load_width<T, CH>()
+                                  ? (TT * CH / kThreads < 4 ? 4 : TT * CH / kThreads)
+                                  : load_width<T, CH>();
     static constexpr int PER = CH / VW;
     static constexpr int IT = (TT * PER + kThreads - 1) / kThreads;  // loads a thread and tile
     static constexpr int VB = 16 / sizeof(T);
