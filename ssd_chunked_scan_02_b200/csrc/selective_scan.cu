@@ -36,7 +36,7 @@ enum class What { SpanState, Output, Checkpoints };
 template <typename T, typename Lay>
 struct Fwd {
     static constexpr int TT = Lay::TT, CH = Lay::CH, NP = Lay::NP;
-    static constexpr int PY = CH + 8;                               // s_y's row: no bank twice
+    static constexpr int PY = CH + 4;                               // s_y's row: no bank twice
     static constexpr int KC = 128;                                  // threads of the carriers
     static constexpr int THREADS = kWalkers + KC;
     static constexpr int VW = load_width<T, CH>();
@@ -62,7 +62,6 @@ scan_fwd_kernel(const SelectiveArgs a, T* __restrict__ y, float* __restrict__ fi
     constexpr bool Output = W == What::Output, Sum = W == What::SpanState;
     constexpr int SPL = Lay::SPL, LPC = Lay::LPC, NP = Lay::NP, CH = Lay::CH, TT = Lay::TT;
     constexpr int VW = F::VW, NI = F::NI, VB = F::VB, NB = F::NB, PY = F::PY, KC = F::KC;
-    constexpr int TG = LPC < 8 ? LPC : 8;                           // tokens summed at once
     // s_du's columns are permuted by the number of the load that brings them, so
     // that neither the eight lanes that store side by side nor those that read
     // meet a bank twice
@@ -146,7 +145,7 @@ scan_fwd_kernel(const SelectiveArgs a, T* __restrict__ y, float* __restrict__ fi
             const float* Ct = s_C + w * TT * NP + lane * SPL;
 #pragma unroll 1
             for (int tt = 0; tt < TT; tt += 8) {
-                float ys[TG];
+                float ys[8];                    // of eight tokens, summed over the lanes at once
 #pragma unroll
                 for (int k = 0; k < 8; ++k) {
                     if (W == What::Checkpoints && k % TS == 0) {
@@ -177,11 +176,15 @@ scan_fwd_kernel(const SelectiveArgs a, T* __restrict__ y, float* __restrict__ fi
                         }
                     }
                     const float2 f = unpack2(yy);
-                    ys[k % TG] = f.x + f.y;
-                    if (Output && k % TG == TG - 1) {
-                        fold<TG, LPC>(ys, lane);
-                        if (lane % (LPC / TG) == 0)
-                            s_y[(w * TT + tt + k + 1 - TG + lane / (LPC / TG)) * PY + ch] = ys[0];
+                    ys[k] = f.x + f.y;
+                }
+                if (Output) {
+                    fold<8, LPC>(ys, lane);
+                    constexpr int NT = LPC < 8 ? 8 / LPC : 1, SH = LPC < 8 ? 1 : LPC / 8;
+                    if (lane % SH == 0) {
+#pragma unroll
+                        for (int i = 0; i < NT; ++i)
+                            s_y[(w * TT + tt + lane / SH * NT + i) * PY + ch] = ys[i];
                     }
                 }
             }

@@ -109,6 +109,8 @@ CASES = [
     Case(1, 29, 12, 100, softplus=False),
     Case(1, 20, 9, 256, dt="f32", lens=[13]),
     Case(2, 300, 8, 1, skip=False),
+    Case(15, 19, 960, 16, init=False),                 # more blocks than 148 SMs hold at once
+    Case(4, 37, 500, 5, G=125, dt="f32", lens=[37, 36, 0, 17]),
 ]
 
 
