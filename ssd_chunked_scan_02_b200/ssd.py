@@ -69,7 +69,9 @@ class ssd_selective_dims_t(ctypes.Structure):
 
 
 class ssd_selective_strides_t(ctypes.Structure):
-    _fields_ = [(k, ssd_stride_t) for k in ("x", "dt", "B", "C", "z")]
+    # the C struct's five ssd_stride_t, flat
+    _fields_ = [(f"{k}_{s}", ctypes.c_int64) for k in ("x", "dt", "B", "C", "z")
+                for s in ("batch", "token")]
 
 
 class ssd_rotate_dims_t(ctypes.Structure):
@@ -620,15 +622,15 @@ def _dense(name, t, shape, dtype, device):
     return t.data_ptr()
 
 
-def _view(name, t, shape, dtype, device, tokens=True):
+def _view(name, t, shape, dtype, device, lead=2):
     """An argument that may be a view of a wider tensor: checked, then its
-    address and its batch and token strides.  The dimensions behind the token
-    (or, without tokens, the batch) have to be contiguous."""
+    address and its strides (batch, token; with lead 1 the batch's alone, and 0).
+    The dimensions behind those have to be contiguous."""
     if t is None:
-        return None, ssd_stride_t(0, 0)
+        return None, 0, 0
     if t.shape != shape or t.dtype != dtype or t.device != device:
         _expect(name, t, shape, dtype, device)
-    lead, strides = 2 if tokens else 1, t.stride()
+    strides = t.stride()
     if not t.is_contiguous():
         run = 1
         for i in range(len(shape) - 1, lead - 1, -1):
@@ -636,7 +638,7 @@ def _view(name, t, shape, dtype, device, tokens=True):
                 raise ValueError(f"{name}: its last {len(shape) - lead} dimension(s) must be "
                                  "contiguous")
             run *= shape[i]
-    return t.data_ptr(), ssd_stride_t(strides[0], strides[1] if tokens else 0)
+    return t.data_ptr(), strides[0], strides[1] if lead == 2 else 0
 
 
 def _workspace(workspace, need, device):
@@ -665,7 +667,8 @@ def ssd_causal_conv_fwd(x, weight, bias=None, init_state=None, seq_lens=None, si
     b, L, D, W, dims = _conv_dims(x, weight)
     dev, T, f32 = x.device, x.dtype, torch.float32
     code = _dtype_code(T)
-    px, sx = _view("x", x, (b, L, D), T, dev)
+    px, *sx = _view("x", x, (b, L, D), T, dev)
+    sx = ssd_stride_t(*sx)
     pw = _dense("weight", weight, (D, W), f32, dev)
     pb = _dense("bias", bias, (D,), f32, dev)
     pi = _dense("init_state", init_state, (b, W - 1, D), T, dev)
@@ -699,7 +702,8 @@ def ssd_causal_conv_bwd(x, weight, bias, dy, init_state=None, dfinal_state=None,
     b, L, D, W, dims = _conv_dims(x, weight)
     dev, T, f32 = x.device, x.dtype, torch.float32
     code = _dtype_code(T)
-    px, sx = _view("x", x, (b, L, D), T, dev)
+    px, *sx = _view("x", x, (b, L, D), T, dev)
+    sx = ssd_stride_t(*sx)
     pw = _dense("weight", weight, (D, W), f32, dev)
     pb = _dense("bias", bias, (D,), f32, dev)
     pi = _dense("init_state", init_state, (b, W - 1, D), T, dev)
@@ -729,7 +733,8 @@ def ssd_causal_conv_step(state, x, weight, bias=None, silu: bool = True, y=None,
     W = weight.shape[1]
     dev, T, f32 = x.device, x.dtype, torch.float32
     code = _dtype_code(T)
-    px, sx = _view("x", x, (b, D), T, dev, tokens=False)
+    px, *sx = _view("x", x, (b, D), T, dev, 1)
+    sx = ssd_stride_t(*sx)
     ps = _dense("state", state, (b, W - 1, D), T, dev)
     pw = _dense("weight", weight, (D, W), f32, dev)
     pb = _dense("bias", bias, (D,), f32, dev)
@@ -757,15 +762,15 @@ def _selective_args(x, dt, A, B, C, D, z, dt_bias, softplus, tokens=True):
     dev, T, f32 = x.device, x.dtype, torch.float32
     code = _dtype_code(T)
     bc = shape[:lead] + (G, N)
-    px, sx = _view("x", x, shape, T, dev, tokens)
-    pdt, sdt = _view("dt", dt, shape, T, dev, tokens)
-    pB, sB = _view("B", B, bc, T, dev, tokens)
-    pC, sC = _view("C", C, bc, T, dev, tokens)
-    pz, sz = _view("z", z, shape, T, dev, tokens)
+    px, x0, x1 = _view("x", x, shape, T, dev, lead)
+    pdt, t0, t1 = _view("dt", dt, shape, T, dev, lead)
+    pB, B0, B1 = _view("B", B, bc, T, dev, lead)
+    pC, C0, C1 = _view("C", C, bc, T, dev, lead)
+    pz, z0, z1 = _view("z", z, shape, T, dev, lead)
     args = (px, pdt, _dense("A", A, (ch, N), f32, dev), pB, pC, _dense("D", D, (ch,), f32, dev), pz,
             _dense("dt_bias", dt_bias, (ch,), f32, dev), int(softplus))
-    return (args, ssd_selective_strides_t(sx, sdt, sB, sC, sz), ssd_selective_dims_t(b, L, ch, N, G),
-            dev, code)
+    return (args, ssd_selective_strides_t(x0, x1, t0, t1, B0, B1, C0, C1, z0, z1),
+            ssd_selective_dims_t(b, L, ch, N, G), dev, code)
 
 
 def ssd_selective_scan_fwd_workspace_size(dims: ssd_selective_dims_t, dtype: torch.dtype) -> int:
@@ -872,11 +877,11 @@ def _rotate_args(B, C, B_weight, C_weight, positions, freq, eps, interleaved):
     b, L, G, N = B.shape
     dev, T, f32 = B.device, B.dtype, torch.float32
     code = _dtype_code(T)
-    pB, sB = _view("B", B, (b, L, G, N), T, dev)
-    pC, sC = _view("C", C, (b, L, G, N), T, dev)
+    pB, *sB = _view("B", B, (b, L, G, N), T, dev)
+    pC, *sC = _view("C", C, (b, L, G, N), T, dev)
     per_group = B_weight.dim() == 2
     shape = (G, N) if per_group else (N,)
-    args = (pB, sB, pC, sC, _dense("B_weight", B_weight, shape, f32, dev),
+    args = (pB, ssd_stride_t(*sB), pC, ssd_stride_t(*sC), _dense("B_weight", B_weight, shape, f32, dev),
             _dense("C_weight", C_weight, shape, f32, dev), int(per_group),
             _dense("positions", positions, (b, L), torch.int64, dev),
             _dense("freq", freq, (freq.shape[0],), f32, dev), float(eps), int(interleaved))

@@ -18,7 +18,7 @@ def lib():
 
 
 P = 0x1000
-ST = ssd.ssd_selective_strides_t(*[ssd.ssd_stride_t(64, 8) for _ in range(5)])
+ST = ssd.ssd_selective_strides_t(*[64, 8] * 5)
 
 
 @pytest.mark.parametrize("dims,want", [
