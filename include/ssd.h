@@ -415,8 +415,9 @@ SSD_API ssd_status_t ssd_chunk_scan_fwd_with_flow(const void* x, const float* dt
  *  - An input that has an ssd_stride_t may be a view of a wider tensor (a slice
  *    of a projection's output): its last dimension (channels, or groups and
  *    states) is contiguous, its batch and token strides are given in elements,
- *    and its pointer only has to be aligned to its element.  Everything else is
- *    dense and 16-byte aligned.
+ *    and its pointer only has to be aligned to its element.  Strides are >= 0
+ *    (0: the same row for all), a token's below 2^31.  Everything else is dense
+ *    and 16-byte aligned.
  *  - Parameters (convolution weights and bias, A, D, dt_bias, norm weights,
  *    frequencies) and their gradients are fp32.  Gradients of activations are in
  *    dtype: computed in fp32, rounded once.  No result depends on the order of
@@ -535,7 +536,8 @@ SSD_API ssd_status_t ssd_selective_scan_fwd(const void* x, const void* dt, const
  * dC (b,L,G,N) dtype (sums over a group's channels), dz (b,L,D) dtype (only
  * where z is given), dA (D,N), dD (D), ddt_bias (D) fp32 (dD, ddt_bias, and
  * dinit_states (b,D,N) fp32 = dL/dinit_states, may be NULL: not wanted).
- * workspace: the states at every eighth token, and partial sums.
+ * workspace: the states before every fourth token, partial sums, and what the
+ * forward keeps there.
  */
 SSD_API ssd_status_t ssd_selective_scan_bwd_workspace_size(const ssd_selective_dims_t* dims,
                                                            ssd_dtype_t dtype, size_t* bytes);

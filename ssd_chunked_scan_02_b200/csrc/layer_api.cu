@@ -26,8 +26,9 @@ ssd_status_t check_tokens(int64_t batch, int64_t seqlen) {
     if (batch < 0 || seqlen < 0)
         return fail(SSD_ERR_INVALID_ARG, "batch (%lld) and seqlen (%lld) must be >= 0",
                     (long long)batch, (long long)seqlen);
-    if (batch > kMaxSize || seqlen > kMaxSize)
-        return fail(SSD_ERR_UNSUPPORTED, "batch and seqlen must be below 2^31");
+    // (token indexes are 32 bits wide, with room for the tile behind the last token)
+    if (batch > kMaxSize || seqlen > kMaxSize - 0xffff)
+        return fail(SSD_ERR_UNSUPPORTED, "batch must be below 2^31 and seqlen below 2^31 - 2^16");
     return SSD_OK;
 }
 
@@ -124,6 +125,13 @@ ssd_status_t check_stride(const ssd_stride_t& s, const char* name) {
     return SSD_OK;
 }
 
+// The step calls ignore the token strides.
+#define CHECK_BATCH_STRIDE(s, name)                                                      \
+    do {                                                                                 \
+        if ((s).batch < 0)                                                               \
+            return fail(SSD_ERR_INVALID_ARG, "%s strides must be >= 0", name);           \
+    } while (0)
+
 #define CHECK_STRIDE(s, name)                                                            \
     do {                                                                                 \
         ssd_status_t st_stride_ = check_stride((s), name);                               \
@@ -219,7 +227,7 @@ ssd_status_t ssd_causal_conv_step(void* state, const void* x, const ssd_stride_t
     if (st != SSD_OK) return st;
     OPTIONAL_PTR(bias);
     REQUIRE_STRIDE(x_stride);
-    CHECK_STRIDE(*x_stride, "x");
+    CHECK_BATCH_STRIDE(*x_stride, "x");
     if (d.b == 0) return SSD_OK;
     REQUIRE_PTR(state); REQUIRE_PTR(weight); REQUIRE_PTR(y);
     REQUIRE_VIEW(x);
@@ -356,9 +364,9 @@ ssd_status_t ssd_selective_step(float* state, const void* x, const void* dt, con
     if (st != SSD_OK) return st;
     OPTIONAL_PTR(D); OPTIONAL_PTR(dt_bias);
     REQUIRE_STRIDE(strides);
-    CHECK_STRIDE(strides->x, "x"); CHECK_STRIDE(strides->dt, "dt");
-    CHECK_STRIDE(strides->B, "B"); CHECK_STRIDE(strides->C, "C");
-    if (z) CHECK_STRIDE(strides->z, "z");
+    CHECK_BATCH_STRIDE(strides->x, "x"); CHECK_BATCH_STRIDE(strides->dt, "dt");
+    CHECK_BATCH_STRIDE(strides->B, "B"); CHECK_BATCH_STRIDE(strides->C, "C");
+    if (z) CHECK_BATCH_STRIDE(strides->z, "z");
     if (d.b == 0) return SSD_OK;
     REQUIRE_PTR(state); REQUIRE_PTR(A); REQUIRE_PTR(y);
     REQUIRE_VIEW(x); REQUIRE_VIEW(dt); REQUIRE_VIEW(B); REQUIRE_VIEW(C);

@@ -482,24 +482,38 @@ scan_bwd_kernel(const SelectiveArgs a, const SelectiveGrads gr, const float* __r
 }
 
 // dB, dC (b,L,G,N): the sum of a group's channel blocks' partial rows
-// (blocks, b, L, 2, NP), four states a thread, several rows in flight.
+// (blocks, b, L, 2, NP).  64 columns of four states x 4 shares of the blocks a
+// thread block, eight rows of a share in flight.
 template <typename T>
 __global__ void __launch_bounds__(256)
 reduce_bc_kernel(const float* __restrict__ part, T* __restrict__ dB, T* __restrict__ dC,
-                 const SelectiveDims d, int64_t per_group, int NP) {
+                 const SelectiveDims d, int per_group, int NP) {
     const int64_t tokens = d.b * d.L, row = 2 * NP, total = tokens * d.G * row / 4;
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+    __shared__ float4 red[4][64];
+    for (int64_t i0 = (int64_t)blockIdx.x * 64; i0 < total; i0 += (int64_t)gridDim.x * 64) {
+        const int64_t i = i0 + threadIdx.x;
         const int64_t at = i * 4 % (tokens * row), g = i * 4 / (tokens * row);
-        const int64_t tok = at / row, n = at % NP;
-        const bool isC = at % row >= NP;
-        const float4* p = reinterpret_cast<const float4*>(part + g * per_group * tokens * row + at);
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (i < total) {
+            const float4* p = reinterpret_cast<const float4*>(part + g * per_group * tokens * row + at);
+            const int64_t step = tokens * row / 4;
 #pragma unroll 8
-        for (int64_t k = 0; k < per_group; ++k) {
-            const float4 o = __ldcs(p + k * (tokens * row / 4));
+            for (int k = threadIdx.y; k < per_group; k += 4) {
+                const float4 o = __ldcs(p + k * step);
+                v.x += o.x; v.y += o.y; v.z += o.z; v.w += o.w;
+            }
+        }
+        __syncthreads();
+        red[threadIdx.y][threadIdx.x] = v;
+        __syncthreads();
+        if (threadIdx.y || i >= total) continue;
+#pragma unroll
+        for (int k = 1; k < 4; ++k) {
+            const float4 o = red[k][threadIdx.x];
             v.x += o.x; v.y += o.y; v.z += o.z; v.w += o.w;
         }
-        T* out = (isC ? dC : dB) + (tok * d.G + g) * d.N + n;
+        const int64_t tok = at / row, n = at % NP;
+        T* out = (at % row >= NP ? dC : dB) + (tok * d.G + g) * d.N + n;
         if (n < d.N) out[0] = from_f32<T>(v.x);
         if (n + 1 < d.N) out[1] = from_f32<T>(v.y);
         if (n + 2 < d.N) out[2] = from_f32<T>(v.z);
@@ -572,9 +586,9 @@ cudaError_t launch_selective_bwd(const SelectiveArgs& a, const SelectiveGrads& g
             else
                 both(scan_bwd_kernel<T, Lay, false, true>, scan_bwd_kernel<T, Lay, false, false>);
             if (err == cudaSuccess && d.L > 0) {
-                const int64_t total = d.b * d.L * d.G * 2 * Lay::NP / 4, nblk = (total + 255) / 256;
-                reduce_bc_kernel<T><<<(unsigned)(nblk < 148 * 16 ? nblk : 148 * 16), 256, 0, s>>>(
-                    ws + w.bc, static_cast<T*>(g.dB), static_cast<T*>(g.dC), d, nb / d.G,
+                const int64_t nblk = (d.b * d.L * d.G * 2 * Lay::NP / 4 + 63) / 64;
+                reduce_bc_kernel<T><<<(unsigned)(nblk < 148 * 8 ? nblk : 148 * 8), dim3(64, 4), 0, s>>>(
+                    ws + w.bc, static_cast<T*>(g.dB), static_cast<T*>(g.dC), d, (int)(nb / d.G),
                     Lay::NP);
             }
         });

@@ -33,7 +33,7 @@ def _fwd(lib, dims, x=P, xs=ST, w=P, bias=P, init=None, lens=None, y=P, fin=None
 
 @pytest.mark.parametrize("dims,want", [
     ((-1, 8, 8, 4), 1), ((1, -8, 8, 4), 1), ((1, 8, 0, 4), 1), ((1, 8, 8, 1), 2), ((1, 8, 8, 5), 2),
-    ((1 << 31, 8, 8, 4), 2), ((1, 1 << 31, 8, 4), 2), ((1, 8, 1 << 30, 4), 2),
+    ((1 << 31, 8, 8, 4), 2), ((1, 1 << 31, 8, 4), 2), ((1, (1 << 31) - 9, 8, 4), 2), ((1, 8, 1 << 30, 4), 2),
     ((1 << 20, 1 << 20, 64, 4), 2)])
 def test_sizes_refused(lib, dims, want):
     d = ssd.ssd_conv_dims_t(*dims)
@@ -52,6 +52,10 @@ def test_pointers_refused(lib):
         assert _fwd(lib, d, **{k: P + 8}) == 1 and b"16-byte" in lib.ssd_last_error_detail(), k
     assert _fwd(lib, d, lens=P + 2) == 1
     assert _fwd(lib, d, dt=7) == 1
+    for bad, want in ((ssd.ssd_stride_t(-1, 8), 1), (ssd.ssd_stride_t(64, -8), 1),
+                      (ssd.ssd_stride_t(64, 1 << 31), 2)):
+        assert _fwd(lib, d, xs=bad) == want
+    assert lib.ssd_causal_conv_step(P, P, ssd.ssd_stride_t(-1, 0), P, P, 1, P, d, 1, None) == 1
     # an empty batch, and no tokens without a final state, launch nothing
     assert _fwd(lib, ssd.ssd_conv_dims_t(0, 8, 8, 4), x=None, w=None, y=None) == 0
     assert _fwd(lib, ssd.ssd_conv_dims_t(2, 0, 8, 4), x=None, w=None, y=None) == 0
@@ -146,7 +150,7 @@ def grads(d, lens, silu, dy, df, keys=("x", "w", "bias", "init")):
 @pytest.mark.parametrize("case", CASES, ids=lambda c: "x".join(map(str, c[:4])) + c[4])
 def test_gradients(lib, case, dyt):
     """|g| <= 1.1 |dy| (the slope of silu), its error 64 roundings of |dy| (1 + S);
-    dx sums W of them, dweight and dbias all the tokens: 32 in a run, 8 runs,
+    dx sums W of them, dweight and dbias all the tokens: 64 in a run, 4 runs,
     then the partial rows in eight columns."""
     b, L, D, W, dt, view, init, lens, silu = case
     d = make(b, L, D, W, DT[dt], 200 + L, view, init)
@@ -164,7 +168,7 @@ def test_gradients(lib, case, dyt):
     dxb = sum(wa[:, k] * ahead[:, W - 1 - k:W - 1 - k + L] for k in range(W))
     R.within("dx", g["dx"], ref["x"], 64 * R.U * (dxb + 8))
     rows = -(-L // 256) * b
-    steps = 64 + 32 + 8 + rows / 8 + 8
+    steps = 64 + 64 + 4 + rows / 8 + 8
     back = torch.cat((z if d["init"] is None else R.f64(d["init"]).abs(), xa), 1)
     dwb = torch.stack([(big * back[:, k:k + L]).sum((0, 1)) for k in range(W)], 1)
     R.within("dweight", g["dweight"], ref["w"], steps * R.U * dwb)
