@@ -641,10 +641,11 @@ def _view(name, t, shape, dtype, device, lead=2):
     return t.data_ptr(), strides[0], strides[1] if lead == 2 else 0
 
 
-def _workspace(workspace, need, device):
-    """The caller's workspace, or one of ``need`` bytes."""
+def _workspace(workspace, need, like):
+    """The caller's workspace, or one of ``need`` bytes on the device of ``like``."""
+    device = like.device
     if workspace is None:
-        workspace = torch.empty(max(need, 16), device=device, dtype=torch.uint8)
+        workspace = like.new_empty(max(need, 16), dtype=torch.uint8)
     elif not workspace.is_contiguous() or workspace.device != device:
         raise ValueError(f"workspace: must be contiguous and on {device}")
     return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
@@ -711,11 +712,10 @@ def ssd_causal_conv_bwd(x, weight, bias, dy, init_state=None, dfinal_state=None,
     pdy = _dense("dy", dy, (b, L, D), f32 if dy.dtype == f32 else T, dev)
     pdf = _dense("dfinal_state", dfinal_state, (b, W - 1, D), T, dev)
     with _scope(_device_of(x), stream) as st:
-        out = {"dx": torch.empty((b, L, D), device=dev, dtype=T),
-               "dweight": torch.empty((D, W), device=dev, dtype=f32),
-               "dbias": torch.empty((D,), device=dev, dtype=f32),
-               "dinit": torch.empty((b, W - 1, D), device=dev, dtype=T) if want_dinit else None}
-        workspace, pws, nws = _workspace(workspace, ssd_causal_conv_bwd_workspace_size(dims, T), dev)
+        out = {"dx": x.new_empty((b, L, D)), "dweight": weight.new_empty((D, W)),
+               "dbias": weight.new_empty((D,)),
+               "dinit": x.new_empty((b, W - 1, D)) if want_dinit else None}
+        workspace, pws, nws = _workspace(workspace, ssd_causal_conv_bwd_workspace_size(dims, T), x)
         _check(load().ssd_causal_conv_bwd(
             px, sx, pw, pb, pi, pl, int(silu), pdy, int(dy.dtype == f32), pdf,
             out["dx"].data_ptr(), out["dweight"].data_ptr(), out["dbias"].data_ptr(),
@@ -801,12 +801,12 @@ def ssd_selective_scan_fwd(x, dt, A, B, C, D=None, z=None, dt_bias=None, softplu
             y = x.new_empty((b, L, ch))
             py = y.data_ptr()
         if return_final_states and final_states is None:
-            final_states = torch.empty((b, ch, N), device=dev, dtype=f32)
+            final_states = A.new_empty((b, ch, N))
             pf = final_states.data_ptr()
         need = ssd_selective_scan_fwd_workspace_size(dims, T)
         pws, nws = None, 0
         if need or workspace is not None:
-            workspace, pws, nws = _workspace(workspace, need, dev)
+            workspace, pws, nws = _workspace(workspace, need, x)
         _check(load().ssd_selective_scan_fwd(*args, pi, pl, py, pf, strides, dims, code, pws, nws,
                                              st), "ssd_selective_scan_fwd")
     return (y, final_states) if final_states is not None else y
@@ -834,15 +834,14 @@ def ssd_selective_scan_bwd(x, dt, A, B, C, D, dy, z=None, dt_bias=None, softplus
     pdy = _dense("dy", dy, (b, L, ch), T, dev)
     pdf = _dense("dfinal_states", dfinal_states, (b, ch, N), f32, dev)
     with _scope(_device_of(x), stream) as st:
-        new = lambda shape, t, want=True: (torch.empty(shape, device=dev, dtype=t)    # noqa: E731
-                                           if want else None)
-        out = {"dx": new(x.shape, T), "ddt": new(x.shape, T), "dA": new(A.shape, f32),
-               "dB": new(B.shape, T), "dC": new(C.shape, T), "dD": new((ch,), f32, D is not None),
-               "dz": new(x.shape, T, z is not None),
-               "ddt_bias": new((ch,), f32, dt_bias is not None),
-               "dinit": new((b, ch, N), f32, want_dinit)}
+        new, par = x.new_empty, A.new_empty
+        out = {"dx": new(x.shape), "ddt": new(x.shape), "dA": par(A.shape), "dB": new(B.shape),
+               "dC": new(C.shape), "dD": par((ch,)) if D is not None else None,
+               "dz": new(x.shape) if z is not None else None,
+               "ddt_bias": par((ch,)) if dt_bias is not None else None,
+               "dinit": par((b, ch, N)) if want_dinit else None}
         workspace, pws, nws = _workspace(workspace,
-                                         ssd_selective_scan_bwd_workspace_size(dims, T), dev)
+                                         ssd_selective_scan_bwd_workspace_size(dims, T), x)
         _check(load().ssd_selective_scan_bwd(*args, pi, pl, pdy, pdf,
                                              *(None if v is None else v.data_ptr()
                                                for v in out.values()),
@@ -931,12 +930,10 @@ def ssd_bc_norm_rotate_bwd(B, C, B_weight, C_weight, positions, freq, dB_out, dC
     gB = _dense("dB_out", dB_out, tuple(B.shape), gt, dev)
     gC = _dense("dC_out", dC_out, tuple(B.shape), gt, dev)
     with _scope(_device_of(B), stream) as st:
-        out = {"dB": torch.empty(B.shape, device=dev, dtype=B.dtype),
-               "dC": torch.empty(B.shape, device=dev, dtype=B.dtype),
-               "dwB": torch.empty(shape, device=dev, dtype=f32),
-               "dwC": torch.empty(shape, device=dev, dtype=f32)}
+        out = {"dB": B.new_empty(B.shape), "dC": B.new_empty(B.shape),
+               "dwB": B_weight.new_empty(shape), "dwC": B_weight.new_empty(shape)}
         workspace, pws, nws = _workspace(workspace,
-                                         ssd_bc_norm_rotate_bwd_workspace_size(dims, B.dtype), dev)
+                                         ssd_bc_norm_rotate_bwd_workspace_size(dims, B.dtype), B)
         _check(load().ssd_bc_norm_rotate_bwd(*args, gB, gC, int(gt == f32),
                                              *(v.data_ptr() for v in out.values()), dims, code,
                                              pws, nws, st), "ssd_bc_norm_rotate_bwd")
