@@ -16,6 +16,11 @@
 // keeps to one row index (B or C, one group), so that the weights, and in the
 // backward their gradients' sums, stay in registers over all its tokens.
 //
+// 4 x 8192 tokens of 8 groups, N = 128, 64 elements turned, bf16: 53 us, 269 MB at
+// 5.0 TB/s (77% of a plain copy's rate), the issue slots 67% busy: conversions,
+// norm and turn are about 130 instructions a lane and eight elements.  Gradients
+// (8 x 2048 tokens, fp32 in, all turned): 60 us, and 6 us for the weights' sums.
+//
 // Far positions: pos * freq is wanted modulo 2 pi, where the product's integer
 // part is useless.  freq / (2 pi) is taken as a 64-bit fixed-point fraction of
 // a turn, and pos times it modulo 2^64 is one exact integer product: its error

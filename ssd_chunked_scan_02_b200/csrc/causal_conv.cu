@@ -14,6 +14,11 @@
 // shared memory, each thread its own rows (no barrier), run 12 rows ahead
 // without a register; rows that cannot be copied 8 bytes at a time (odd widths or
 // views) are loaded as they are needed.
+//
+// 4 x 8192 x 5376 in bf16 (W = 4, SiLU): forward 132 us, 704 MB at 5.3 TB/s (81%
+// of a plain copy's rate); gradients 229 us, 1057 MB at 4.6 TB/s, and 6 us for the
+// sum of the partial rows.  Loads held in registers instead of the ring took 156
+// and 465 us (too few rows under way, then too many registers).
 #include <cuda_bf16.h>
 
 #include "common.cuh"

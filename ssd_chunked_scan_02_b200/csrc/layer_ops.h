@@ -43,7 +43,7 @@ struct SelectiveArgs {
 size_t selective_fwd_workspace_bytes(const SelectiveDims& d, Elt t);
 cudaError_t launch_selective_fwd(const SelectiveArgs& a, void* y, float* final_states, float* ws,
                                  const SelectiveDims& d, Elt t, cudaStream_t s);
-// The states before every TS-th token, ckpt (b, ceil(L / TS), D, padded N) (ws: as
+// The states before every kTS-th token, ckpt (b, ceil(L / TS), D, padded N) (ws: as
 // the forward's).
 cudaError_t launch_selective_checkpoints(const SelectiveArgs& a, float* ckpt, float* ws,
                                          const SelectiveDims& d, Elt t, cudaStream_t s);

@@ -71,7 +71,7 @@ __device__ __forceinline__ void fold(float* v, int lane) {
 }
 
 // Tokens whose states the backward holds in registers at once; the states before
-// every TS-th token are its checkpoints.
+// every kTS-th token are its checkpoints.
 constexpr int kTS = 4;
 
 // Layout of (channel, state) over a block of 128 threads: LPC lanes a channel,
