@@ -210,3 +210,45 @@ def test_selective_path_ragged_prompts_then_tokens_from_a_graph(lib):
         graph.replay()
         close(f"token {t}", out, torch.stack([ry[i][m + t] for i, m in enumerate(lens)]))
     close("states", h, rh)
+
+
+@pytest.mark.gpu
+def test_offsets_beyond_32_bits(lib):
+    """A sequence of more than 2^31 elements: its last rows against a call on them
+    alone (the convolution bit for bit; the scan's spans differ, so that its bf16
+    results are one rounding apart at most, 2^-7 of the value with what fp32 adds:
+    its few hundred roundings stay below 2^-14 of the largest element)."""
+    L, D, cut = (1 << 20) + 8, 2056, 600
+    assert L * D > 1 << 31
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.empty(1, L, D, device="cuda", dtype=torch.bfloat16).normal_(generator=g)
+    w, b = torch.randn(D, 4, device="cuda", generator=g), torch.randn(D, device="cuda", generator=g)
+    y = ssd.ssd_causal_conv_fwd(x, w, b)
+    part = ssd.ssd_causal_conv_fwd(x[:, L - cut:], w, b,
+                                   init_state=x[:, L - cut - 3:L - cut].contiguous())
+    assert torch.equal(y[:, L - cut:], part)
+    del y
+
+    A = -torch.rand(D, 16, device="cuda", generator=g) * 8
+    bc = torch.randn(1, L, 1, 32, device="cuda", generator=g).bfloat16()
+    args = lambda s: (x[:, s], x[:, s], A, bc[:, s, :, :16], bc[:, s, :, 16:])   # noqa: E731
+    bias = torch.full((D,), -4.0, device="cuda")
+    y, h = ssd.ssd_selective_scan_fwd(*args(slice(None)), dt_bias=bias, return_final_states=True)
+    _, before = ssd.ssd_selective_scan_fwd(*args(slice(0, L - cut)), dt_bias=bias,
+                                           return_final_states=True)
+    part, hp = ssd.ssd_selective_scan_fwd(*args(slice(L - cut, None)), dt_bias=bias,
+                                          init_states=before, return_final_states=True)
+    whole, part = y[0, L - cut:].double(), part[0].double()
+    assert ((whole - part).abs() <= 2.0 ** -7 * part.abs() + 2.0 ** -14 * part.abs().max()).all()
+    assert float((h - hp).abs().max()) <= 2.0 ** -14 * float(hp.abs().max())
+    del y, whole, part
+
+    rows = x.view(1, -1)[:, :(1 << 31) + 4096].view(1, -1, 2, 64)     # more than 2^31 elements of B
+    C, L = rows, rows.shape[1]
+    pos = torch.arange(L, device="cuda")[None]
+    freq = 10000.0 ** (-torch.arange(0, 64, 2, device="cuda") / 64)
+    one = torch.ones(64, device="cuda")
+    B1, C1 = ssd.ssd_bc_norm_rotate_fwd(rows, C, one, one, pos, freq)
+    B2, C2 = ssd.ssd_bc_norm_rotate_fwd(rows[:, L - 100:], C[:, L - 100:], one, one,
+                                        pos[:, L - 100:].contiguous(), freq)
+    assert torch.equal(B1[:, L - 100:], B2) and torch.equal(C1[:, L - 100:], C2)
