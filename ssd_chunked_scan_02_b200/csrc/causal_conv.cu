@@ -15,8 +15,8 @@
 // without a register; rows that cannot be copied 8 bytes at a time (odd widths or
 // views) are loaded as they are needed.
 //
-// 4 x 8192 x 5376 in bf16 (W = 4, SiLU): forward 132 us, 704 MB at 5.3 TB/s (81%
-// of a plain copy's rate); gradients 229 us, 1057 MB at 4.6 TB/s, and 6 us for the
+// 4 x 8192 x 5376 in bf16 (W = 4, SiLU): forward 126 us, 704 MB at 5.6 TB/s (85%
+// of a plain copy's rate); gradients 228 us, 1057 MB at 4.6 TB/s, and 6 us for the
 // sum of the partial rows.  Loads held in registers instead of the ring took 156
 // and 465 us (too few rows under way, then too many registers).
 #include <cuda_bf16.h>
@@ -552,10 +552,11 @@ template <typename T, int V, int W>
 void fwd_v(const void* x, Stride xs, const float* w, const float* bias, const void* init,
            const int32_t* lens, bool silu, void* y, void* fin, const ConvDims& d,
            cudaStream_t s) {
-    // 32-token runs read 9% of the rows twice at W = 4; where those are too few
-    // threads for 148 SMs, shorter runs spread the tokens over more of them
+    // 64-token runs read 5% of the rows twice at W = 4 (runs of 32: 358 instead of
+    // 353 us for the convolution and its gradients at 4 x 8192 x 5376); where those
+    // are too few threads for 148 SMs, shorter runs spread the tokens over more
     const int64_t nvec = d.D / V;
-    int64_t run = 32;
+    int64_t run = 64;
     while (run > 8 && d.b * nvec * ((d.L + run - 1) / run) < 148 * 1024) run /= 2;
     const int64_t nrun = d.L > 0 ? (d.L + run - 1) / run : 1;
     const int64_t items = d.b * nvec * nrun;
