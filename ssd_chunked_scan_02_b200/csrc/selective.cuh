@@ -39,6 +39,10 @@ __device__ __forceinline__ float softplus_f32(float v) {
 // instruction (the gradient of A over 2048 tokens: 1.9e-6 off without, 1.0e-6 with).  2^(the shift)
 // alone is 1: a step of length zero leaves the state as it is.
 constexpr float kDecayShift = 2.9e-8f;
+// A parameter's A as the kernels hold it: -inf (a state that forgets at once) as the
+// lowest finite value, whose product with the dt = 0 of rows behind a sequence is 0
+// and not NaN, and with any dt above 1e-36 decays to 0 just the same.  NaN stays.
+__device__ __forceinline__ float decay_rate(float A) { return A < -3.4028234e38f ? -3.4028234e38f : A; }
 __device__ __forceinline__ float decay(float dl, float A) { return ex2(fmaf(dl, A, kDecayShift)); }
 __device__ __forceinline__ F2 decay2(F2 dl, F2 A) {
     return ex2_2(fma2(dl, A, pack2(kDecayShift, kDecayShift)));

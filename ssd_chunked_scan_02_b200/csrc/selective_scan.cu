@@ -121,7 +121,7 @@ scan_fwd_kernel(const SelectiveArgs a, T* __restrict__ y, float* __restrict__ fi
             for (int i = 0; i < SPL; ++i) {
                 const int n = lane * SPL + i;
                 const bool on = ch < pl.count && n < d.N;
-                av[i] = on ? a.A[(pl.c0 + ch) * d.N + n] : 0.f;
+                av[i] = on ? decay_rate(a.A[(pl.c0 + ch) * d.N + n]) : 0.f;
                 hv[i] = on && !Sum && a.init ? a.init[row * d.N + n] : 0.f;
             }
             if (!Sum && ch < pl.count) {
@@ -459,6 +459,8 @@ step_kernel(float* __restrict__ state, const SelectiveArgs a, T* __restrict__ y,
 #pragma unroll
             for (int i = 0; i < 4; ++i) As[i] = n + i < N ? Ar[n + i] : 0.f;
         }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) As[i] = decay_rate(As[i]);
     };
     load(lane * 4);
 

@@ -135,7 +135,7 @@ scan_bwd_kernel(const SelectiveArgs a, const SelectiveGrads gr, const float* __r
         for (int i = 0; i < SPL; ++i) {
             const int n = lane * SPL + i;
             const bool on = ch < pl.count && n < d.N;
-            av[i] = on ? a.A[(pl.c0 + ch) * d.N + n] : 0.f;
+            av[i] = on ? decay_rate(a.A[(pl.c0 + ch) * d.N + n]) : 0.f;
             gv[i] = on && !Carry && gr.dfinal ? gr.dfinal[row * d.N + n] : 0.f;
         }
         if (!Carry && ch < pl.count) {

@@ -345,3 +345,26 @@ def test_spans(lib, c):
         if of in leaf:
             want = ref[of] if ref[of] is not None else torch.zeros_like(leaf[of])
             R.within(k, g[k], want, bound[k])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("c", [CASES[2], CASES[3], CASES[8], Case(1, 700, 24, 16, lens=[650])], ids=repr)
+def test_states_that_forget_at_once(lib, c):
+    # exp(dt A) is 0 for A = -inf as for A = -1e30 (dt > 1e-28), also where the rows
+    # behind a sequence have a step of zero: the same bits, nothing of it NaN
+    d, m = make(c, 2000)
+    some = torch.rand(c.ch, c.N, generator=m["gen"]).cuda() < 0.3
+    dy = torch.randn(c.b, c.L, c.ch, generator=m["gen"]).to(DT[c.dt]).cuda()
+    got = []
+    for low in (-float("inf"), -1e30):
+        e = d | dict(A=torch.where(some, low, d["A"]))
+        y, f = ssd.ssd_selective_scan_fwd(**e, init_states=m["init"], seq_lens=m["lens_t"],
+                                          return_final_states=True)
+        g = ssd.ssd_selective_scan_bwd(**e, dy=dy, init_states=m["init"], seq_lens=m["lens_t"])
+        t = {k: e[k] if e[k] is None or k in ("A", "D", "dt_bias") else e[k][:, 0]
+             for k in ("x", "dt", "A", "B", "C", "D", "z", "dt_bias")}
+        state = f.clone()
+        yt = ssd.ssd_selective_step(state, **t)
+        got.append([y, f, state, yt] + [v for _, v in sorted(g.items()) if v is not None])
+    for a, b in zip(*got):
+        assert torch.isfinite(a).all() and torch.equal(a, b)
