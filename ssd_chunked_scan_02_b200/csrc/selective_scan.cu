@@ -24,8 +24,8 @@
 // themselves take 158 us, the carriers by themselves 128.  Holding the loads in
 // registers (220 us), both jobs in one kind of warp (259 us; with half the registers
 // and more blocks no faster than this either, 361 against 360 us at 4 x 2048 x
-// 5120) and exponentials computed a step ahead of the recurrence (no change) were
-// tried.
+// 5120), exponentials computed a step ahead of the recurrence (no change) and eight
+// or sixteen states a lane with two or one walking warps (210 and 272 us) were tried.
 //
 // Where batch and channels are too few blocks for the GPU, a sequence is cut
 // into spans (blockIdx.y).  A first launch walks all spans but the last from a
@@ -549,8 +549,8 @@ template bool selective_vec<__nv_bfloat16>(const SelectiveArgs&, const Selective
 // Spans of a sequence: one where the blocks of (batch, channels) are two for each
 // of 148 SMs or more; else as many as give every SM what it holds (three blocks in
 // bf16, two in fp32), of at least two tiles.  Below three spans the second walk
-// over the tokens costs what the first gains.  (1 x 32768 x 1536, 9 spans: 628 us;
-// 6 spans 672, 12 spans 662, one 2300.)
+// over the tokens costs what the first gains.  (1 x 32768 x 1536, 9 spans: 608 us;
+// 6 spans 631, 12 spans 630, 18 spans 602, one 1471.)
 Spans selective_spans(const SelectiveDims& d, Elt t, float* ws) {
     Spans sp{1, d.L, nullptr, nullptr};
     with_layout(d.N, [&](auto lay) {
