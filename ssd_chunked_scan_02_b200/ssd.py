@@ -641,6 +641,11 @@ def _view(name, t, shape, dtype, device, lead=2):
     return t.data_ptr(), strides[0], strides[1] if lead == 2 else 0
 
 
+def _out_like(t):
+    """A dense output of t's shape (the cheapest way to ask for one)."""
+    return torch.empty_like(t, memory_format=torch.contiguous_format)
+
+
 def _workspace(workspace, need, like):
     """The caller's workspace, or one of ``need`` bytes on the device of ``like``."""
     device = like.device
@@ -678,7 +683,7 @@ def ssd_causal_conv_fwd(x, weight, bias=None, init_state=None, seq_lens=None, si
     pf = _dense("final_state", final_state, (b, W - 1, D), T, dev)
     with _scope(_device_of(x), stream) as st:
         if y is None:
-            y = x.new_empty((b, L, D))
+            y = _out_like(x)
             py = y.data_ptr()
         if return_final_state and final_state is None:
             final_state = x.new_empty((b, W - 1, D))
@@ -712,7 +717,7 @@ def ssd_causal_conv_bwd(x, weight, bias, dy, init_state=None, dfinal_state=None,
     pdy = _dense("dy", dy, (b, L, D), f32 if dy.dtype == f32 else T, dev)
     pdf = _dense("dfinal_state", dfinal_state, (b, W - 1, D), T, dev)
     with _scope(_device_of(x), stream) as st:
-        out = {"dx": x.new_empty((b, L, D)), "dweight": weight.new_empty((D, W)),
+        out = {"dx": _out_like(x), "dweight": weight.new_empty((D, W)),
                "dbias": weight.new_empty((D,)),
                "dinit": x.new_empty((b, W - 1, D)) if want_dinit else None}
         workspace, pws, nws = _workspace(workspace, ssd_causal_conv_bwd_workspace_size(dims, T), x)
@@ -741,7 +746,7 @@ def ssd_causal_conv_step(state, x, weight, bias=None, silu: bool = True, y=None,
     py = _dense("y", y, (b, D), T, dev)
     with _scope(_device_of(x), stream) as st:
         if y is None:
-            y = x.new_empty((b, D))
+            y = _out_like(x)
             py = y.data_ptr()
         _check(load().ssd_causal_conv_step(ps, px, sx, pw, pb, int(silu), py,
                                            ssd_conv_dims_t(b, 1, D, W), code, st),
@@ -798,7 +803,7 @@ def ssd_selective_scan_fwd(x, dt, A, B, C, D=None, z=None, dt_bias=None, softplu
     pf = _dense("final_states", final_states, (b, ch, N), f32, dev)
     with _scope(_device_of(x), stream) as st:
         if y is None:
-            y = x.new_empty((b, L, ch))
+            y = _out_like(x)
             py = y.data_ptr()
         if return_final_states and final_states is None:
             final_states = A.new_empty((b, ch, N))
@@ -861,7 +866,7 @@ def ssd_selective_step(state, x, dt, A, B, C, D=None, z=None, dt_bias=None, soft
     py = _dense("y", y, (b, ch), x.dtype, dev)
     with _scope(_device_of(x), stream) as st:
         if y is None:
-            y = x.new_empty((b, ch))
+            y = _out_like(x)
             py = y.data_ptr()
         _check(load().ssd_selective_step(ps, *args, py, strides, dims, code, st),
                "ssd_selective_step")
@@ -900,10 +905,10 @@ def ssd_bc_norm_rotate_fwd(B, C, B_weight, C_weight, positions, freq, eps: float
     oC = _dense("C_out", C_out, tuple(B.shape), B.dtype, dev)
     with _scope(_device_of(B), stream) as st:
         if B_out is None:
-            B_out = B.new_empty(B.shape)
+            B_out = _out_like(B)
             oB = B_out.data_ptr()
         if C_out is None:
-            C_out = B.new_empty(B.shape)
+            C_out = _out_like(B)
             oC = C_out.data_ptr()
         _check(load().ssd_bc_norm_rotate_fwd(*args, oB, oC, dims, code, st),
                "ssd_bc_norm_rotate_fwd")
@@ -930,7 +935,7 @@ def ssd_bc_norm_rotate_bwd(B, C, B_weight, C_weight, positions, freq, dB_out, dC
     gB = _dense("dB_out", dB_out, tuple(B.shape), gt, dev)
     gC = _dense("dC_out", dC_out, tuple(B.shape), gt, dev)
     with _scope(_device_of(B), stream) as st:
-        out = {"dB": B.new_empty(B.shape), "dC": B.new_empty(B.shape),
+        out = {"dB": _out_like(B), "dC": _out_like(B),
                "dwB": B_weight.new_empty(shape), "dwC": B_weight.new_empty(shape)}
         workspace, pws, nws = _workspace(workspace,
                                          ssd_bc_norm_rotate_bwd_workspace_size(dims, B.dtype), B)
