@@ -12,8 +12,7 @@
 // rows before a run are read twice, and those come from L2.  What keeps the
 // memory busy is the number of rows under way: asynchronous copies into a ring in
 // shared memory, each thread its own rows (no barrier), run 12 rows ahead
-// without a register; rows that cannot be copied 8 bytes at a time (odd widths or
-// views) are loaded as they are needed.
+// without a register.
 //
 // 4 x 8192 x 5376 in bf16 (W = 4, SiLU): forward 126 us, 704 MB at 5.6 TB/s (85%
 // of a plain copy's rate); gradients 228 us, 1057 MB at 4.6 TB/s, and 6 us for the
@@ -165,34 +164,49 @@ __device__ __forceinline__ Raw<T, V> load_row(const T* x, int64_t token_stride, 
     return init ? raw_load<T, V>(init + (W - 1 + t) * D) : raw_zero<T, V>();
 }
 
-// A thread's rows on their way through shared memory, in groups of kGroup: rows(g)
-// are asked for kAhead groups before they are taken.
+// A thread's rows on their way through shared memory, in groups of kGroup: a group
+// is asked for kAhead groups before it is taken.  Rows of two bytes a thread (bf16 of
+// odd width or view) are too small for an asynchronous copy: the gradients hold a
+// group in registers until the next is asked for (6 x 2048 x 1001: 89 -> 69 us for
+// both), the forward, with more threads an SM, loads them as they are needed (18 us;
+// 22 with held groups).
 constexpr int kGroup = 4, kAhead = 3, kRing = kGroup * (kAhead + 1);
 
-template <typename T, int V, int THREADS>
+template <typename T, int V, int THREADS, bool HOLD>
 struct Rows {
-    static constexpr bool kAsync = sizeof(T) * V >= 8;
-    static constexpr int kBytes = kAsync ? kRing * THREADS * V * (int)sizeof(T) : 0;
+    static constexpr bool kAsync = sizeof(T) * V >= 4, kRinged = kAsync || HOLD;
+    static constexpr int kBytes = kRinged ? kRing * THREADS * V * (int)sizeof(T) : 0;
     Raw<T, V>* ring;                  // [kRing][THREADS], this thread's column
     const T* p;                       // the next row to ask for
     int64_t step;
+    Raw<T, V> held[kGroup];           // HOLD, not kAsync: the group asked for last
     __device__ __forceinline__ Rows(unsigned char* smem, int tid, const T* from, int64_t stride)
-        : ring(reinterpret_cast<Raw<T, V>*>(smem) + tid), p(from), step(stride) {}
-    // asks for the rows of group g that are below n
+        : ring(reinterpret_cast<Raw<T, V>*>(smem) + tid), p(from), step(stride) {
+#pragma unroll
+        for (int u = 0; u < kGroup; ++u) held[u] = raw_zero<T, V>();
+    }
+    __device__ __forceinline__ Raw<T, V>* place(int r) { return ring + r % kRing * THREADS; }
+    // asks for the rows of group g (0, 1, ... in turn) that are below n
     __device__ __forceinline__ void ask(int g, int n) {
-        if constexpr (kAsync) {
+        if constexpr (kRinged) {
+            if (!kAsync && g > 0) {
+#pragma unroll
+                for (int u = 0; u < kGroup; ++u) *place((g - 1) * kGroup + u) = held[u];
+            }
 #pragma unroll
             for (int u = 0; u < kGroup; ++u) {
-                if (g * kGroup + u < n)
-                    copy_async(ring + (g * kGroup + u) % kRing * THREADS, p, true);
+                if (g * kGroup + u < n) {
+                    if constexpr (kAsync) copy_async(place(g * kGroup + u), p, true);
+                    else held[u] = raw_load<T, V>(p);
+                }
                 p += step;
             }
         }
     }
     // row r, whose group has arrived (or is loaded now)
     __device__ __forceinline__ Raw<T, V> take(int r) {
-        if constexpr (kAsync) {
-            return ring[r % kRing * THREADS];
+        if constexpr (kRinged) {
+            return *place(r);
         } else {
             const Raw<T, V> v = raw_load<T, V>(p);
             p += step;
@@ -223,8 +237,8 @@ conv_fwd_kernel(const T* __restrict__ x, Stride xs, const float* __restrict__ w,
     const int64_t te = t1 < len ? t1 : len;          // tokens of the sequence itself
     y += t0 * D;
     int left = (int)(t1 - t0), live = (int)(te - t0);
-    __shared__ __align__(16) unsigned char ring[Rows<T, V, kThreads>::kBytes + 16];
-    Rows<T, V, kThreads> rows(ring, threadIdx.x, x + t0 * xs.token, xs.token);
+    __shared__ __align__(16) unsigned char ring[Rows<T, V, kThreads, false>::kBytes + 16];
+    Rows<T, V, kThreads, false> rows(ring, threadIdx.x, x + t0 * xs.token, xs.token);
     for (int g = 0; g < kAhead; ++g) {
         rows.ask(g, live);
         copies_commit();
@@ -331,8 +345,8 @@ conv_bwd_kernel(const T* __restrict__ x, Stride xs, const float* __restrict__ w,
             const int ahead = (int)(len - s1 < W - 1 ? len - s1 : W - 1);   // tokens behind with a g
             const int rows = todo + ahead;
             constexpr int kAll = 32 * kSlots;
-            Rows<T, V, kAll> rx(ring, slot * 32 + lane, x + t0 * xs.token, xs.token);
-            Rows<TG, V, kAll> rg(ring + Rows<T, V, kAll>::kBytes, slot * 32 + lane, dy, D);
+            Rows<T, V, kAll, true> rx(ring, slot * 32 + lane, x + t0 * xs.token, xs.token);
+            Rows<TG, V, kAll, true> rg(ring + Rows<T, V, kAll, true>::kBytes, slot * 32 + lane, dy, D);
             auto ask = [&](int g) {
                 rx.ask(g, rows);
                 rg.ask(g, rows);
@@ -582,7 +596,7 @@ cudaError_t bwd_v(const void* x, Stride xs, const float* w, const float* bias, c
            float* dw, float* dbias, void* dinit, float* ws, const ConvDims& d, cudaStream_t s) {
     const int64_t ncb = (d.D / V + 31) / 32, nt = bwd_tiles(d);
     if (d.b > 0 && d.L > 0) {
-        constexpr int rows = Rows<T, V, 32 * kSlots>::kBytes + Rows<TG, V, 32 * kSlots>::kBytes,
+        constexpr int rows = Rows<T, V, 32 * kSlots, true>::kBytes + Rows<TG, V, 32 * kSlots, true>::kBytes,
                       sums = kSlots * (W + 1) * V * 32 * 4, smem = rows > sums ? rows : sums;
         if (smem > 48 * 1024) {
             const cudaError_t e = cudaFuncSetAttribute(
