@@ -71,6 +71,10 @@ scan_fwd_kernel(const SelectiveArgs a, T* __restrict__ y, float* __restrict__ fi
     // s_du's columns are permuted by the number of the load that brings them, so
     // that neither the eight lanes that store side by side nor those that read
     // meet a bank twice
+    // fp32 rows of odd widths or views are copied element by element (3 x 1825 x 1365,
+    // N = 16: 213 -> 123 us); bf16's two bytes cannot be, and are loaded in place
+    // (155 us; 170 with the loads held in registers)
+    constexpr bool Each = !Vec && sizeof(T) == 4;
     constexpr int SWZ = (CH < 8 ? CH : 8) - 1, PER = CH / VW;       // PER: loads of a token
     static_assert(8 * PER % (SWZ + 1) == 0, "the permutation repeats after eight tokens");
     extern __shared__ __align__(16) unsigned char smem[];
@@ -261,6 +265,14 @@ scan_fwd_kernel(const SelectiveArgs a, T* __restrict__ y, float* __restrict__ fi
                         copy_async(r_x + o, px[k], in);
                         copy_async(r_dt + o, pdt[k], in);
                         if (z) copy_async(r_z + o, pz[k], in);
+                    } else if constexpr (Each) {
+                        const int n = t < TT && at + t < own_rows ? pl.count - c : 0;
+#pragma unroll
+                        for (int j = 0; j < VW; ++j) {
+                            copy_async(&r_x[o].v[j], px[k] + j, j < n);
+                            copy_async(&r_dt[o].v[j], pdt[k] + j, j < n);
+                            if (z) copy_async(&r_z[o].v[j], pz[k] + j, j < n);
+                        }
                     } else {
                         const int n = t < TT && at + t < own_rows ? pl.count - c : 0;
                         r_x[o] = load_channels<T, VW>(px[k], n, false);
@@ -280,7 +292,7 @@ scan_fwd_kernel(const SelectiveArgs a, T* __restrict__ y, float* __restrict__ fi
                     }
                 }
             }
-            if constexpr (Vec) copies_commit();
+            if constexpr (Vec || Each) copies_commit();
         };
         float sum_dt[NI][VW];
 #pragma unroll
@@ -291,7 +303,7 @@ scan_fwd_kernel(const SelectiveArgs a, T* __restrict__ y, float* __restrict__ fi
         auto stage = [&](int at, int w) {
             float2* du = s_du + w * TT * CH;
             const int ring = at / TT & 3;
-            if constexpr (Vec) copies_pending<1>();                 // the tile behind may be under way
+            if constexpr (Vec || Each) copies_pending<1>();         // the tile behind may be under way
 #pragma unroll
             for (int k = 0; k < NI; ++k) {
                 const int i = k * KC + tid, t = i / PER, c = i % PER * VW, o = (ring * NI + k) * KC + tid;

@@ -78,6 +78,7 @@ scan_bwd_kernel(const SelectiveArgs a, const SelectiveGrads gr, const float* __r
     constexpr int SPL = Lay::SPL, LPC = Lay::LPC, NP = Lay::NP, CH = Lay::CH, TS = kTS;
     constexpr int TT = S::TT, VW = S::VW, PER = S::PER, IT = S::IT, VB = S::VB, NB = S::NB;
     constexpr int PY = S::PY;
+    constexpr bool Each = !Vec && sizeof(T) == 4;               // copied element by element
     constexpr int CPW = 32 / LPC;                               // channels of a warp
     constexpr int FG = 2;                                       // tokens of a sum over channels
     constexpr int NG = 4;                                       // tokens of a sum over states
@@ -183,17 +184,34 @@ scan_bwd_kernel(const SelectiveArgs a, const SelectiveGrads gr, const float* __r
                                        : Cp + (int64_t)r * Ct_ + (v - nvb) * VB, in);
             }
             copies_commit();
+        } else if constexpr (Each) {
+#pragma unroll
+            for (int k = 0; k < IT; ++k) {
+                const int i = k * kThreads + tid, t = t0 + i / PER, c = i % PER * VW;
+                const int o = (w * IT + k) * kThreads + tid;
+                const int n = i / PER < TT && t < own ? pl.count - c : 0;
+                const int r = n > 0 ? t : 0, cc = n > 0 ? c : 0;
+#pragma unroll
+                for (int j = 0; j < VW; ++j) {
+                    const int e = j < n ? cc + j : 0;
+                    copy_async(&r_x[o].v[j], x + (int64_t)r * xt + e, j < n);
+                    copy_async(&r_dt[o].v[j], dt + (int64_t)r * dtt + e, j < n);
+                    copy_async(&r_dy[o].v[j], dy + (int64_t)r * Dt + e, j < n);
+                    if (z) copy_async(&r_z[o].v[j], z + (int64_t)r * zt + e, j < n);
+                }
+            }
+            copies_commit();
         }
     };
     auto stage = [&](int t0, int w) {
-        if constexpr (Vec) copies_pending<0>();
+        if constexpr (Vec || Each) copies_pending<0>();
 #pragma unroll
         for (int k = 0; k < IT; ++k) {
             const int i = k * kThreads + tid, tl = i / PER, t = t0 + tl, c = i % PER * VW;
             const int o = (w * IT + k) * kThreads + tid;
             if (tl >= TT) continue;
             const int n = t < own ? pl.count - c : 0;
-            if constexpr (!Vec) {
+            if constexpr (!Vec && !Each) {
                 r_x[o] = load_channels<T, VW>(x + (int64_t)t * a.xs.token + c, n, false);
                 r_dt[o] = load_channels<T, VW>(dt + (int64_t)t * a.dts.token + c, n, false);
                 r_dy[o] = load_channels<T, VW>(dy + (int64_t)t * Dt + c, n, false);

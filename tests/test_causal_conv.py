@@ -119,6 +119,8 @@ CASES = [  # b, L, D, W, dtype, view, init, lens, silu
     (2, 520, 24, 2, "f32", 0, True, [257, 256], True),
     (1, 130, 21, 4, "f32", 2, True, None, False),
     (2, 40, 12, 3, "f32", 4, False, [-5, 3], True),        # a negative length: empty
+    (2, 300, 33, 4, "bf16", 3, True, [300, 131], True),    # odd, several runs
+    (2, 300, 33, 3, "f32", 1, True, [299, 64], True),
 ]
 DT = {"bf16": torch.bfloat16, "f32": torch.float32}
 

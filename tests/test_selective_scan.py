@@ -111,6 +111,8 @@ CASES = [
     Case(2, 300, 8, 1, skip=False),
     Case(15, 19, 960, 16, init=False),                 # more blocks than 148 SMs hold at once
     Case(4, 37, 500, 5, G=125, dt="f32", lens=[37, 36, 0, 17]),
+    Case(2, 145, 33, 16, dt="f32", view=3, lens=[140, 3]),   # odd slices, element by element
+    Case(3, 67, 41, 24, dt="f32", view=1, gate=False),
 ]
 
 
