@@ -307,7 +307,10 @@ norm_rotate_kernel(const Args a) {
                     sq2 = fma2(v2[k], v2[k], sq2);
                 }
                 const float2 sq = unpack2(sq2);
-                const float r = rsqrtf(unit_sum<LANES>(sq.x + sq.y, lanes) * inv_n + a.eps);
+                // (a place without a row has no norm: eps may be 0, and 1 / 0 times its
+                // zeros would reach the weights' gradients)
+                const float mean = unit_sum<LANES>(sq.x + sq.y, lanes) * inv_n;
+                const float r = !Bwd || live ? rsqrtf(mean + a.eps) : 0.f;
                 const F2 rr = pack2(r, r);
                 auto turn_by = [&](float (&u)[8], float sign) {
                     if (!turned || !live) return;

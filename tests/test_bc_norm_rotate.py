@@ -229,3 +229,37 @@ def test_streams_graphs_repeats_and_no_tokens(lib):
     B, C = ssd.ssd_bc_norm_rotate_fwd(*args(e))
     g = ssd.ssd_bc_norm_rotate_bwd(*args(e), B, C)
     assert B.shape == (2, 0, 4, 64) and not g["dwB"].any() and not g["dwC"].any()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("case", [
+    (1, 1, 1, 128, 128, "bf16", False, False, 0, "near"),   # one token: eight places, one taken
+    (2, 5, 1, 128, 64, "bf16", True, False, 0, "near"),
+    (8, 2048, 1, 128, 128, "bf16", False, False, 0, "near"),  # tiles of 28 tokens in eight places
+    (3, 33, 5, 64, 64, "f32", True, True, 8, "near"),
+    (2, 9, 2, 33, 30, "bf16", False, True, 0, "near"),      # element by element
+    (1, 40, 16, 128, 0, "bf16", False, True, 0, "near"),    # every place taken
+], ids=lambda c: "x".join(map(str, c[:5])) + c[5])
+def test_no_epsilon(lib, case):
+    """eps = 0 is the plain norm.  Places of a tile that hold no token (the last
+    tokens of a tile, a single token of one group) have no norm and must not
+    reach the weights' gradients.  Bounds: test_forward's and test_gradients'."""
+    b, L, G, N, Rr, dt, inter, per, view, where = case
+    d = make(case, 70)
+    gB, gC = (torch.randn(b, L, G, N, generator=d["gen"]).cuda() for _ in range(2))
+    out = ssd.ssd_bc_norm_rotate_fwd(*args(d), eps=0.0, interleaved=inter)
+    g = ssd.ssd_bc_norm_rotate_bwd(*args(d), gB, gC, eps=0.0, interleaved=inter)
+    for k, up, got in (("B", gB, out[0]), ("C", gC, out[1])):
+        v, w = R.f64(d[k]).requires_grad_(), R.f64(d["w" + k]).requires_grad_()
+        ref = R.norm_rotate(v, w, d["pos"].cpu(), d["freq"].cpu(), 0.0, inter)
+        rv, rw = torch.autograd.grad((ref * R.f64(up)).sum(), (v, w))
+        v, w = v.detach(), w.detach()
+        r = 1 / torch.sqrt(v.square().mean(-1, keepdim=True))
+        R.within(k, got, ref, 24 * R.U * turned_size(v * r * w, Rr, inter))
+        size = turned_size(R.f64(up), Rr, inter)
+        dd = size * w.abs()
+        M = (dd * v.abs()).mean(-1, keepdim=True) * r * r * v.abs() + dd
+        R.within("d" + k, g["d" + k], rv, 64 * R.U * r * M)
+        sums = (size * v.abs() * r).sum((0, 1) if per else (0, 1, 2))
+        steps = 48 + max(32, b * L / 592) + 128 + 592 * G / 8 + 8
+        R.within("dw" + k, g["dw" + k], rw, steps * R.U * sums)
