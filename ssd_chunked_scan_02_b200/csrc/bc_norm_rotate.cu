@@ -425,10 +425,11 @@ int lanes_of(int N) {
 }
 
 // Four blocks for each of 148 SMs, each with the same number of tiles of at most
-// 32 tokens.
+// kMaxTile tokens.
+constexpr int kMaxTile = 32;
 int tile_of(const RotateDims& d) {
     const int64_t per = (d.b * d.L + 591) / 592;         // tokens of a block
-    const int64_t tiles = (per + 31) / 32;
+    const int64_t tiles = (per + kMaxTile - 1) / kMaxTile;
     const int64_t tile = tiles > 0 ? (per + tiles - 1) / tiles : 1;
     return (int)(tile < d.L ? tile : (d.L > 0 ? d.L : 1));
 }
@@ -479,10 +480,15 @@ cudaError_t launch(Args& a, int64_t blocks, cudaStream_t s) {
     int smem = a.table_bytes + Rows<T, Vec>::kBytes + (Bwd ? Rows<TG, Vec>::kBytes : 0);
     const int acc = units / wide * wide * a.N * 4;
     if (Bwd && smem < acc) smem = acc;
+    // The limit that a kernel instance is given is the largest that any call of it
+    // needs, the same every time: other host threads launch it too.  (A block's sums,
+    // at most 2048 floats, are less than the table.)
+    constexpr int most = kMaxTile * (256 / 2) * (int)sizeof(float2) + Rows<T, Vec>::kBytes +
+                         (Bwd ? Rows<TG, Vec>::kBytes : 0);
     auto go = [&](auto kernel) {
         if (smem > 48 * 1024) {
             const cudaError_t e = cudaFuncSetAttribute(
-                kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+                kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
             if (e != cudaSuccess) return e;
         }
         kernel<<<(unsigned)blocks, kThreads, smem, s>>>(a);

@@ -8,6 +8,7 @@ and sine are off by 2^-25 pi (the angle held as a fp32 number of half turns)
 and two roundings; a turned element is a sum of two products: 24 roundings of
 |u_i| + |u_j| cover all."""
 import ctypes
+import threading
 
 import pytest
 import torch
@@ -263,3 +264,42 @@ def test_no_epsilon(lib, case):
         sums = (size * v.abs() * r).sum((0, 1) if per else (0, 1, 2))
         steps = 48 + max(32, b * L / 592) + 128 + 592 * G / 8 + 8
         R.within("dw" + k, g["dw" + k], rw, steps * R.U * sums)
+
+
+@pytest.mark.gpu
+def test_calls_from_two_threads(lib):
+    """Two host threads, a stream each, gradients that need different amounts of
+    shared memory (128 and 64 turned elements): neither's calls fail, and both give
+    what they give alone."""
+    made = []
+    for Rr in (128, 64):
+        d = make((8, 2048, 1, 128, Rr, "bf16", False, False, 0, "near"), 90 + Rr)
+        up = torch.randn(8, 2048, 1, 128, generator=d["gen"]).cuda()
+        alone = ssd.ssd_bc_norm_rotate_bwd(*args(d), up, up)
+        dims, n = ssd.ssd_rotate_dims_t(8, 2048, 1, 128, Rr), ctypes.c_size_t(0)
+        assert lib.ssd_bc_norm_rotate_bwd_workspace_size(dims, ssd.SSD_BF16, n) == 0
+        out = {k: torch.empty_like(v) for k, v in alone.items()}
+        ws = torch.empty(n.value, dtype=torch.uint8, device="cuda")
+        row = [ssd.ssd_stride_t(*d[k].stride()[:2]) for k in "BC"]
+        p = {k: d[k].data_ptr() for k in ("B", "C", "wB", "wC", "pos", "freq")}
+        call = [p["B"], row[0], p["C"], row[1], p["wB"], p["wC"], 0, p["pos"], p["freq"], 1e-5, 0,
+                up.data_ptr(), up.data_ptr(), 1, *(v.data_ptr() for v in out.values()), dims,
+                ssd.SSD_BF16, ws.data_ptr(), n.value]
+        made.append((call, torch.cuda.Stream(), alone, out, (d, up, ws)))
+    torch.cuda.synchronize()
+    start, status = threading.Barrier(2), [set(), set()]
+
+    def work(i):
+        call, stream = made[i][:2]
+        start.wait()
+        for _ in range(4000):
+            status[i].add(lib.ssd_bc_norm_rotate_bwd(*call, stream.cuda_stream))
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert status == [{ssd.SSD_OK}, {ssd.SSD_OK}]
+    for _, _, alone, out, _ in made:
+        assert all(torch.equal(alone[k], out[k]) for k in alone)
