@@ -439,8 +439,8 @@ step_kernel(float* __restrict__ state, const SelectiveArgs a, T* __restrict__ y,
     const float* Ar = a.A + (int64_t)c * N;
     float* st = state + (b0 * D + c) * N;
     const int64_t next = (int64_t)D * N;                   // the same channel of the next sequence
-    const T* Bp = static_cast<const T*>(a.B) + b0 * a.Bs.batch + g * N;
-    const T* Cp = static_cast<const T*>(a.C) + b0 * a.Cs.batch + g * N;
+    const T* Bp = static_cast<const T*>(a.B) + b0 * a.Bs.batch + (int64_t)g * N;
+    const T* Cp = static_cast<const T*>(a.C) + b0 * a.Cs.batch + (int64_t)g * N;
 
     // one round for up to 4 LANES states, two for 129 to 256
     float hs[KB][4], As[4], acc[KB];

@@ -370,3 +370,20 @@ def test_states_that_forget_at_once(lib, c):
         got.append([y, f, state, yt] + [v for _, v in sorted(g.items()) if v is not None])
     for a, b in zip(*got):
         assert torch.isfinite(a).all() and torch.equal(a, b)
+
+
+@pytest.mark.gpu
+def test_step_with_groups_beyond_32_bits(lib):
+    """A group a channel, more than 2^31 elements of B and C a sequence: the last
+    channels against a call on them alone, bit for bit."""
+    D, N, cut = (1 << 23) + 24, 256, 40
+    assert (D - 1) * N > 1 << 31
+    g = torch.Generator(device="cuda").manual_seed(2)
+    n = lambda *s: torch.empty(s, device="cuda", dtype=torch.bfloat16).normal_(generator=g)   # noqa: E731
+    bc, x, dt = n(1, D, N), n(1, D), n(1, D)
+    A = torch.empty(D, N, device="cuda").uniform_(-8, -0.1, generator=g)
+    state = torch.empty(1, D, N, device="cuda").normal_(generator=g)
+    tail = state[:, -cut:].clone()
+    y = ssd.ssd_selective_step(state, x, dt, A, bc, bc)
+    part = ssd.ssd_selective_step(tail, x[:, -cut:], dt[:, -cut:], A[-cut:], bc[:, -cut:], bc[:, -cut:])
+    assert torch.equal(y[:, -cut:], part) and torch.equal(state[:, -cut:], tail)
