@@ -47,6 +47,14 @@ __device__ __forceinline__ float decay(float dl, float A) { return ex2(fmaf(dl, 
 __device__ __forceinline__ F2 decay2(F2 dl, F2 A) {
     return ex2_2(fma2(dl, A, pack2(kDecayShift, kDecayShift)));
 }
+// What a span of tokens leaves of a state h that enters it, 2^e h (e = sum of dl A), and
+// what it adds, S.  The factor goes in as two roots: a growth beyond fp32 (A > 0)
+// takes a small state only as far as the tokens one by one would, and a decay
+// below it a large one.  Zero stays zero, which an infinite factor would make NaN.
+__device__ __forceinline__ float over_span(float e, float h, float S) {
+    const float root = ex2(0.5f * e);
+    return h == 0.f ? S : fmaf(root, root * h, S);
+}
 
 // Adds v[i] over LANES lanes that lie STRIDE apart, `lane` being this one's place
 // among them, for all NV values at once: each step gives half of the values away and keeps the sums of the

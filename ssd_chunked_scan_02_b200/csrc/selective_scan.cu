@@ -134,7 +134,7 @@ scan_fwd_kernel(const SelectiveArgs a, T* __restrict__ y, float* __restrict__ fi
                     const float sum = sp.sum[at];
                     const float* S = sp.state + at * NP + lane * SPL;
 #pragma unroll
-                    for (int i = 0; i < SPL; ++i) hv[i] = fmaf(ex2(sum * av[i]), hv[i], S[i]);
+                    for (int i = 0; i < SPL; ++i) hv[i] = over_span(sum * av[i], hv[i], S[i]);
                 }
             }
 #pragma unroll

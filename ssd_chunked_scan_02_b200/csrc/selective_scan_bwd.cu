@@ -145,7 +145,7 @@ scan_bwd_kernel(const SelectiveArgs a, const SelectiveGrads gr, const float* __r
                 const float sum = sp.sum[at];
                 const float* G = sp.state + at * NP + lane * SPL;
 #pragma unroll
-                for (int i = 0; i < SPL; ++i) gv[i] = fmaf(ex2(sum * av[i]), gv[i], G[i]);
+                for (int i = 0; i < SPL; ++i) gv[i] = over_span(sum * av[i], gv[i], G[i]);
             }
         }
 #pragma unroll

@@ -387,3 +387,49 @@ def test_step_with_groups_beyond_32_bits(lib):
     y = ssd.ssd_selective_step(state, x, dt, A, bc, bc)
     part = ssd.ssd_selective_step(tail, x[:, -cut:], dt[:, -cut:], A[-cut:], bc[:, -cut:], bc[:, -cut:])
     assert torch.equal(y[:, -cut:], part) and torch.equal(state[:, -cut:], tail)
+
+
+@pytest.mark.gpu
+def test_growing_states_over_spans(lib):
+    """A > 0 over a sequence that is cut into spans: a state (or a gradient) of zero
+    stays zero through any growth, and a small one grows as far as it does token
+    by token, also where the growth alone is beyond fp32."""
+    c = Case(1, 700, 40, 16, dt="f32", gate=False, skip=False, bias=False, softplus=False, init=False)
+    dims = ssd.ssd_selective_dims_t(c.b, c.L, c.ch, c.N, c.G)
+    assert ssd.ssd_selective_scan_fwd_workspace_size(dims, torch.float32) > 0
+    d, m = make(c, 41)
+    d["A"] = torch.full_like(d["A"], 4.0)
+
+    def forward(init=None):
+        y, f = ssd.ssd_selective_scan_fwd(**d, init_states=init, return_final_states=True)
+        ra = ref_args(d, m) | dict(init=R.f64(init))
+        ry, rf = R.scan(**ra)
+        bound = R.scan_bounds(**ra)
+        assert torch.isfinite(ry).all() and torch.isfinite(rf).all()
+        R.within("y", y, ry, bound["y"])
+        R.within("final", f, rf, bound["final"])
+    # exp(4 * 128) before the first input
+    d["dt"] = torch.full_like(d["dt"], 1e-3)
+    d["dt"][:, :128] = 1.0
+    d["x"][:, :128] = 0
+    forward()
+    # exp(97) = 2^140 over the first 64 tokens, of 1e-30
+    d["dt"][:, :128] = 1e-3
+    d["dt"][:, :64] = 97 / 256
+    forward(torch.full((1, c.ch, c.N), 1e-30, device="cuda"))
+    # in reverse: exp(4 * 100) behind the last token that has a gradient
+    d["dt"][:] = 1e-3
+    d["dt"][:, 600:] = 1.0
+    d["x"][:] = 0
+    dy = torch.randn(1, c.L, c.ch, generator=m["gen"]).cuda()
+    dy[:, 600:] = 0
+    g = ssd.ssd_selective_scan_bwd(**d, dy=dy)
+    ra = ref_args(d, m)
+    leaf = {k: v.requires_grad_() for k, v in ra.items() if torch.is_tensor(v)}
+    y, _ = R.scan(**ra)
+    ref = dict(zip(leaf, torch.autograd.grad((y * R.f64(dy)).sum(), list(leaf.values()))))
+    bound = R.scan_bounds(**{k: (v.detach() if torch.is_tensor(v) else v) for k, v in ra.items()},
+                          dy=R.f64(dy))
+    for k, of in NAMES.items():
+        if of in leaf:
+            R.within(k, g[k], ref[of], bound[k])
