@@ -425,22 +425,22 @@ constexpr int kStepBatch = 4;
 template <typename T, int LANES, bool Vec>
 __global__ void __launch_bounds__(256, 3)
 step_kernel(float* __restrict__ state, const SelectiveArgs a, T* __restrict__ y, int64_t b, int D,
-            int N, int per_group, unsigned across) {
+            int count, int N, int per_group, unsigned across) {
     constexpr int KB = kStepBatch, PER = 256 / LANES;
     constexpr int OWN = LANES >= KB ? 1 : KB / LANES;      // sequences a lane is in charge of
     constexpr int SPAN = LANES >= KB ? LANES / KB : 1;     // lanes in charge of one
     const int lane = threadIdx.x % LANES;
     const unsigned group = blockIdx.x / across;            // `across` blocks hold a sequence's channels
     const unsigned at = (blockIdx.x - group * across) * PER + threadIdx.x / LANES;
-    const bool on = at < (unsigned)D;
+    const bool on = at < (unsigned)count;
     const int c = on ? (int)at : 0, g = c / per_group;
     const int64_t b0 = (int64_t)group * KB;
     const int nb = b - b0 < KB ? (int)(b - b0) : KB;
     const float* Ar = a.A + (int64_t)c * N;
     float* st = state + (b0 * D + c) * N;
     const int64_t next = (int64_t)D * N;                   // the same channel of the next sequence
-    const T* Bp = static_cast<const T*>(a.B) + b0 * a.Bs.batch + (int64_t)g * N;
-    const T* Cp = static_cast<const T*>(a.C) + b0 * a.Cs.batch + (int64_t)g * N;
+    const T* Bp = static_cast<const T*>(a.B) + b0 * a.Bs.batch + g * N;
+    const T* Cp = static_cast<const T*>(a.C) + b0 * a.Cs.batch + g * N;
 
     // one round for up to 4 LANES states, two for 129 to 256
     float hs[KB][4], As[4], acc[KB];
@@ -530,13 +530,30 @@ step_kernel(float* __restrict__ state, const SelectiveArgs a, T* __restrict__ y,
     }
 }
 
+// A launch takes groups whose states' elements together stay below 2^31, which is
+// all of them but for millions of groups: a thread's offset into B and C then fits 32
+// bits (64-bit ones spill without Vec: 256 x 5120 x 33 took 162 us instead of 140).
 template <typename T, bool Vec>
 void step_lanes(float* state, const SelectiveArgs& a, void* y, const SelectiveDims& d, cudaStream_t s) {
     auto go = [&](auto kernel, int lanes) {
-        const int64_t across = (d.D + 256 / lanes - 1) / (256 / lanes);
-        const int64_t blocks = across * ((d.b + kStepBatch - 1) / kStepBatch);
-        kernel<<<(unsigned)blocks, 256, 0, s>>>(state, a, static_cast<T*>(y), d.b, (int)d.D, (int)d.N,
-                                                (int)(d.D / d.G), (unsigned)across);
+        const int64_t per = d.D / d.G, most = 0x7fffffff / d.N;
+        for (int64_t g0 = 0; g0 < d.G; g0 += most) {
+            const int64_t c0 = g0 * per, count = (d.G - g0 < most ? d.G - g0 : most) * per;
+            const int64_t across = (count + 256 / lanes - 1) / (256 / lanes);
+            const int64_t blocks = across * ((d.b + kStepBatch - 1) / kStepBatch);
+            SelectiveArgs q = a;                           // from group g0 on
+            q.x = static_cast<const T*>(a.x) + c0;
+            q.dt = static_cast<const T*>(a.dt) + c0;
+            if (a.z) q.z = static_cast<const T*>(a.z) + c0;
+            q.B = static_cast<const T*>(a.B) + g0 * d.N;
+            q.C = static_cast<const T*>(a.C) + g0 * d.N;
+            q.A = a.A + c0 * d.N;
+            if (a.D) q.D = a.D + c0;
+            if (a.dt_bias) q.dt_bias = a.dt_bias + c0;
+            kernel<<<(unsigned)blocks, 256, 0, s>>>(state + c0 * d.N, q, static_cast<T*>(y) + c0, d.b,
+                                                    (int)d.D, (int)count, (int)d.N, (int)per,
+                                                    (unsigned)across);
+        }
     };
     if (d.N <= 4) go(step_kernel<T, 1, Vec>, 1);
     else if (d.N <= 8) go(step_kernel<T, 2, Vec>, 2);
