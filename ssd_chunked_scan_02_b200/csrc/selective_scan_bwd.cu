@@ -308,8 +308,7 @@ scan_bwd_kernel(const SelectiveArgs a, const SelectiveGrads gr, const float* __r
 #pragma unroll 2
             for (int tt = TT - TS; tt >= 0; tt -= TS) {
                 // a_t and h_t of TS tokens; h[0] is the state before them.  (Behind the
-                // last token dt = 0 keeps whatever state is loaded, and u, dyg, B and C
-                // are zero: nothing of it is used.)
+                // last token dt = 0 keeps the state, and u, dyg, B and C are zero.)
                 F2 e[TS][SPL / 2], h[TS + 1][SPL / 2];
 #pragma unroll
                 for (int i = 0; i < SPL / 2; ++i) h[0][i] = pack2(hn[i / 2].v[i % 2 * 2], hn[i / 2].v[i % 2 * 2 + 1]);
@@ -494,7 +493,9 @@ scan_bwd_kernel(const SelectiveArgs a, const SelectiveGrads gr, const float* __r
             for (int j = 0; j < 2; ++j) {
                 const int n = lane * SPL + 2 * i + j;
                 if (n >= d.N) continue;
-                part_a[(part * d.D + pl.c0 + ch) * d.N + n] = (j ? da.y : da.x) * kLn2;
+                // (nothing from an empty sequence: steps of zero times an infinite or
+                // NaN entering state would be NaN)
+                part_a[(part * d.D + pl.c0 + ch) * d.N + n] = own > 0 ? (j ? da.y : da.x) * kLn2 : 0.f;
                 if (gr.dinit && span == 0) gr.dinit[row * d.N + n] = j ? gv.y : gv.x;
             }
         }
@@ -510,12 +511,14 @@ scan_bwd_kernel(const SelectiveArgs a, const SelectiveGrads gr, const float* __r
 }
 
 // dB, dC (b,L,G,N): the sum of a group's channel blocks' partial rows
-// (blocks, b, L, 2, NP).  64 columns of four states x 4 shares of the blocks a
+// (blocks, b, L, 2, NP); zero behind a sequence, where an infinite or NaN state, times a
+// dyg of zero, is NaN.  64 columns of four states x 4 shares of the blocks a
 // thread block, eight rows of a share in flight.
 template <typename T>
 __global__ void __launch_bounds__(256)
-reduce_bc_kernel(const float* __restrict__ part, T* __restrict__ dB, T* __restrict__ dC,
-                 const SelectiveDims d, int per_group, int NP) {
+reduce_bc_kernel(const float* __restrict__ part, const int32_t* __restrict__ lens,
+                 T* __restrict__ dB, T* __restrict__ dC, const SelectiveDims d, int per_group,
+                 int NP) {
     const int64_t tokens = d.b * d.L, row = 2 * NP, total = tokens * d.G * row / 4;
     __shared__ float4 red[4][64];
     for (int64_t i0 = (int64_t)blockIdx.x * 64; i0 < total; i0 += (int64_t)gridDim.x * 64) {
@@ -541,6 +544,7 @@ reduce_bc_kernel(const float* __restrict__ part, T* __restrict__ dB, T* __restri
             v.x += o.x; v.y += o.y; v.z += o.z; v.w += o.w;
         }
         const int64_t tok = at / row, n = at % NP;
+        if (lens && tok % d.L >= own_length(lens, tok / d.L, d.L)) v = make_float4(0.f, 0.f, 0.f, 0.f);
         T* out = (at % row >= NP ? dC : dB) + (tok * d.G + g) * d.N + n;
         if (n < d.N) out[0] = from_f32<T>(v.x);
         if (n + 1 < d.N) out[1] = from_f32<T>(v.y);
@@ -616,8 +620,8 @@ cudaError_t launch_selective_bwd(const SelectiveArgs& a, const SelectiveGrads& g
             if (err == cudaSuccess && d.L > 0) {
                 const int64_t nblk = (d.b * d.L * d.G * 2 * Lay::NP / 4 + 63) / 64;
                 reduce_bc_kernel<T><<<(unsigned)(nblk < 148 * 8 ? nblk : 148 * 8), dim3(64, 4), 0, s>>>(
-                    ws + w.bc, static_cast<T*>(g.dB), static_cast<T*>(g.dC), d, (int)(nb / d.G),
-                    Lay::NP);
+                    ws + w.bc, a.lens, static_cast<T*>(g.dB), static_cast<T*>(g.dC), d,
+                    (int)(nb / d.G), Lay::NP);
             }
         });
     });

@@ -433,3 +433,38 @@ def test_growing_states_over_spans(lib):
     for k, of in NAMES.items():
         if of in leaf:
             R.within(k, g[k], ref[of], bound[k])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("c", [Case(3, 50, 40, 16, lens=[50, 0, 5]), Case(3, 37, 24, 33, dt="f32", lens=[37, 0, 6]),
+                               Case(3, 700, 40, 16, dt="f32", lens=[650, 0, 70])], ids=repr)
+def test_empty_sequences_with_any_entering_state(lib, c):
+    """What enters an empty sequence (a place of the batch that nobody uses: any
+    bits, NaN among them) leaves it again, and reaches no other result; a state
+    that overflowed is not seen in the rows behind its sequence."""
+    d, m = make(c, 51)
+    dy = torch.randn(c.b, c.L, c.ch, generator=m["gen"]).to(DT[c.dt]).cuda()
+    df = torch.randn(c.b, c.ch, c.N, generator=m["gen"]).cuda()
+
+    def call(init, df):
+        y, f = ssd.ssd_selective_scan_fwd(**d, init_states=init, seq_lens=m["lens_t"], return_final_states=True)
+        return dict(y=y, f=f, **ssd.ssd_selective_scan_bwd(**d, dy=dy, init_states=init, dfinal_states=df,
+                                                           seq_lens=m["lens_t"]))
+    init, dead, want = m["init"].clone(), df.clone(), None
+    init[1], dead[1] = 0, 0
+    want = call(init, dead)
+    init[1], dead[1] = float("nan"), float("nan")
+    init[1, ::2], dead[1, 1::2] = float("inf"), -float("inf")
+    got = call(init, dead)
+    assert torch.equal(got["f"][1].nan_to_num(7.0), init[1].nan_to_num(7.0))
+    assert torch.equal(got["dinit"][1].nan_to_num(7.0), dead[1].nan_to_num(7.0))
+    for k in want:
+        some = [0, 2] if k in ("f", "dinit") else slice(None)
+        assert torch.isfinite(want[k][some]).all(), k
+        assert torch.equal(got[k][some], want[k][some]), k
+    init[1], dead[1] = 0, 0
+    init[2] = float("inf")
+    got = call(init, dead)
+    for k in ("y", "dx", "ddt", "dz", "dB", "dC"):
+        assert not got[k][2, c.lens[2]:].any(), k
+        assert torch.equal(got[k][:2], want[k][:2]), k
