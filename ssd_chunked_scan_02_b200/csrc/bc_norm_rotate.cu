@@ -57,11 +57,14 @@ struct Args {
 };
 
 // The fraction of a turn that position `pos` makes at `step` = freq / (2 pi),
-// as a signed 64-bit fixed-point number.
+// as a signed 64-bit fixed-point number; kNoStep where freq is infinite or NaN.
+constexpr int64_t kNoStep = -0x7fffffffffffffffLL - 1;
 __device__ __forceinline__ int64_t turn_step(float freq) {
     const double turns = (double)freq * 0.15915494309189533577;
     const double frac = turns - rint(turns);                 // whole turns of one step drop out
-    return __double2ll_rn(frac * 18446744073709551616.0);    // half a turn saturates: 2^-64 off
+    // (half a turn either way is the largest number, 2^-64 off)
+    const int64_t step = __double2ll_rn(fabs(frac) * 18446744073709551616.0);
+    return isfinite(freq) ? (frac < 0 ? -step : step) : kNoStep;
 }
 
 // Cosine and sine of pos * freq: the turn modulo 2^64, its upper 32 bits to the
@@ -287,7 +290,8 @@ norm_rotate_kernel(const Args a) {
             __syncthreads();                        // the last tile's readers are done
             for (int t = pair_from; t < nt; t += pair_step)
                 if (pair < half) {
-                    const float2 q = cos_sin(a.pos[bb * a.L + t0 + t], turn);
+                    float2 q = cos_sin(a.pos[bb * a.L + t0 + t], turn);
+                    if (turn == kNoStep) q.x = q.y = __int_as_float(0x7fffffff);   // NaN
                     table[2 * t * half + pair] = q.x;
                     table[(2 * t + 1) * half + pair] = q.y;
                 }

@@ -303,3 +303,30 @@ def test_calls_from_two_threads(lib):
     assert status == [{ssd.SSD_OK}, {ssd.SSD_OK}]
     for _, _, alone, out, _ in made:
         assert all(torch.equal(alone[k], out[k]) for k in alone)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("case", [(2, 9, 2, 64, 32, "f32", False, True, 0, "near"),
+                                  (1, 5, 3, 33, 20, "bf16", True, True, 0, "far")],
+                         ids=lambda c: "x".join(map(str, c[:5])) + c[5])
+def test_frequencies_that_are_no_numbers(lib, case):
+    """An infinite or NaN frequency gives NaN where its pair goes (also at position
+    0: 0 * inf) and in that pair's weights' gradients; the other pairs are what
+    they are without it."""
+    b, L, G, N, Rr, inter = *case[:5], case[6]
+    d = make(case, 80)
+    up = torch.randn(b, L, G, N, generator=d["gen"]).cuda()
+    a = args(d)
+    bad = [1, 4, Rr // 2 - 1]
+    a[5] = d["freq"].clone()
+    a[5][bad] = torch.tensor([float("nan"), float("inf"), -float("inf")]).cuda()
+    spoilt = torch.zeros(N, dtype=torch.bool, device="cuda")
+    for p in bad:
+        spoilt[[2 * p, 2 * p + 1] if inter else [p, p + Rr // 2]] = True
+    want = ssd.ssd_bc_norm_rotate_fwd(*args(d), interleaved=inter)
+    got = ssd.ssd_bc_norm_rotate_fwd(*a, interleaved=inter)
+    gw = ssd.ssd_bc_norm_rotate_bwd(*args(d), up, up, interleaved=inter)
+    gg = ssd.ssd_bc_norm_rotate_bwd(*a, up, up, interleaved=inter)
+    for o, w in [*zip(got, want), (gg["dwB"], gw["dwB"]), (gg["dwC"], gw["dwC"])]:
+        assert torch.isnan(o[..., spoilt]).all()
+        assert torch.equal(o[..., ~spoilt], w[..., ~spoilt])
