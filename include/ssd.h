@@ -588,8 +588,11 @@ typedef struct {
  * and ssd_step's (at seqlen 1) B and C as they stand.
  * B, C (b,L,G,N) dtype (strided, by B_stride and C_stride); B_out, C_out (b,L,G,N) dtype,
  * dense.  B_weight, C_weight fp32, (N) for all groups or (if weight_per_group
- * is non-zero) (G,N).  positions (b,L) int64 (any value: the angle is reduced
- * in exact integer arithmetic); freq (R/2) fp32, radians a position.
+ * is non-zero) (G,N).  positions (b,L) int64; freq (R/2) fp32, radians a
+ * position.  The angle is a fixed-point turn times the position, modulo a turn:
+ * beside fp32's roundings it is off by |position| 2^-64 of a turn at most (7e-10
+ * radians at 2^31, 4e-7 at 2^40), for frequencies up to 2^40.  An infinite or
+ * NaN frequency gives NaN in its pair.  eps >= 0; with 0, a row of zeros is NaN.
  */
 SSD_API ssd_status_t ssd_bc_norm_rotate_fwd(const void* B, const ssd_stride_t* B_stride,
                                             const void* C, const ssd_stride_t* C_stride,

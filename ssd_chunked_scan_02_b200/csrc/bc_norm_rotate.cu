@@ -23,9 +23,10 @@
 //
 // Far positions: pos * freq is wanted modulo 2 pi, where the product's integer
 // part is useless.  freq / (2 pi) is taken as a 64-bit fixed-point fraction of
-// a turn, and pos times it modulo 2^64 is one exact integer product: its error
-// is pos * 2^-65 turns, and the error of freq / (2 pi) in fp64 (2^-53 of it)
-// times pos.
+// a turn, and pos times it modulo 2^64 is one exact integer product: what the
+// fraction's last place leaves out, 2^-64 of a turn, times pos is its error (7e-10
+// radians at 2^31, less than the sines' own; 4e-7 at 2^40).  freq / (2 pi) has to be
+// known to as many places for that (a product in fp64 is off by 5e-7 radians at 2^33).
 #include <cuda_bf16.h>
 
 #include "common.cuh"
@@ -56,15 +57,18 @@ struct Args {
     int64_t tiles, ntile;             // of a sequence, and of all
 };
 
-// The fraction of a turn that position `pos` makes at `step` = freq / (2 pi),
-// as a signed 64-bit fixed-point number; kNoStep where freq is infinite or NaN.
+// The fraction of a turn that a position makes, freq / (2 pi), as a signed 64-bit
+// fixed-point number less than 2^-64 off; kNoStep where freq is infinite or NaN.
+// 1 / (2 pi) is the sum of two fp64 numbers, and the product keeps its rounding error.
 constexpr int64_t kNoStep = -0x7fffffffffffffffLL - 1;
 __device__ __forceinline__ int64_t turn_step(float freq) {
-    const double turns = (double)freq * 0.15915494309189533577;
-    const double frac = turns - rint(turns);                 // whole turns of one step drop out
-    // (half a turn either way is the largest number, 2^-64 off)
-    const int64_t step = __double2ll_rn(fabs(frac) * 18446744073709551616.0);
-    return isfinite(freq) ? (frac < 0 ? -step : step) : kNoStep;
+    const double f = freq, hi = 0.15915494309189533577, lo = -9.8393383375912434770e-18;
+    const double turns = f * hi, rest = fma(f, hi, -turns) + f * lo;
+    // (whole turns of one step drop out, and the sum is modulo a turn)
+    const uint64_t step = (uint64_t)__double2ll_rn((turns - rint(turns)) * 18446744073709551616.0) +
+                          (uint64_t)__double2ll_rn((rest - rint(rest)) * 18446744073709551616.0);
+    if (!isfinite(freq)) return kNoStep;
+    return (int64_t)step == kNoStep ? kNoStep + 1 : (int64_t)step;
 }
 
 // Cosine and sine of pos * freq: the turn modulo 2^64, its upper 32 bits to the
@@ -290,11 +294,13 @@ norm_rotate_kernel(const Args a) {
             __syncthreads();                        // the last tile's readers are done
             for (int t = pair_from; t < nt; t += pair_step)
                 if (pair < half) {
-                    float2 q = cos_sin(a.pos[bb * a.L + t0 + t], turn);
-                    if (turn == kNoStep) q.x = q.y = __int_as_float(0x7fffffff);   // NaN
+                    const float2 q = cos_sin(a.pos[bb * a.L + t0 + t], turn);
                     table[2 * t * half + pair] = q.x;
                     table[(2 * t + 1) * half + pair] = q.y;
                 }
+            if (turn == kNoStep)
+                for (int t = pair_from; t < nt; t += pair_step)
+                    table[2 * t * half + pair] = table[(2 * t + 1) * half + pair] = __int_as_float(0x7fffffff);
             __syncthreads();
             for (int i = 0; i * slots < nt; ++i) {               // uniform in a block
                 const int t = slot + i * slots;

@@ -9,6 +9,7 @@ and two roundings; a turned element is a sum of two products: 24 roundings of
 |u_i| + |u_j| cover all."""
 import ctypes
 import threading
+from fractions import Fraction
 
 import pytest
 import torch
@@ -330,3 +331,31 @@ def test_frequencies_that_are_no_numbers(lib, case):
     for o, w in [*zip(got, want), (gg["dwB"], gw["dwB"]), (gg["dwC"], gw["dwC"])]:
         assert torch.isnan(o[..., spoilt]).all()
         assert torch.equal(o[..., ~spoilt], w[..., ~spoilt])
+
+
+PI = Fraction("3.14159265358979323846264338327950288419716939937510582097494459")
+
+
+@pytest.mark.gpu
+def test_far_positions(lib):
+    """Positions up to 2^40, against angles in exact arithmetic.  Beside
+    test_forward's bound, a step is 2^-64 of a turn off at most."""
+    b, L, G, N, Rr = 6, 2, 1, 64, 64
+    d = make((b, L, G, N, Rr, "f32", False, False, 0, "near"), 60)
+    base = torch.tensor([(1 << 31) - 1, (1 << 32) + 5, (1 << 36) + 12345, (1 << 40) - 77, -(1 << 38) - 3,
+                         (1 << 33) + 1])
+    pos = base[:, None] + torch.arange(L)
+    freq = torch.cat((torch.tensor([1.0, 0.99999994, 3.0, 100.25]),
+                      10000.0 ** (-torch.arange(4, 32, dtype=torch.float32) / 32)))
+    turns = [[[Fraction(int(p)) * Fraction(float(f)) / (2 * PI) for f in freq] for p in row] for row in pos]
+    ang = torch.tensor([[[float((t - round(t)) * 2 * PI) for t in r] for r in row] for row in turns],
+                       dtype=torch.float64)
+    out = ssd.ssd_bc_norm_rotate_fwd(d["B"], d["C"], d["wB"], d["wC"], pos.cuda(), freq.cuda(), eps=EPS)
+    c, s = ang.cos()[:, :, None], ang.sin()[:, :, None]
+    for k, got in zip("BC", out):
+        v = R.f64(d[k])
+        u = v / torch.sqrt(v.square().mean(-1, keepdim=True) + EPS) * R.f64(d["w" + k])
+        p, q = u[..., :32], u[..., 32:]
+        ref = torch.cat((p * c - q * s, p * s + q * c), -1)
+        step = 2 * float(PI) * 2.0 ** -64 * pos.abs().double()[:, :, None, None]
+        R.within(k, got, ref, (24 * R.U + step) * turned_size(u, Rr, False))
