@@ -277,3 +277,35 @@ def test_streams_graphs_and_repeats(lib):
     torch.cuda.synchronize()
     assert torch.equal(y3, y4) and not torch.equal(y, y4)
     assert all(torch.equal(g3[k], g4[k]) for k in g if g[k] is not None)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("case", [(4, 300, 136, 4, "bf16", 64, True, [300, 1, 0, 77], True),
+                                  (2, 65, 33, 3, "f32", 1, True, None, True),
+                                  (2, 40, 12, 2, "bf16", 0, False, None, False)],
+                         ids=lambda c: "x".join(map(str, c[:4])) + c[4])
+def test_without_bias(lib, case):
+    """bias = None is a bias of zero, bit for bit, and dbias is written all the same;
+    both against the definition (bounds: test_forward's and test_gradients')."""
+    b, L, D, W, dt, view, init, lens, silu = case
+    d = make(b, L, D, W, DT[dt], 300 + L, view, init)
+    d["bias"] = None
+    zero = torch.zeros(D, device="cuda")
+    ln = torch.tensor(lens, dtype=torch.int32, device="cuda") if lens else None
+    more = dict(init_state=d["init"], seq_lens=ln, silu=silu)
+    y, f = ssd.ssd_causal_conv_fwd(d["x"], d["w"], **more, return_final_state=True)
+    R.within("y", y, R.conv(R.f64(d["x"]), R.f64(d["w"]), None, R.f64(d["init"]), lens, silu)[0],
+             32 * R.U * sizes_of(d))
+    assert torch.equal(y, ssd.ssd_causal_conv_fwd(d["x"], d["w"], zero, **more))
+    dy = torch.randn(b, L, D, generator=d["gen"]).to(DT[dt]).cuda()
+    g = ssd.ssd_causal_conv_bwd(d["x"], d["w"], None, dy, **more)
+    for k, v in ssd.ssd_causal_conv_bwd(d["x"], d["w"], zero, dy, **more).items():
+        assert torch.equal(g[k], v), k
+    ref = grads(d | dict(bias=zero), lens, silu, dy, None)
+    big = R.f64(dy).abs() * (1 + sizes_of(d))
+    steps = 64 + 64 + 4 + -(-L // 256) * b / 8 + 8
+    R.within("dbias", g["dbias"], ref["bias"], steps * R.U * big.sum((0, 1)))
+    token = torch.randn(b, D, generator=d["gen"]).to(DT[dt]).cuda()
+    states = [f.clone(), f.clone()]
+    ys = [ssd.ssd_causal_conv_step(s, token, d["w"], v, silu=silu) for s, v in zip(states, (None, zero))]
+    assert torch.equal(*ys) and torch.equal(*states)
