@@ -219,18 +219,25 @@ chunk_out_simt_kernel(const T* __restrict__ x, const float* __restrict__ dt,
     }
 }
 
-size_t state_smem(const Dims& d) { return sizeof(float) * (2 * d.Q + kJT * (d.P + d.N)); }
-size_t out_smem(const Dims& d) {
-    return sizeof(float) *
-           (2 * d.Q + kIT * d.N + kJT * (d.N + 1) + kJT * d.P + kIT * kJT + d.P * 33);
+// Shared memory at a chunk of Q, headdim P and N states.  The limit that a kernel is
+// given is the largest that any call needs, the same every time: other host
+// threads launch it too, at other sizes.
+constexpr int kMost = 256;        // of Q, P and N
+constexpr size_t state_smem(int64_t Q, int64_t P, int64_t N) {
+    return sizeof(float) * (2 * Q + kJT * (P + N));
 }
+constexpr size_t out_smem(int64_t Q, int64_t P, int64_t N) {
+    return sizeof(float) * (2 * Q + kIT * N + kJT * (N + 1) + kJT * P + kIT * kJT + P * 33);
+}
+static_assert(out_smem(kMost, kMost, kMost) <= 227 * 1024, "fits an SM");
 
 template <typename T>
 cudaError_t state_impl(const void* x, const float* dt, const float* A, const void* B,
                        float* states, float* logdecay, const Dims& d, cudaStream_t s) {
-    const size_t smem = state_smem(d);
+    const size_t smem = state_smem(d.Q, d.P, d.N);
     cudaError_t e = cudaFuncSetAttribute(chunk_state_simt_kernel<T>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)state_smem(kMost, kMost, kMost));
     if (e != cudaSuccess) return e;
     dim3 grid((unsigned)(d.b * d.T), (unsigned)d.H);
     chunk_state_simt_kernel<T><<<grid, kThreads, smem, s>>>(
@@ -241,9 +248,10 @@ cudaError_t state_impl(const void* x, const float* dt, const float* A, const voi
 template <typename T>
 cudaError_t out_impl(const void* x, const float* dt, const float* A, const void* B, const void* C,
                      const float* D, const void* prev, void* y, const Dims& d, cudaStream_t s) {
-    const size_t smem = out_smem(d);
+    const size_t smem = out_smem(d.Q, d.P, d.N);
     cudaError_t e = cudaFuncSetAttribute(chunk_out_simt_kernel<T>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)out_smem(kMost, kMost, kMost));
     if (e != cudaSuccess) return e;
     dim3 grid((unsigned)(d.b * d.T), (unsigned)d.H);
     chunk_out_simt_kernel<T><<<grid, kThreads, smem, s>>>(

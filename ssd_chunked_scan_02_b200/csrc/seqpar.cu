@@ -281,17 +281,20 @@ cudaError_t launch_correction_simt(const float* h_in, const float* dt, const flo
     if (d.b * nt == 0) return cudaSuccess;
     const int PB = (int)(d.P < 64 ? d.P : 64);
     const size_t smem = (size_t)(kTile + PB * (d.N + 1) + 32 * (d.N + 1)) * 4;
+    // the kernel's limit: what N = 256 needs, the same for every call (other host
+    // threads launch it too, at other sizes)
+    constexpr int most = (kTile + (64 + 32) * 257) * 4;
     dim3 grid((unsigned)(d.b * nt), (unsigned)d.H, (unsigned)((d.P + PB - 1) / PB));
     if (t == Elt::F32) {
         cudaError_t e = cudaFuncSetAttribute(correction_simt_kernel<float>,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize, most);
         if (e != cudaSuccess) return e;
         correction_simt_kernel<float><<<grid, 256, smem, s>>>(
             h_in, dt, A, static_cast<const float*>(C), tile_prefix, static_cast<float*>(y), d.L,
             (int)d.H, (int)d.G, (int)d.P, (int)d.N, PB, nt);
     } else {
         cudaError_t e = cudaFuncSetAttribute(correction_simt_kernel<__nv_bfloat16>,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize, most);
         if (e != cudaSuccess) return e;
         correction_simt_kernel<__nv_bfloat16><<<grid, 256, smem, s>>>(
             h_in, dt, A, static_cast<const __nv_bfloat16*>(C), tile_prefix,
