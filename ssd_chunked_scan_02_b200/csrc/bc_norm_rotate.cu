@@ -19,7 +19,7 @@
 // 4 x 8192 tokens of 8 groups, N = 128, 64 elements turned, bf16: 53 us, 269 MB at
 // 5.0 TB/s (77% of a plain copy's rate), the issue slots 67% busy: conversions,
 // norm and turn are about 130 instructions a lane and eight elements.  Gradients
-// (8 x 2048 tokens, fp32 in, all turned): 60 us, and 6 us for the weights' sums.
+// (8 x 2048 tokens, fp32 in, all turned): 61 us, and 6 us for the weights' sums.
 //
 // Far positions: pos * freq is wanted modulo 2 pi, where the product's integer
 // part is useless.  freq / (2 pi) is taken as a 64-bit fixed-point fraction of
@@ -434,8 +434,9 @@ int lanes_of(int N) {
     return lanes;
 }
 
-// Four blocks for each of 148 SMs, each with the same number of tiles of at most
-// kMaxTile tokens.
+// 592 blocks, four for each of 148 SMs, each with the same number of tiles of at most
+// kMaxTile tokens.  (Of the gradients' kernels, with up to 110 registers and 63 KB or
+// more for bf16 rows and fp32 gradients, two or three fit an SM at a time.)
 constexpr int kMaxTile = 32;
 int tile_of(const RotateDims& d) {
     const int64_t per = (d.b * d.L + 591) / 592;         // tokens of a block

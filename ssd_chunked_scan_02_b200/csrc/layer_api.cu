@@ -43,7 +43,8 @@ ssd_status_t conv_dims(const ssd_conv_dims_t* dims, ssd_dtype_t dtype, ssd::Conv
                     (long long)dims->width);
     if (dims->channels > kMaxSize / 8)
         return fail(SSD_ERR_UNSUPPORTED, "channels must be below 2^28");
-    // the finest split: one thread a channel and 8 tokens, 256 threads a block
+    // the finest split: a channel and 8 tokens a thread, 32 channels across a block
+    // (the gradients' blocks; the forward's are 128 threads)
     if ((double)dims->batch * ((double)dims->seqlen / 8 + 1) * ((double)dims->channels / 32 + 1) >
         (double)kMaxSize)
         return fail(SSD_ERR_UNSUPPORTED, "batch * seqlen * channels exceeds the launch grid");

@@ -14,8 +14,9 @@ namespace ssd {
 // w P(w), P the degree-9 polynomial that interpolates log(1 + w) / w at the
 // Chebyshev points of [0, 1]; the nearest singularity, w = -1, makes its error
 // fall by 3 + sqrt(8) a degree, to 6e-9 relative, so that small steps (large
-// negative v, where 1 + w would lose w) keep full accuracy.  One element at a
-// time: the coefficients are then immediates and hold no registers.
+// negative v, where 1 + w would lose w) keep their accuracy but for the rounding
+// of w's exponent, |v| 2^-24 relative.  One element at a time: the coefficients
+// are then immediates and hold no registers.
 __device__ __forceinline__ float softplus_f32(float v) {
     constexpr float kP[10] = {
         0.999999995f, -0.499998926f,

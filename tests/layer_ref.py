@@ -98,7 +98,8 @@ def scan_bounds(x, dt, A, B, C, D=None, z=None, dt_bias=None, softplus=True, ini
     """How far fp32 arithmetic may take each result, running error bounds beside
     the recurrences (all values fp64, absolute values throughout, in units of
     one rounding 2^-24):
-      dt: the bias sum, __expf and log1p: 8 of |dt|, and of 1 near zero inputs' sum
+      dt: 8 of |dt| for the softplus (an exponential and a polynomial), and what
+        rounding the bias sum (and with it the exponent) moves it by
       a = exp(dt A): its argument is off by (8 + 2) |dt A|, ex2 by 3
       h: E_t = a E_{t-1} + (13 + 10 |dt A|) a H_{t-1} + 16 |u B|, H the recurrence of |h|
       g: the same in reverse from dyg C, dyg off by 8 + |z| (the sigmoid's argument)

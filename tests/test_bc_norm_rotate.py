@@ -4,7 +4,7 @@ gradients against the fp64 definition.
 Bounds.  The mean of N <= 256 squares is off by at most (8 + 5 + 2) roundings
 relative to itself (eight terms a lane, five joins), its reciprocal root by half
 of that and two more; u = v r w by three more: 16 roundings of |u|.  The cosine
-and sine are off by 2^-25 pi (the angle held as a fp32 number of half turns)
+and sine are off by 2^-24 pi / 4 (the rest of a turn, at most an eighth, in fp32)
 and two roundings; a turned element is a sum of two products: 24 roundings of
 |u_i| + |u_j| cover all."""
 import ctypes
