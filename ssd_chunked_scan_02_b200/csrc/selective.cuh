@@ -51,10 +51,11 @@ __device__ __forceinline__ F2 decay2(F2 dl, F2 A) {
 // What a span of tokens leaves of a state h that enters it, 2^e h (e = sum of dl A), and
 // what it adds, S.  The factor goes in as two roots: a growth beyond fp32 (A > 0)
 // takes a small state only as far as the tokens one by one would, and a decay
-// below it a large one.  Zero stays zero, which an infinite factor would make NaN.
+// below it a large one.  The roots stay finite (2^254 takes any normal number beyond
+// fp32), so that zero stays zero.
 __device__ __forceinline__ float over_span(float e, float h, float S) {
-    const float root = ex2(0.5f * e);
-    return h == 0.f ? S : fmaf(root, root * h, S);
+    const float root = ex2(fminf(0.5f * e, 127.f));
+    return fmaf(root, root * h, S);
 }
 
 // Adds v[i] over LANES lanes that lie STRIDE apart, `lane` being this one's place
